@@ -30,6 +30,12 @@ EXPORTS = (
     "w4_status_string", "w4_last_error", "w4_version",
 )
 
+# every entry point declared in include/w8a8.h
+EXPORTS_W8 = (
+    "w8_pitch", "w8_quantize_rows", "w8a8_workspace_bytes", "w8a16_mm_t_workspace_bytes", "w8a8_mm", "w8a8_linear",
+    "w8a16_mm_t", "w8a8_kernel", "tok_workspace_bytes", "tok_logprobs", "tok_logprobs_grad",
+)
+
 
 class W4Desc(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int64), ("mode", ctypes.c_int32), ("group", ctypes.c_int32)]
@@ -99,6 +105,23 @@ def lib() -> ctypes.CDLL:
                  "w4a16_mm", "w4a16_mm_out", "w4a16_mm_noalloc", "w4a16_mm_plan", "w4_serial_layout",
                  "w4_serial_parse"):
         getattr(L, name).restype = ctypes.c_int
+    pseg, psz, dbl = ctypes.POINTER(W4OutSeg), ctypes.POINTER(ctypes.c_size_t), ctypes.c_double
+    L.w8_pitch.argtypes = [i64]
+    L.w8_pitch.restype = i64
+    L.w8_quantize_rows.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+    L.w8a8_workspace_bytes.argtypes = [i64, i64, i64, i32, psz]
+    L.w8a16_mm_t_workspace_bytes.argtypes = [i64, i64, i64, i64, psz]
+    L.w8a8_mm.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, i32, pseg, i32, vp, sz, vp]
+    L.w8a8_linear.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, vp, i32, pseg, i32, vp, sz, vp]
+    L.w8a16_mm_t.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, i32, pseg, i32, vp, sz, vp]
+    L.w8a8_kernel.argtypes = [i64, i64, i64, i32]
+    L.w8a8_kernel.restype = ctypes.c_char_p
+    L.tok_workspace_bytes.argtypes = [i64, i64, i32, psz]
+    L.tok_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, i64, dbl, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.tok_logprobs_grad.argtypes = [vp, i32, i64, i64, i64, vp, i64, dbl, i32, vp, vp, vp, vp, vp, vp, vp, i64, vp]
+    for name in EXPORTS_W8:
+        if name not in ("w8_pitch", "w8a8_kernel"):
+            getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
 

@@ -9,13 +9,15 @@
 #include <cstring>
 #include <string>
 
+#include "api_common.h"
 #include "launch.h"
 
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
 
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace w4 {
+
 int fail(int status, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -31,7 +33,72 @@ int ok() {
   return W4_OK;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+DeviceCaps device_caps() {
+  // queried once per process (one device type); without a device (host-only queries on a
+  // machine with no GPU) the figures are MI355X's: 160 KB of LDS per workgroup, 256 CUs
+  static std::atomic<long long> lds{-1}, cus{-1};
+  if (lds.load() < 0) {
+    int dev = 0, bytes = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&bytes, hipDeviceAttributeMaxSharedMemoryPerBlock, dev) != hipSuccess || bytes <= 0)
+      bytes = 160 * 1024;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
+    cus.store(n);
+    lds.store(bytes);
+  }
+  return DeviceCaps{(size_t)lds.load(), (int)cus.load()};
+}
+
+int launched(hipError_t e, const char* what) {
+  if (e != hipSuccess) return fail(W4_ERR_LAUNCH, "%s: %s", what, hipGetErrorString(e));
+  return ok();
+}
+
+// Output epilogue from the caller's bias, dtype and segments (validated).
+int make_epi(int64_t outc, int64_t M, const void* bias, int out_dtype, const w4_out_seg* segs, int nsegs, Epi* ep) {
+  if (out_dtype != W4_DT_F32 && out_dtype != W4_DT_F16 && out_dtype != W4_DT_BF16)
+    return fail(W4_ERR_INVALID, "out_dtype = %d must be F32, F16 or BF16", out_dtype);
+  if (segs == nullptr || nsegs < 1 || nsegs > kMaxSegs)
+    return fail(W4_ERR_INVALID, "nsegs = %d must be in [1, %d] with a segment array", nsegs, kMaxSegs);
+  const size_t esz = out_dtype == W4_DT_F32 ? 4 : 2;
+  int64_t c = 0;
+  for (int i = 0; i < kMaxSegs; ++i) {
+    if (i < nsegs) {
+      const w4_out_seg& g = segs[i];
+      if (g.cols < 1 || g.ld < g.cols)
+        return fail(W4_ERR_INVALID, "segment %d: cols = %lld must be >= 1 and ld = %lld >= cols", i,
+                    (long long)g.cols, (long long)g.ld);
+      if (M > 0 && g.Y == nullptr) return fail(W4_ERR_INVALID, "segment %d: Y is NULL", i);
+      if (M > 0 && !aligned(g.Y, esz)) return fail(W4_ERR_ALIGN, "segment %d: Y must be %zu-byte aligned", i, esz);
+      ep->c0[i] = c;
+      ep->y[i] = g.Y;
+      ep->ld[i] = g.ld;
+      c += g.cols;
+    } else {
+      ep->c0[i] = INT64_MAX;
+      ep->y[i] = nullptr;
+      ep->ld[i] = 0;
+    }
+  }
+  if (c != outc)
+    return fail(W4_ERR_INVALID, "segment columns sum to %lld, the output has %lld", (long long)c, (long long)outc);
+  if (bias != nullptr && !aligned(bias, esz)) return fail(W4_ERR_ALIGN, "bias must be %zu-byte aligned", esz);
+  ep->bias = bias;
+  ep->dt = out_dtype;
+  ep->nseg = nsegs;
+  return W4_OK;
+}
+
+}  // namespace w4
+
+namespace {
+
+using w4::aligned;
+using w4::device_caps;
+using w4::fail;
+using w4::launched;
+using w4::make_epi;
+using w4::ok;
 
 bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 
@@ -64,27 +131,6 @@ int64_t pairs_of(const w4_desc* d) {
   return d->N * (d->K / d->group);
 }
 
-w4::DeviceCaps device_caps() {
-  // queried once per process (one device type); without a device (host-only queries on a
-  // machine with no GPU) the figures are MI355X's: 160 KB of LDS per workgroup, 256 CUs
-  static std::atomic<long long> lds{-1}, cus{-1};
-  if (lds.load() < 0) {
-    int dev = 0, bytes = 0, n = 0;
-    if (hipGetDevice(&dev) != hipSuccess ||
-        hipDeviceGetAttribute(&bytes, hipDeviceAttributeMaxSharedMemoryPerBlock, dev) != hipSuccess || bytes <= 0)
-      bytes = 160 * 1024;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
-    cus.store(n);
-    lds.store(bytes);
-  }
-  return w4::DeviceCaps{(size_t)lds.load(), (int)cus.load()};
-}
-
-int launched(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(W4_ERR_LAUNCH, "%s: %s", what, hipGetErrorString(e));
-  return ok();
-}
-
 int check_mm(const uint16_t* A, int64_t M, const int32_t* packed, const uint16_t* scales, const uint16_t* zeros,
              const w4_desc* desc, int transposed) {
   int s = check_desc(desc);
@@ -103,43 +149,6 @@ int check_mm(const uint16_t* A, int64_t M, const int32_t* packed, const uint16_t
   if (!A || !packed || !scales || !zeros) return fail(W4_ERR_INVALID, "a required pointer is NULL");
   if (!aligned(A, 16) || !aligned(packed, 16)) return fail(W4_ERR_ALIGN, "A and packed must be 16-byte aligned");
   if (!aligned(scales, 2) || !aligned(zeros, 2)) return fail(W4_ERR_ALIGN, "scales / zeros must be 2-byte aligned");
-  return W4_OK;
-}
-
-// Output epilogue from the caller's bias, dtype and segments (validated).
-int make_epi(const w4_desc* desc, int transposed, int64_t M, const void* bias, int out_dtype, const w4_out_seg* segs,
-             int nsegs, w4::Epi* ep) {
-  if (out_dtype != W4_DT_F32 && out_dtype != W4_DT_F16 && out_dtype != W4_DT_BF16)
-    return fail(W4_ERR_INVALID, "out_dtype = %d must be F32, F16 or BF16", out_dtype);
-  if (segs == nullptr || nsegs < 1 || nsegs > w4::kMaxSegs)
-    return fail(W4_ERR_INVALID, "nsegs = %d must be in [1, %d] with a segment array", nsegs, w4::kMaxSegs);
-  const int64_t outc = transposed ? desc->K : desc->N;
-  const size_t esz = out_dtype == W4_DT_F32 ? 4 : 2;
-  int64_t c = 0;
-  for (int i = 0; i < w4::kMaxSegs; ++i) {
-    if (i < nsegs) {
-      const w4_out_seg& g = segs[i];
-      if (g.cols < 1 || g.ld < g.cols)
-        return fail(W4_ERR_INVALID, "segment %d: cols = %lld must be >= 1 and ld = %lld >= cols", i,
-                    (long long)g.cols, (long long)g.ld);
-      if (M > 0 && g.Y == nullptr) return fail(W4_ERR_INVALID, "segment %d: Y is NULL", i);
-      if (M > 0 && !aligned(g.Y, esz)) return fail(W4_ERR_ALIGN, "segment %d: Y must be %zu-byte aligned", i, esz);
-      ep->c0[i] = c;
-      ep->y[i] = g.Y;
-      ep->ld[i] = g.ld;
-      c += g.cols;
-    } else {
-      ep->c0[i] = INT64_MAX;
-      ep->y[i] = nullptr;
-      ep->ld[i] = 0;
-    }
-  }
-  if (c != outc)
-    return fail(W4_ERR_INVALID, "segment columns sum to %lld, the output has %lld", (long long)c, (long long)outc);
-  if (bias != nullptr && !aligned(bias, esz)) return fail(W4_ERR_ALIGN, "bias must be %zu-byte aligned", esz);
-  ep->bias = bias;
-  ep->dt = out_dtype;
-  ep->nseg = nsegs;
   return W4_OK;
 }
 
@@ -292,7 +301,7 @@ int w4a16_mm(const uint16_t* A, int64_t M, const int32_t* packed, const uint16_t
   const int64_t outc = transposed ? desc->K : desc->N;
   const w4_out_seg seg = {Y, outc, outc};
   w4::Epi ep;
-  s = make_epi(desc, transposed, M, bias, W4_DT_F32, &seg, 1, &ep);
+  s = make_epi(transposed ? desc->K : desc->N, M, bias, W4_DT_F32, &seg, 1, &ep);
   if (s != W4_OK) return s;
   return run_mm(make_args(A, M, packed, scales, zeros, desc, transposed, ep), ws, ws_bytes, stream);
 }
@@ -306,7 +315,7 @@ int w4a16_mm_out(const void* A, int a_dtype, int64_t M, const int32_t* packed, c
   int s = check_mm(A16, M, packed, scales, zeros, desc, transposed);
   if (s != W4_OK) return s;
   w4::Epi ep;
-  s = make_epi(desc, transposed, M, bias, out_dtype, segs, nsegs, &ep);
+  s = make_epi(transposed ? desc->K : desc->N, M, bias, out_dtype, segs, nsegs, &ep);
   if (s != W4_OK) return s;
   if (M == 0) return ok();
   return run_mm(make_args(A16, M, packed, scales, zeros, desc, transposed, ep, a_dtype == W4_DT_F16), ws, ws_bytes,
@@ -323,7 +332,7 @@ int w4a16_mm_noalloc(const uint16_t* A, int64_t M, const int32_t* packed, const 
   const int64_t outc = transposed ? desc->K : desc->N;
   const w4_out_seg seg = {Y, outc, outc};
   w4::Epi ep;
-  s = make_epi(desc, transposed, M, bias, W4_DT_F32, &seg, 1, &ep);
+  s = make_epi(transposed ? desc->K : desc->N, M, bias, W4_DT_F32, &seg, 1, &ep);
   if (s != W4_OK) return s;
   const w4::MmArgs a = make_args(A, M, packed, scales, zeros, desc, transposed, ep);
   const w4::DeviceCaps caps = device_caps();

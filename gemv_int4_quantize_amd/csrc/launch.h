@@ -43,6 +43,13 @@ struct MmArgs {
   int group;  // GROUPWISE g, else K
   bool transposed;
   bool a_f16;  // activations (and the weight operand) fp16 instead of bf16
+  // Transposed product on int8 rows (w8a16_mm_t): `packed` holds int8 codes with wpitch bytes a
+  // row and scales8 one fp32 scale a row (mode ROWWISE).  dY rows are lda elements apart
+  // (0: N, contiguous); a_zeros: lda is N rounded up to 64 and the columns past N hold zeros.
+  const float* scales8 = nullptr;
+  int64_t wpitch = 0;
+  int64_t lda = 0;
+  bool a_zeros = false;
 };
 
 // Properties of the current device that kernel plans depend on.
@@ -107,5 +114,64 @@ hipError_t launch_skinny(const MmArgs& a, const SkinnyPlan& p, float* part, hipS
 // fixed order).
 hipError_t launch_splitk_reduce(const float* part, int splits, int64_t M, int64_t c_lo, int64_t pw, const Epi& ep,
                                 hipStream_t st);
+
+// ---- 8-bit integer linear operators (include/w8a8.h)
+
+// X [rows][cols] (dtype dt, row stride ld) -> codes [rows][pitch], scales [rows].
+hipError_t launch_quantize_rows(const void* X, int dt, int64_t rows, int64_t cols, int64_t ld, int8_t* codes,
+                                float* scales, hipStream_t st);
+
+// Product of int8 rows after validation.  X != nullptr: float activations (dtype x_dt, row
+// stride ldx) that the decode kernel quantizes itself; else A / a_scales.
+struct W8Args {
+  const int8_t* A;
+  const float* a_scales;
+  const void* X;
+  int x_dt;
+  int64_t ldx;
+  const int8_t* W;
+  const float* w_scales;
+  Epi ep;
+  int64_t M, N, K, pitch;
+};
+size_t w8_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps);
+const char* w8_mm_name(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps);
+hipError_t launch_w8_mm(const W8Args& a, const DeviceCaps& caps, void* ws, size_t ws_bytes, hipStream_t st);
+
+// dY [M][N] 16-bit, row stride ld -> out [M][npad], zeros past column N.
+hipError_t launch_pad_rows(const uint16_t* dY, int64_t M, int64_t N, int64_t ld, uint16_t* out, int64_t npad,
+                           hipStream_t st);
+
+// ---- token scores (include/w8a8.h)
+
+struct TokArgs {
+  const void* z;
+  int dt;
+  int64_t M, V, ld;
+  const int64_t* targets;
+  int64_t ignore;
+  float inv_t;  // fp32(1 / temperature)
+  int top;
+  float *lp, *ent, *stats, *top_lp;
+  int64_t* top_ids;
+};
+size_t tok_ws_bytes(int64_t M, int64_t V, int top, const DeviceCaps& caps);
+hipError_t launch_tok(const TokArgs& a, const DeviceCaps& caps, void* ws, hipStream_t st);
+
+struct TokGradArgs {
+  const void* z;
+  int dt;
+  int64_t M, V, ld;
+  const int64_t* targets;
+  int64_t ignore;
+  float inv_t;
+  int top;
+  const float *stats, *ent;
+  const int64_t* top_ids;
+  const float *g, *h, *a;
+  void* dz;
+  int64_t ldd;
+};
+hipError_t launch_tok_grad(const TokGradArgs& a, const DeviceCaps& caps, hipStream_t st);
 
 }  // namespace w4

@@ -1,0 +1,223 @@
+"""PyTorch-facing binding of the 8-bit integer linear operators.
+
+``quantize_int8`` turns rows (tokens, or the output channels of a weight) into int8 codes
+with one fp32 scale a row; ``mm_int8`` multiplies two such operands, quantizing float
+activations on the way; ``mm_int8_t`` is the product's input gradient on the same weight.
+Argument marshalling only: every step runs in the library's gfx950 kernels (see
+include/w8a8.h for the contract).
+"""
+
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib
+from ._lib import check, lib
+from .ops import _ODT, _WDT, _stream
+
+
+@dataclass
+class Int8Rows:
+    """Rows of int8 codes with one fp32 scale each: row r stands for codes[r, :cols] * scales[r].
+
+    codes is int8 [rows][pitch], pitch = cols rounded up to a multiple of 64, 16-byte aligned,
+    contiguous, with zeros in the columns past ``cols``; scales is a contiguous fp32 [rows].
+    A weight W [N][K] has one row (and scale) per output channel, activations X [M][K] one
+    per token."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    cols: int
+
+
+def _pitch(cols: int) -> int:
+    return (cols + 63) // 64 * 64
+
+
+class on_device:
+    """The device of a call's tensors as the current one, where it is not already."""
+
+    def __init__(self, *tensors):
+        dev = None
+        for t in tensors:
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError("tensors must be on a HIP device")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"tensors on {dev} and {t.device}: one device is wanted")
+        self.device = dev
+        self.back = None
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if self.device.index != now:
+            self.back = now
+            torch.cuda.set_device(self.device)
+        return self
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def float_rows(x: torch.Tensor, what: str) -> torch.Tensor:
+    """x as the library takes float rows: 2-D, columns next to one another, any row stride."""
+    if x.dim() != 2:
+        raise ValueError(f"{what} must be a 2-D tensor (got {x.dim()}-D)")
+    if x.dtype not in _WDT:
+        raise TypeError(f"{what} must be float32, float16 or bfloat16 (got {x.dtype})")
+    if (x.shape[1] > 1 and x.stride(1) != 1) or (x.shape[0] > 1 and x.stride(0) < x.shape[1]):
+        x = x.contiguous()
+    return x
+
+
+def _row_stride(x: torch.Tensor) -> int:
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _check_rows(w: Int8Rows, what: str) -> None:
+    c, s = w.codes, w.scales
+    if c.dtype is not torch.int8 or c.shape != (w.rows, _pitch(w.cols)) or not c.is_contiguous():
+        raise ValueError(f"{what}: codes must be a contiguous int8 [{w.rows}][{_pitch(w.cols)}] tensor")
+    if s.dtype is not torch.float32 or s.numel() != w.rows or not s.is_contiguous():
+        raise ValueError(f"{what}: scales must be a contiguous float32 vector of length {w.rows}")
+
+
+def quantize_int8(x: torch.Tensor) -> Int8Rows:
+    """Int8 codes and scales of the rows of x [rows][cols] (float32, float16 or bfloat16; rows may
+    be strided): scale = max |x| / 127, code = rint(x / scale).  A row with a NaN or an infinity
+    gets a NaN scale."""
+    x = float_rows(x, "x")
+    rows, cols = x.shape
+    with on_device(x):
+        out = Int8Rows(torch.empty((rows, _pitch(cols)), dtype=torch.int8, device=x.device),
+                       torch.empty(rows, dtype=torch.float32, device=x.device), rows, cols)
+        check(lib().w8_quantize_rows(x.data_ptr(), _WDT[x.dtype], rows, cols, _row_stride(x), out.codes.data_ptr(),
+                                     out.scales.data_ptr(), _stream(x.device)))
+    return out
+
+
+def _segments(outs, M: int, width: int, dt: torch.dtype):
+    if dt not in _ODT:
+        raise ValueError(f"outputs must be float32, float16 or bfloat16 (got {dt})")
+    if sum(o.shape[-1] for o in outs) != width:
+        raise ValueError(f"the outputs' columns must sum to {width}")
+    segs = (_lib.W4OutSeg * len(outs))()
+    for i, o in enumerate(outs):
+        if o.dtype != dt or o.dim() != 2 or o.shape[0] != M or (o.shape[1] > 1 and o.stride(1) != 1):
+            raise ValueError(f"each output must be a 2-D [{M}][cols] {dt} tensor with contiguous rows")
+        segs[i].Y = o.data_ptr()
+        segs[i].cols = o.shape[1]
+        segs[i].ld = o.stride(0) if M > 1 else o.shape[1]
+    return segs
+
+
+def _space(size: ctypes.c_size_t, device):
+    return torch.empty(size.value, dtype=torch.uint8, device=device) if size.value else None
+
+
+def _product(a, w: Int8Rows, bias, outs, dt: torch.dtype):
+    """One product written to `outs`, which cover its columns in order."""
+    L = lib()
+    N, K = w.rows, w.cols
+    size = ctypes.c_size_t(0)
+    _check_rows(w, "weight")
+    if bias is not None and (bias.dtype != dt or bias.numel() != N or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous {dt} vector of length {N}")
+    ready = isinstance(a, Int8Rows)
+    if ready:
+        _check_rows(a, "activations")
+        M, width = a.rows, a.cols
+    else:
+        M, width = a.shape
+    if width != K:
+        raise ValueError(f"activation width {width} does not match the weight ({N}x{K})")
+    segs = _segments(outs, M, N, dt)
+    x = a.codes if ready else a
+    with on_device(x, a.scales if ready else None, w.codes, w.scales, bias, *outs):
+        bp = bias.data_ptr() if bias is not None else None
+        check(L.w8a8_workspace_bytes(M, N, K, -1 if ready else _WDT[a.dtype], ctypes.byref(size)))
+        ws = _space(size, x.device)
+        wp = ws.data_ptr() if ws is not None else None
+        if ready:
+            check(L.w8a8_mm(x.data_ptr(), a.scales.data_ptr(), M, w.codes.data_ptr(), w.scales.data_ptr(), N, K, bp,
+                            _ODT[dt], segs, len(outs), wp, size.value, _stream(x.device)))
+        else:
+            check(L.w8a8_linear(x.data_ptr(), _WDT[a.dtype], _row_stride(a), M, w.codes.data_ptr(), w.scales.data_ptr(),
+                                N, K, bp, _ODT[dt], segs, len(outs), wp, size.value, _stream(x.device)))
+
+
+def mm_int8(a, w: Int8Rows, bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+            out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """Y = A @ W^T (+ bias) in 8-bit integers, one scale per token and one per channel.
+
+    `a` is a float tensor [M][K] (float32, float16 or bfloat16), quantized per token within the
+    call, or an Int8Rows.  The integer sums are exact; each is scaled and the bias added in
+    fp32, then rounded once to the output dtype: fp32 unless `out_dtype` (or `out`) asks for
+    bfloat16 / float16.  The bias has the output dtype."""
+    if not isinstance(a, Int8Rows):
+        a = float_rows(a, "activations")
+    dev = w.codes.device
+    M = a.rows if isinstance(a, Int8Rows) else a.shape[0]
+    dt = out_dtype if out_dtype is not None else (out.dtype if out is not None else torch.float32)
+    if out is None:
+        out = torch.empty((M, w.rows), dtype=dt, device=dev)
+    elif out.shape != (M, w.rows) or out.dtype != dt:
+        raise ValueError(f"out must be a {dt} tensor of shape ({M}, {w.rows})")
+    _product(a, w, bias, [out], dt)
+    return out
+
+
+def mm_int8_split(a, w: Int8Rows, outs: list[torch.Tensor], bias: torch.Tensor | None = None) -> list[torch.Tensor]:
+    """mm_int8 written to separate outputs in one launch: outs[i] [M][n_i] receives the next n_i
+    output columns (for a fused Q/K/V weight: Q, K and V).  At most four outputs, of one dtype;
+    they may be row-strided views.  The bias, if any, spans all output columns in that dtype."""
+    if not isinstance(a, Int8Rows):
+        a = float_rows(a, "activations")
+    _product(a, w, bias, list(outs), outs[0].dtype)
+    return list(outs)
+
+
+def mm_int8_t(dy: torch.Tensor, w: Int8Rows, out: torch.Tensor | None = None,
+              out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """dX = dY @ W, the input gradient of ``mm_int8``, on the same int8 weight.
+
+    dY [M][N] is bfloat16 or float16 (rows may be strided); the weight operand is codes * scale
+    rounded to that dtype, sums are fp32 and the result is rounded once to `out_dtype` (fp32
+    unless given)."""
+    if dy.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"dY must be bfloat16 or float16 (got {dy.dtype})")
+    dy = float_rows(dy, "dY")
+    M, width = dy.shape
+    N, K = w.rows, w.cols
+    if width != N:
+        raise ValueError(f"gradient width {width} does not match the weight ({N}x{K})")
+    _check_rows(w, "weight")
+    dt = out_dtype if out_dtype is not None else (out.dtype if out is not None else torch.float32)
+    if out is None:
+        out = torch.empty((M, K), dtype=dt, device=dy.device)
+    elif out.shape != (M, K) or out.dtype != dt:
+        raise ValueError(f"out must be a {dt} tensor of shape ({M}, {K})")
+    segs = _segments([out], M, K, dt)
+    ld = _row_stride(dy)
+    size = ctypes.c_size_t(0)
+    with on_device(dy, w.codes, w.scales, out):
+        L = lib()
+        check(L.w8a16_mm_t_workspace_bytes(M, N, K, ld if dy.data_ptr() % 16 == 0 else -1, ctypes.byref(size)))
+        ws = _space(size, dy.device)
+        check(L.w8a16_mm_t(dy.data_ptr(), _WDT[dy.dtype], ld, M, w.codes.data_ptr(), w.scales.data_ptr(), N, K, _ODT[dt],
+                           segs, 1, ws.data_ptr() if ws is not None else None, size.value, _stream(dy.device)))
+    return out
+
+
+def int8_kernel_for(M: int, N: int, K: int) -> str | None:
+    """Name of the kernel that multiplies M tokens by a weight of this shape (host-side query)."""
+    r = lib().w8a8_kernel(M, N, K, _lib.DT_BF16)
+    return r.decode() if r is not None else None

@@ -26,7 +26,8 @@ from __future__ import annotations
 
 import torch
 
-from . import ops
+from . import int8, ops
+from .int8 import Int8Rows
 from .ops import QuantizedWeight
 
 _OUT_DTYPES = (None, torch.float32, torch.bfloat16, torch.float16)
@@ -106,3 +107,72 @@ class W4A16Linear(torch.nn.Module):
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         return w4a16_linear(x, self.qw, self.bias, self.out_dtype)
+
+
+class _W8A8Matmul(torch.autograd.Function):
+    """Forward: tokens quantized to int8, integer product.  Backward: dX = dY @ (codes * scale)
+    with 16-bit gradients, the rounding of the tokens passed straight through."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, w: Int8Rows, bias: torch.Tensor | None, out_dtype: torch.dtype | None):
+        lead = x.shape[:-1]
+        odt = torch.float32 if out_dtype is None else out_dtype
+        y = int8.mm_int8(x.reshape(-1, x.shape[-1]), w, bias=None if bias is None else _operand(bias, odt),
+                         out_dtype=odt)
+        ctx.w, ctx.lead, ctx.x_dtype = w, lead, x.dtype
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y.view(*lead, w.rows)
+
+    @staticmethod
+    def backward(ctx, gy: torch.Tensor):
+        w: Int8Rows = ctx.w
+        g2 = gy.reshape(-1, w.rows)
+        dx = None
+        if ctx.needs_input_grad[0]:
+            # fp32 activations take bf16 gradients (fp32's range) and an fp32 result
+            g16 = g2.to(ctx.x_dtype if ctx.x_dtype in _HALF else torch.bfloat16)
+            dx = int8.mm_int8_t(g16, w, out_dtype=ctx.x_dtype).view(*ctx.lead, w.cols)
+        db = g2.float().sum(0).to(ctx.bias_dtype) if ctx.needs_input_grad[2] else None
+        return dx, None, db, None
+
+
+def w8a8_linear(x: torch.Tensor, w: Int8Rows, bias: torch.Tensor | None = None,
+                out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """Differentiable ``x @ w^T (+ bias)`` in 8-bit integers over an int8 weight (one scale per
+    output channel), x (float32, float16 or bfloat16) quantized per token: fp32 result, or
+    ``out_dtype`` (bfloat16 / float16) rounded once."""
+    if out_dtype not in _OUT_DTYPES:
+        raise ValueError(f"out_dtype must be None, float32, bfloat16 or float16, not {out_dtype}")
+    return _W8A8Matmul.apply(x, w, bias, out_dtype)
+
+
+class W8A8Linear(torch.nn.Module):
+    """A frozen int8 linear layer on dynamically quantized activations; fp32 output, or
+    ``out_dtype`` (bfloat16 / float16, the bias held in that dtype)."""
+
+    def __init__(self, w: Int8Rows, bias: torch.Tensor | None = None, out_dtype: torch.dtype | None = None):
+        super().__init__()
+        if out_dtype not in _OUT_DTYPES:
+            raise ValueError(f"out_dtype must be None, float32, bfloat16 or float16, not {out_dtype}")
+        self.w = w
+        self.out_dtype = out_dtype
+        if bias is not None:
+            bias = bias.detach().to(torch.float32 if out_dtype is None else out_dtype).contiguous()
+        self.register_buffer("bias", bias)
+
+    @classmethod
+    def from_weight(cls, weight: torch.Tensor, bias: torch.Tensor | None = None,
+                    out_dtype: torch.dtype | None = None) -> "W8A8Linear":
+        """Quantize a [N][K] fp32 / fp16 / bf16 device weight, one scale per row, and wrap it."""
+        return cls(int8.quantize_int8(weight), bias, out_dtype)
+
+    @property
+    def in_features(self) -> int:
+        return self.w.cols
+
+    @property
+    def out_features(self) -> int:
+        return self.w.rows
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        return w8a8_linear(x, self.w, self.bias, self.out_dtype)

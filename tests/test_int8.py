@@ -1,0 +1,403 @@
+"""The 8-bit integer linear operators: refusals on the host, and on the GPU the quantizer
+bit for bit, the product against int64 sums, the gradient against its formula in 64 bits
+and against differences of the product itself."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import gemv_int4_quantize_amd as w4
+from gemv_int4_quantize_amd import _lib
+
+DEV = "cuda:0"
+EPS32 = 2.0**-24  # half an ulp of 1 in fp32
+HALF_ULP = {torch.float32: 2.0**-24, torch.float16: 2.0**-11, torch.bfloat16: 2.0**-8}
+TINY = {torch.float32: 2.0**-149, torch.float16: 2.0**-24, torch.bfloat16: 2.0**-133}
+
+
+# ---------------------------------------------------------------- host only
+
+
+def _p(v=0x10000):  # an aligned address that is never dereferenced: every call below is refused
+    return ctypes.c_void_p(v)
+
+
+def _seg(cols, y=0x10000, ld=None):
+    s = (_lib.W4OutSeg * 1)()
+    s[0].Y, s[0].cols, s[0].ld = y, cols, cols if ld is None else ld
+    return s
+
+
+def test_header_and_exports():
+    import os
+    import re
+
+    path = os.path.join(os.path.dirname(os.path.dirname(__file__)), "include", "w8a8.h")
+    names = re.findall(r"^(?:int|int64_t|const char\*)\s+(w8\w+|tok\w+)\s*\(", open(path).read(), flags=re.M)
+    assert sorted(names) == sorted(_lib.EXPORTS_W8)
+    for n in names:
+        assert hasattr(w4.lib(), n), n
+
+
+def test_pitch():
+    L = w4.lib()
+    assert [L.w8_pitch(k) for k in (0, 1, 64, 65, 11008)] == [-1, 64, 64, 128, 11008]
+
+
+def test_quantize_refusals():
+    q = w4.lib().w8_quantize_rows
+    assert q(_p(), 0, 4, 0, 64, _p(), _p(), None) == _lib.W4_ERR_INVALID
+    assert q(_p(), 7, 4, 64, 64, _p(), _p(), None) == _lib.W4_ERR_INVALID
+    assert q(_p(), 2, -1, 64, 64, _p(), _p(), None) == _lib.W4_ERR_INVALID
+    assert q(_p(), 2, 4, 64, 63, _p(), _p(), None) == _lib.W4_ERR_INVALID
+    assert q(None, 2, 4, 64, 64, _p(), _p(), None) == _lib.W4_ERR_INVALID
+    assert q(_p(), 2, 4, 64, 64, None, _p(), None) == _lib.W4_ERR_INVALID
+    assert q(_p(), 2, 4, 1 << 17, 1 << 17, _p(), _p(), None) == _lib.W4_ERR_UNSUPPORTED
+    assert q(_p(0x10001), 2, 4, 64, 64, _p(), _p(), None) == _lib.W4_ERR_ALIGN
+    assert q(_p(), 2, 4, 64, 64, _p(0x10008), _p(), None) == _lib.W4_ERR_ALIGN
+    assert q(None, 2, 0, 64, 64, None, None, None) == _lib.W4_OK
+
+
+def test_product_refusals():
+    def mm(A=_p(), sa=_p(), M=4, W=_p(), sw=_p(), N=64, K=128, bias=None, dt=0, segs=_seg(64), n=1, ws=None, wsb=0):
+        return w4.lib().w8a8_mm(A, sa, M, W, sw, N, K, bias, dt, segs, n, ws, wsb, None)
+
+    assert mm(M=-1) == _lib.W4_ERR_INVALID
+    assert mm(N=0) == _lib.W4_ERR_INVALID
+    assert mm(K=0) == _lib.W4_ERR_INVALID
+    assert mm(K=1 << 17) == _lib.W4_ERR_UNSUPPORTED
+    assert mm(A=None) == _lib.W4_ERR_INVALID
+    assert mm(sw=None) == _lib.W4_ERR_INVALID
+    assert mm(W=_p(0x10004)) == _lib.W4_ERR_ALIGN
+    assert mm(dt=3) == _lib.W4_ERR_INVALID
+    assert mm(segs=_seg(63)) == _lib.W4_ERR_INVALID
+    assert mm(segs=_seg(64, ld=60)) == _lib.W4_ERR_INVALID
+    assert mm(segs=_seg(64, y=None)) == _lib.W4_ERR_INVALID
+    assert mm(n=5) == _lib.W4_ERR_INVALID
+    assert mm(bias=_p(0x10002)) == _lib.W4_ERR_ALIGN
+    assert mm(ws=_p(0x10004), wsb=64) == _lib.W4_ERR_ALIGN
+    assert mm(M=0, A=None) == _lib.W4_OK
+    assert "4" in _lib.status_string(_lib.W4_ERR_ALIGN)
+
+
+def test_linear_and_gradient_refusals():
+    L = w4.lib()
+
+    def linear(X=_p(), dt=2, ld=128, M=64, ws=None, wsb=0):
+        return L.w8a8_linear(X, dt, ld, M, _p(), _p(), 64, 128, None, 0, _seg(64), 1, ws, wsb, None)
+
+    assert linear(dt=5) == _lib.W4_ERR_INVALID
+    assert linear(ld=100) == _lib.W4_ERR_INVALID
+    assert linear(X=None) == _lib.W4_ERR_INVALID
+    size = ctypes.c_size_t(0)
+    assert L.w8a8_workspace_bytes(64, 64, 128, 2, ctypes.byref(size)) == 0 and size.value >= 64 * 128 + 64 * 4
+    assert linear() == _lib.W4_ERR_RESOURCE
+    assert linear(ws=_p(), wsb=size.value - 1) == _lib.W4_ERR_RESOURCE
+
+    def mt(dY=_p(), dt=2, ld=64, M=4, N=64, K=128, segs=_seg(128), ws=None, wsb=0):
+        return L.w8a16_mm_t(dY, dt, ld, M, _p(), _p(), N, K, 0, segs, 1, ws, wsb, None)
+
+    assert mt(dt=0) == _lib.W4_ERR_INVALID
+    assert mt(dY=None) == _lib.W4_ERR_INVALID
+    assert mt(segs=_seg(64)) == _lib.W4_ERR_INVALID
+    assert mt(N=1 << 22, ld=1 << 22) == _lib.W4_ERR_UNSUPPORTED
+    assert mt(N=63) == _lib.W4_ERR_RESOURCE  # an unaligned dY needs its copy
+    assert mt(dY=_p(0x10002)) == _lib.W4_ERR_RESOURCE
+    assert L.w8a16_mm_t_workspace_bytes(4, 63, 128, 63, ctypes.byref(size)) == 0 and size.value >= 4 * 64 * 2
+
+
+def test_binding_refusals():
+    w = w4.Int8Rows(torch.zeros(8, 64, dtype=torch.int8), torch.ones(8), 8, 64)
+    x = torch.zeros(2, 64)
+    with pytest.raises(ValueError, match="HIP device"):
+        w4.mm_int8(x, w)
+    with pytest.raises(ValueError, match="width"):
+        w4.mm_int8(torch.zeros(2, 63), w)
+    with pytest.raises(TypeError):
+        w4.mm_int8(torch.zeros(2, 64, dtype=torch.float64), w)
+    with pytest.raises(ValueError, match="bias"):
+        w4.mm_int8(x, w, bias=torch.zeros(7))
+    with pytest.raises(ValueError, match="out must"):
+        w4.mm_int8(x, w, out=torch.zeros(2, 9))
+    with pytest.raises(ValueError, match="codes"):
+        w4.mm_int8(x, w4.Int8Rows(torch.zeros(8, 63, dtype=torch.int8), torch.ones(8), 8, 63))
+    with pytest.raises(ValueError, match="scales"):
+        w4.mm_int8(x, w4.Int8Rows(torch.zeros(8, 64, dtype=torch.int8), torch.ones(7), 8, 64))
+    with pytest.raises(ValueError, match="sum to"):
+        w4.mm_int8_split(x, w, [torch.zeros(2, 3)])
+    with pytest.raises(TypeError):
+        w4.mm_int8_t(torch.zeros(2, 8), w)
+    with pytest.raises(ValueError, match="width"):
+        w4.mm_int8_t(torch.zeros(2, 9, dtype=torch.bfloat16), w)
+    with pytest.raises(ValueError, match="out_dtype"):
+        w4.W8A8Linear(w, out_dtype=torch.int8)
+
+
+# ---------------------------------------------------------------- GPU
+
+
+def _rows(seed, rows, cols, dtype, pad=0, scale=1.0):
+    """Seeded rows with per-row magnitudes, as (device tensor of rows `pad` longer, fp32 numpy)."""
+    g = np.random.default_rng(seed)
+    a = g.standard_normal((rows, cols)) * np.exp(g.standard_normal((rows, 1))) * scale
+    t = torch.from_numpy(a.astype(np.float32)).to(dtype)
+    wide = torch.full((rows, cols + pad), float("nan"), dtype=dtype)
+    wide[:, :cols] = t
+    return wide.to(DEV)[:, :cols], t.float().numpy()
+
+
+def _quantize_ref(x32):
+    """The definition in IEEE fp32, step by step."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        a = np.abs(x32).max(axis=1)
+        s = np.maximum(a / np.float32(127), np.float32(2.0**-126)).astype(np.float32)
+        q = np.rint(x32 * (np.float32(1) / s)[:, None])
+    bad = ~np.isfinite(x32).all(axis=1)
+    s[bad] = np.nan
+    q[bad] = 0
+    return q.astype(np.int8), s
+
+
+def _weight(seed, n, k):
+    g = np.random.default_rng(seed)
+    codes = np.zeros((n, (k + 63) // 64 * 64), dtype=np.int8)
+    codes[:, :k] = g.integers(-127, 128, (n, k), dtype=np.int8)
+    scales = (0.001 * np.exp(0.5 * g.standard_normal(n))).astype(np.float32)
+    w = w4.Int8Rows(torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV), n, k)
+    return w, codes[:, :k].astype(np.int64), scales.astype(np.float64)
+
+
+def _check_rounded(y, ref, size, dtype, what, steps=4):
+    """|y - ref| <= `steps` fp32 roundings of magnitude `size`, and one rounding to dtype."""
+    y = y.double().cpu().numpy()
+    tol = steps * EPS32 * size + (HALF_ULP[dtype] * (np.abs(ref) + steps * EPS32 * size) + TINY[dtype]
+                                  if dtype != torch.float32 else 0.0)
+    bad = ~(np.abs(y - ref) <= tol)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.size} outside, worst {np.abs(y - ref)[bad].max():.3e}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (3, 7, 1), (5, 64, 0), (2, 65, 3), (9, 2048, 0), (4, 2049, 5),
+                                           (3, 8191, 0), (7, 11008, 0), (2, 16385, 0), (1, 70001, 2)])
+def test_quantize_bits(dtype, rows, cols, pad):
+    x, x32 = _rows(rows * 1000 + cols, rows, cols, dtype, pad)
+    r = w4.quantize_int8(x)
+    q, s = _quantize_ref(x32)
+    np.testing.assert_array_equal(r.scales.cpu().numpy(), s)
+    got = r.codes.cpu().numpy()
+    np.testing.assert_array_equal(got[:, :cols], q)
+    assert not got[:, cols:].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_quantize_special_rows(dtype):
+    x32 = np.random.default_rng(3).standard_normal((7, 100)).astype(np.float32)
+    x32[0] = 0
+    x32[1, 17] = np.nan
+    x32[2, 99] = np.inf
+    x32[3, 0] = -np.inf
+    x32[4] = 2.0**-130 if dtype != torch.float16 else 2.0**-24  # below the least normal fp32 (or fp16)
+    x32[5, :] = 1.0
+    x32[6, 5] = torch.finfo(dtype).max
+    t = torch.from_numpy(x32).to(dtype)
+    r = w4.quantize_int8(t.to(DEV))
+    q, s = _quantize_ref(t.float().numpy())
+    np.testing.assert_array_equal(r.scales.cpu().numpy(), s)
+    np.testing.assert_array_equal(r.codes.cpu().numpy()[:, :100], q)
+    w, _, _ = _weight(1, 16, 100)
+    y = w4.mm_int8(t.to(DEV), w).cpu().numpy()
+    assert np.isnan(y[1:4]).all() and np.isfinite(y[[0, 4, 5, 6]]).all() and not y[0].any()
+
+
+SHAPES = [(1, 1, 1), (1, 64, 64), (1, 2048, 2048), (2, 33, 70), (3, 1000, 4096), (4, 512, 11008), (5, 100, 129),
+          (16, 48, 4096), (17, 515, 2048), (32, 256, 1030), (33, 130, 640), (64, 96, 8192), (65, 300, 1000),
+          (127, 257, 511), (128, 128, 128), (200, 640, 192), (257, 259, 300), (300, 1003, 1555), (515, 2050, 257)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", SHAPES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_product(m, n, k, dtype):
+    """Float activations and int8 rows give the same bits, equal to the int64 sums scaled."""
+    x, x32 = _rows(m + n + k, m, k, dtype, pad=3 if m % 2 else 0)
+    w, codes, scales = _weight(n + k, n, k)
+    bias = torch.from_numpy(np.random.default_rng(5).standard_normal(n).astype(np.float32)).to(dtype)
+    y = w4.mm_int8(x, w, bias=bias.to(DEV), out_dtype=dtype)
+    xq = w4.quantize_int8(x)
+    y2 = w4.mm_int8(xq, w, bias=bias.to(DEV), out_dtype=dtype)
+    assert torch.equal(y, y2)
+    q, s = _quantize_ref(x32)
+    prod = (q.astype(np.int64) @ codes.T).astype(np.float64) * s.astype(np.float64)[:, None] * scales
+    b = bias.double().numpy()
+    # conversion of the sum, two products, the bias
+    _check_rounded(y, prod + b, np.abs(prod) + np.abs(b), dtype, f"{m}x{n}x{k}")
+    y3 = w4.mm_int8(xq, w)
+    _check_rounded(y3, prod, np.abs(prod), torch.float32, f"{m}x{n}x{k} fp32")
+    assert torch.equal(w4.mm_int8(xq, w), y3)  # the same bits again
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 2, 20, 130])
+def test_product_extreme_codes(m):
+    """Sums near the int32 limit: K = 131071 codes of -128 and 127."""
+    k, n = 131071, 5
+    codes = torch.full((n, 131072), -128, dtype=torch.int8)
+    codes[:, k:] = 0
+    codes[1] = -codes[1].to(torch.int16).clamp(-127, 127).to(torch.int8)
+    a = torch.full((m, 131072), -128, dtype=torch.int8)
+    a[:, k:] = 0
+    w = w4.Int8Rows(codes.to(DEV), torch.ones(n, device=DEV), n, k)
+    y = w4.mm_int8(w4.Int8Rows(a.to(DEV), torch.ones(m, device=DEV), m, k), w).cpu()
+    ref = (a[0].long() * codes.long()).sum(1).float()
+    assert torch.equal(y, ref.expand(m, n))
+
+
+@pytest.mark.gpu
+def test_product_split_outputs_and_views():
+    m, k = 37, 320
+    w, _, _ = _weight(8, 24 + 8 + 9, k)
+    x, _ = _rows(4, m, k, torch.bfloat16)
+    whole = w4.mm_int8(x, w, out_dtype=torch.bfloat16)
+    bufs = [torch.full((m, c + 5), 7.0, dtype=torch.bfloat16, device=DEV) for c in (24, 8, 9)]
+    w4.mm_int8_split(x, w, [b[:, 2:-3] for b in bufs])
+    assert torch.equal(torch.cat([b[:, 2:-3] for b in bufs], 1), whole)
+    for b in bufs:
+        assert (b[:, :2] == 7).all() and (b[:, -3:] == 7).all()
+    for mm in (1, 4, 40):  # rows before and after the output stay as they are
+        x, _ = _rows(mm, mm, k, torch.bfloat16)
+        guard = torch.full((mm + 2, 41), 3.0, device=DEV)
+        w4.mm_int8(x, w, out=guard[1:-1])
+        assert (guard[0] == 3).all() and (guard[-1] == 3).all() and (guard[1:-1] != 3).any()
+
+
+@pytest.mark.gpu
+def test_product_no_rows():
+    w, _, _ = _weight(2, 8, 64)
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV)
+    assert w4.mm_int8(x, w).shape == (0, 8)
+    assert w4.mm_int8_t(torch.empty(0, 8, dtype=torch.bfloat16, device=DEV), w).shape == (0, 64)
+    assert w4.quantize_int8(x).codes.shape == (0, 64)
+
+
+@pytest.mark.gpu
+def test_product_far_offsets():
+    """A weight of more than 2^31 bytes."""
+    n, k = 70003, 32768
+    codes = torch.randint(-127, 128, (n, k), dtype=torch.int8, device=DEV)
+    scales = torch.rand(n, device=DEV) + 0.5
+    w = w4.Int8Rows(codes, scales, n, k)
+    for m in (2, 40, 130):
+        x = torch.randn(m, k, device=DEV)
+        xq = w4.quantize_int8(x)
+        y = w4.mm_int8(xq, w)
+        rows = torch.cat([torch.arange(4), torch.arange(65530, 65540), torch.arange(n - 60, n)]).to(DEV)
+        ref = (xq.codes.double() @ codes[rows].double().t()) * xq.scales.double()[:, None] * scales[rows].double()
+        _check_rounded(y[:, rows], ref.cpu().numpy(), ref.abs().cpu().numpy(), torch.float32, f"m={m}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k,pad", [(1, 64, 64, 0), (3, 100, 70, 0), (16, 2027, 130, 0), (33, 512, 1030, 8),
+                                       (64, 8, 2048, 0), (100, 1000, 257, 3), (131, 515, 128, 0), (300, 264, 520, 0),
+                                       (257, 1024, 1024, 0), (520, 320, 4160, 16)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_gradient_formula(m, n, k, pad, dtype):
+    dy, dy32 = _rows(m + n, m, n, dtype, pad, scale=0.1)
+    w, codes, _ = _weight(k, n, k)
+    s32 = w.scales.cpu().numpy()
+    op = torch.from_numpy(codes.astype(np.float32) * s32[:, None]).to(dtype).double().numpy()
+    ref = dy32.astype(np.float64) @ op
+    size = np.abs(dy32).astype(np.float64) @ np.abs(op)
+    for out in (dtype, torch.float32):
+        # n products and as many additions in fp32, in any order
+        _check_rounded(w4.mm_int8_t(dy, w, out_dtype=out), ref, size, out, f"{m}x{n}x{k}", steps=n + 2)
+
+
+@pytest.mark.gpu
+def test_gradient_misaligned():
+    w, _, _ = _weight(11, 200, 96)
+    buf = torch.randn(50 * 200 + 8, device=DEV).to(torch.bfloat16)
+    dy = buf[1:1 + 50 * 200].view(50, 200)  # two bytes off a 16-byte boundary
+    assert torch.equal(w4.mm_int8_t(dy, w), w4.mm_int8_t(dy.clone(), w))
+
+
+@pytest.mark.gpu
+def test_gradient_differences():
+    """Central differences of the product itself: integer tokens with a 127 in each row have scale
+    1, so a step of one in another entry moves the output by exactly one code's worth."""
+    m, n, k = 5, 24, 40
+    g = np.random.default_rng(6)
+    x = g.integers(-60, 61, (m, k)).astype(np.float32)
+    x[:, 0] = 127
+    w, _, _ = _weight(12, n, k)
+    dy = torch.from_numpy(g.standard_normal((m, n)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    dx = w4.mm_int8_t(dy, w).double().cpu().numpy()
+
+    def f(a):
+        return (dy.double() * w4.mm_int8(torch.from_numpy(a).to(DEV), w).double()).sum(1).cpu().numpy()
+
+    wop = np.abs(w.codes.cpu().numpy()[:, :k] * w.scales.cpu().numpy()[:, None].astype(np.float64))
+    ybig = np.abs(x).astype(np.float64) @ wop.T
+    dyn = dy.double().abs().cpu().numpy()
+    for j in range(1, k):
+        up, dn = x.copy(), x.copy()
+        up[:, j] += 1
+        dn[:, j] -= 1
+        # the weight operand's rounding to bf16, and the fp32 rounding of the two outputs
+        tol = (dyn @ wop[:, j]) * (2.0**-8 + 30 * EPS32) + (dyn * (ybig + 127 * wop.max())).sum(1) * 4 * EPS32
+        assert (np.abs((f(up) - f(dn)) / 2 - dx[:, j]) <= tol).all(), j
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_layer_autograd(dtype):
+    wt = torch.randn(48, 96, device=DEV) * 0.05
+    layer = w4.W8A8Linear.from_weight(wt, bias=torch.randn(48, device=DEV), out_dtype=dtype)
+    layer.bias.requires_grad_()
+    x = torch.randn(2, 7, 96, device=DEV).to(dtype).requires_grad_()
+    y = layer(x)
+    assert y.shape == (2, 7, 48) and y.dtype == dtype
+    gy = torch.randn_like(y)
+    y.backward(gy)
+    g16 = gy if dtype != torch.float32 else gy.to(torch.bfloat16)
+    assert torch.equal(x.grad.view(-1, 96), w4.mm_int8_t(g16.view(-1, 48), layer.w, out_dtype=dtype))
+    assert torch.allclose(layer.bias.grad.float(), gy.view(-1, 48).float().sum(0).to(dtype).float())
+    # the int8 product is within one half code a term of the float one
+    ref = torch.nn.functional.linear(x.double(), wt.double(), layer.bias.double())
+    assert ((y.double() - ref).norm() / ref.norm()).item() < 0.03
+
+
+@pytest.mark.gpu
+def test_other_stream():
+    w, _, _ = _weight(21, 128, 512)
+    st = torch.cuda.Stream()
+    for m in (2, 70):
+        x, _ = _rows(m, m, 512, torch.bfloat16)
+        want = w4.mm_int8(x, w)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            got = w4.mm_int8(x, w)
+        st.synchronize()
+        assert torch.equal(got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 48, 160])
+def test_graph_replays(m):
+    w, _, _ = _weight(31, 256, 1024)
+    x, _ = _rows(m, m, 1024, torch.bfloat16)
+    x = x.contiguous()
+    w4.mm_int8(x, w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = w4.mm_int8(x, w)
+    for i in range(3):
+        x.copy_(_rows(100 + i, m, 1024, torch.bfloat16)[0])
+        want = w4.mm_int8(x, w)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
