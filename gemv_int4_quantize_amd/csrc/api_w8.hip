@@ -243,7 +243,8 @@ int tok_workspace_bytes(int64_t M, int64_t V, int top, size_t* bytes) {
 
 static int check_temperature(double t, float* inv) {
   *inv = (float)(1.0 / t);
-  if (!(t > 0.0) || !(*inv > 0.0f) || !std::isfinite(*inv))
+  // the kernels scale by log2(e) / t as well
+  if (!(t > 0.0) || !(*inv > 0.0f) || !std::isfinite(*inv * 1.5f))
     return fail(W4_ERR_INVALID, "temperature = %g must be positive with a finite fp32 reciprocal", t);
   return W4_OK;
 }

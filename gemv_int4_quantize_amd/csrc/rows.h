@@ -63,6 +63,19 @@ __device__ __forceinline__ void widen8(const Raw8<DT>& r, float v[8]) {
   }
 }
 
+// Maximum over the wave in every lane, without LDS round trips: partners lane ^ 32 and ^ 16
+// by permlane swaps, then row mirror, half-row mirror and quad permutes.
+__device__ __forceinline__ float wave_max(float v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+  v = __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, false)));
+  v = __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false)));
+  v = __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false)));
+  return __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false)));
+}
+
 template <int DT>
 __device__ __forceinline__ float elem_to_f32(typename Elem<DT>::type x) {
   if constexpr (DT == W4_DT_F32) return x;

@@ -3,6 +3,21 @@
 //   S = sum e^d,  logprob = d_t - log S,  entropy = log S - sum e^d d / S.
 // The maximum is taken off before the division by T, so that nothing overflows (a mask of
 // the type's lowest value divided by a small T) and the most likely tokens keep their bits.
+//
+// Forward: one pass over the logits.  Each thread keeps the maximum of what it has read and
+// S and sum e^d d relative to it, rescaled once per group of kU chunks (a group's maximum
+// is taken before its exponentials, so the rescaling costs one exponential per group and
+// not one per new maximum).  A row is read by one workgroup, or cut into parts whose
+// results a second, one-wave launch joins, when there are few rows.
+//
+// Alternatives: the maxima of 128 pairs of threads are on hand after the pass, and the k-th
+// largest of them is a threshold that at least k logits reach, while only the chunks of
+// those pairs can hold one that does.  These few chunks are read again (from cache).
+// Logits above the threshold are collected and ranked by counting; of those equal to it the
+// lowest ids are kept, in order.  So rows with many equal logits, or with fewer unmasked
+// logits than alternatives, cost the same few chunks.
+#include <algorithm>
+
 #include "api_common.h"
 #include "launch.h"
 #include "rows.h"
@@ -11,179 +26,568 @@ namespace w4 {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-// below this a term of the softmax is 0 in fp32: arguments are held above it, so that
-// -infinity gives 0 and not infinity * 0
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -3.4028234663852886e38f;
+// e^d d is 0 below this (exp2 is): arguments are held above it, so that -infinity gives 0
+// and not infinity * 0
 constexpr float kFloor = -1.0e4f;
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+constexpr int kT = 256;       // threads
+constexpr int kPairs = kT / 2;
+constexpr int kMaxTop = 64;
+constexpr int kCand = 1024;   // logits above the threshold that are held at a time
+constexpr int kMaxParts = 64; // parts of a row, one per lane of the joining wave
+constexpr int kMinSeg = kT * 8;
+
+// Running softmax statistics: the largest logit, S and sum e^d d (in units of log2) relative
+// to it.  m is -infinity while only masked logits were seen.
+struct Stat {
+  float m, s, t;
+};
+
+// The statistics of both, relative to the larger maximum.
+__device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c) {
+  Stat r;
+  r.m = fmaxf(a.m, b.m);
+  const float base = fmaxf(r.m, kLowest);
+  // an infinite distance scales a zero sum by zero
+  const float da = fminf((base - fmaxf(a.m, kLowest)) * c, 1e30f), db = fminf((base - fmaxf(b.m, kLowest)) * c, 1e30f);
+  const float ea = __builtin_amdgcn_exp2f(-da), eb = __builtin_amdgcn_exp2f(-db);
+  r.s = a.s * ea + b.s * eb;
+  r.t = (a.t - da * a.s) * ea + (b.t - db * b.s) * eb;
+  return r;
 }
 
-template <int T>
-__device__ __forceinline__ float block_sum(float v, float* sh) {
-  v = wave_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.0f;
+__device__ __forceinline__ Stat wave_join(Stat st, float c) {
 #pragma unroll
-  for (int i = 0; i < T / 64; ++i) s += sh[i];
-  return s;
+  for (int o = 32; o > 0; o >>= 1) {
+    const Stat p = {__shfl_xor(st.m, o), __shfl_xor(st.s, o), __shfl_xor(st.t, o)};
+    st = join(st, p, c);
+  }
+  return st;
 }
 
-constexpr int kT = 512;
+// One group of N logits into the running statistics.
+template <int N>
+__device__ __forceinline__ void take(Stat& st, const float (&v)[N], float c) {
+  float m = st.m;
+#pragma unroll
+  for (int j = 0; j < N; j += 2) m = __builtin_fmaxf(__builtin_fmaxf(m, v[j]), v[j + 1]);
+  const float base = __builtin_fmaxf(m, kLowest);
+  const float d = __builtin_fminf((base - __builtin_fmaxf(st.m, kLowest)) * c, 1e30f);
+  const float e = __builtin_amdgcn_exp2f(-d);
+  float s = st.s * e, t = (st.t - d * st.s) * e;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float x = (v[j] - base) * c;
+    const float p = __builtin_amdgcn_exp2f(x);
+    s += p;
+    t = __builtin_fmaf(p, __builtin_fmaxf(x, kFloor), t);
+  }
+  st.m = m;
+  st.s = s;
+  st.t = t;
+}
 
-// One workgroup a row; the alternatives one at a time, each the largest (value, lowest
-// index) after the one before.
+// What a row's statistics say.  A NaN or +infinity among the logits makes S NaN (infinity -
+// infinity); nothing but -infinity leaves S at 0.
+struct RowOut {
+  float mx, logs, ent;
+  bool bad, empty;
+};
+__device__ __forceinline__ RowOut row_out(const Stat& st) {
+  RowOut r;
+  r.bad = !(st.s == st.s) || st.m == INFINITY;
+  r.empty = !r.bad && st.m == -INFINITY;
+  r.mx = st.m;
+  r.logs = r.empty ? 0.0f : logf(st.s);
+  r.ent = r.empty ? 0.0f : r.logs - st.t / st.s * kLn2;
+  if (r.bad) r.mx = r.logs = r.ent = __uint_as_float(0x7FC00000u);
+  return r;
+}
+__device__ __forceinline__ float row_logprob(const RowOut& r, float z, float inv_t) {
+  return r.bad ? r.mx : r.empty ? -INFINITY : (z - r.mx) * inv_t - r.logs;
+}
+
+// Largest first, then the lower id.
+__device__ __forceinline__ bool before(float va, int ja, float vb, int jb) { return va > vb || (va == vb && ja < jb); }
+
 template <int DT>
-__global__ __launch_bounds__(kT) void tok_kernel(TokArgs a) {
+__device__ void write_row(const TokArgs& a, int64_t row, const RowOut& r) {
   typedef typename Elem<DT>::type E;
-  __shared__ float sh[kT / 64];
-  __shared__ int shi[kT / 64];
-  const int64_t row = blockIdx.x;
   const E* z = static_cast<const E*>(a.z) + row * a.ld;
-  const int V = (int)a.V;
-  float mx = -INFINITY;
-  int bad = 0;
-  for (int j = threadIdx.x; j < V; j += kT) {
-    const float v = elem_to_f32<DT>(z[j]);
-    bad |= !(v < INFINITY);
-    mx = fmaxf(mx, v);
-  }
-  bad = __syncthreads_or(bad);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kT / 64; ++i) mx = fmaxf(mx, sh[i]);
-  const bool empty = mx == -INFINITY;
-  if (empty) mx = 0.0f;
-  float S = 0.0f, D = 0.0f;
-  for (int j = threadIdx.x; j < V; j += kT) {
-    const float d = fmaxf((elem_to_f32<DT>(z[j]) - mx) * a.inv_t, kFloor);
-    const float e = __builtin_amdgcn_exp2f(d * kLog2e);
-    S += e;
-    D += e * d;
-  }
-  S = block_sum<kT>(S, sh);
-  D = block_sum<kT>(D, sh);
-  const float logs = logf(S);
+  a.ent[row] = r.ent;
+  a.stats[2 * row] = r.mx;
+  a.stats[2 * row + 1] = r.logs;
+  const int64_t t = a.targets[row];
   const float nan = __uint_as_float(0x7FC00000u);
-  if (threadIdx.x == 0) {
-    a.ent[row] = bad ? nan : empty ? 0.0f : logs - D / S;
-    a.stats[2 * row] = bad ? nan : empty ? -INFINITY : mx;
-    a.stats[2 * row + 1] = bad ? nan : empty ? 0.0f : logs;
-    const int64_t t = a.targets[row];
-    float lp;
-    if (t == a.ignore) lp = 0.0f;
-    else if (t < 0 || t >= V || bad) lp = nan;
-    else lp = empty ? -INFINITY : (elem_to_f32<DT>(z[t]) - mx) * a.inv_t - logs;
-    a.lp[row] = lp;
-  }
-  float last = INFINITY;
-  int last_j = -1;
-  for (int i = 0; i < a.top; ++i) {
-    float bv = -INFINITY;
-    int bj = 0x7FFFFFFF;
-    for (int j = threadIdx.x; j < V; j += kT) {
-      const float v = elem_to_f32<DT>(z[j]);
-      const bool after = v < last || (v == last && j > last_j);
-      if (after && (v > bv || (v == bv && j < bj))) {
-        bv = v;
-        bj = j;
-      }
-    }
+  a.lp[row] = t == a.ignore ? 0.0f : t < 0 || t >= a.V ? nan : row_logprob(r, elem_to_f32<DT>(z[t]), a.inv_t);
+}
+
+// One part of a row's results, for the joining launch: statistics, then `top` (logit, id)
+// pairs in order.
+struct Part {
+  Stat st;
+  float pad;
+};
+
+struct __attribute__((aligned(16))) TopShared {
+  float gm[kPairs];
+  float cv[kCand];  // logits above the threshold and their ids; then the result
+  int cj[kCand];
+  float tau;
+  int ng;                // logits above the threshold that were seen
+  uint8_t list[kPairs];  // pairs whose maximum reaches the threshold, in order
+  int tie[kMaxTop];
+  int wsum[kT / 64];
+};
+
+// The k-th largest (equal values count each) of the n values in v, by counting, to sh.tau;
+// n is a multiple of 4.  All threads call it.
+__device__ __forceinline__ void kth_largest(const float* v, int n, int k, TopShared& sh) {
+  const f32x4* v4 = reinterpret_cast<const f32x4*>(v);
+  for (int i = threadIdx.x; i < n; i += kT) {
+    const float x = v[i];
+    int above = 0, equal = 0;
+#pragma unroll 4
+    for (int j = 0; j < n / 4; ++j) {
+      const f32x4 o = v4[j];
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      const float pv = __shfl_xor(bv, o);
-      const int pj = __shfl_xor(bj, o);
-      if (pv > bv || (pv == bv && pj < bj)) {
-        bv = pv;
-        bj = pj;
+      for (int u = 0; u < 4; ++u) {
+        above += o[u] > x ? 1 : 0;
+        equal += o[u] == x ? 1 : 0;
+      }
+    }
+    if (above < k && above + equal >= k) sh.tau = x;  // every such thread writes the same value
+  }
+}
+
+// The `top` best (logit, id) pairs of the n logits from z, in order, to sh.cv / sh.cj [top]
+// (ids from z; past n: -infinity and INT_MAX).  tm: the maximum of the chunks that this
+// thread read.  Chunk ch (eight logits) was read by thread ch % kT.
+template <int DT>
+__device__ void top_of(const typename Elem<DT>::type* z, int n, int top, float tm, TopShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int chunks = (n + 7) >> 3, rounds = (chunks + kT - 1) / kT;
+  const float pm = fmaxf(tm, __shfl_xor(tm, 1));
+  __syncthreads();
+  if ((tid & 1) == 0) sh.gm[tid >> 1] = pm;
+  __syncthreads();
+  kth_largest(sh.gm, kPairs, top, sh);
+  __syncthreads();
+  for (;;) {
+    const float tau = sh.tau;
+    // the pairs to read again, in order (two waves' worth of flags)
+    const bool in = tid < kPairs && sh.gm[tid < kPairs ? tid : 0] >= tau;
+    const uint64_t mask = __ballot(in);
+    if (lane == 0) sh.wsum[wave] = __popcll(mask);
+    if (tid == 0) sh.ng = 0;
+    __syncthreads();
+    const int off = wave == 1 ? sh.wsum[0] : 0;
+    if (in) sh.list[off + __popcll(mask & ((1ull << lane) - 1))] = (uint8_t)tid;
+    const int nlist = 2 * (sh.wsum[0] + sh.wsum[1]);  // chunk columns: both threads of each pair
+    int nt = 0;
+    __syncthreads();
+    // chunk `f` in order of ids: round f / nlist, the list's column f % nlist
+    const int total = nlist * rounds;
+    for (int f0 = 0; f0 < total; f0 += kT) {
+      const int f = f0 + tid;
+      float v[8];
+      int j0 = n;
+      if (f < total) {
+        const int rd = f / nlist, col = f - rd * nlist;
+        j0 = (rd * kT + sh.list[col >> 1] * 2 + (col & 1)) * 8;
+      }
+      int ties = 0;
+      if (j0 + 8 <= n) widen8<DT>(load_raw8<DT>(z + j0), v);
+      else
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j0 + j < n ? elem_to_f32<DT>(z[j0 + j]) : __uint_as_float(0x7FC00000u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (v[j] > tau) {
+          const int at = atomicAdd(&sh.ng, 1);
+          if (at < kCand) {
+            sh.cv[at] = v[j];
+            sh.cj[at] = j0 + j;
+          }
+        }
+        ties += v[j] == tau ? 1 : 0;
+      }
+      // keep the first `top` equal ones: their places by a prefix sum over the workgroup
+      if (nt < top && __syncthreads_or(ties)) {
+        int run = ties;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+          const int p = __shfl_up(run, o);
+          if (lane >= o) run += p;
+        }
+        if (lane == 63) sh.wsum[wave] = run;
+        __syncthreads();
+        int at = nt + run - ties;
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < kT / 64; ++w) {
+          at += w < wave ? sh.wsum[w] : 0;
+          all += sh.wsum[w];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (v[j] == tau) {
+            if (at < top) sh.tie[at] = j0 + j;
+            ++at;
+          }
+        nt = min(top, nt + all);
       }
     }
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) {
-      sh[threadIdx.x >> 6] = bv;
-      shi[threadIdx.x >> 6] = bj;
-    }
-    __syncthreads();
-    for (int w = 0; w < kT / 64; ++w)
-      if (sh[w] > bv || (sh[w] == bv && shi[w] < bj)) {
-        bv = sh[w];
-        bj = shi[w];
+    const int ng = sh.ng;
+    if (ng <= kCand) {
+      // rank by counting; the order of the list does not matter (its last group of four is
+      // filled up with entries that come after every other)
+      if (tid < 3 && ng + tid < kCand) {
+        sh.cv[ng + tid] = -INFINITY;
+        sh.cj[ng + tid] = 0x7FFFFFFF;
       }
-    last = bv;
-    last_j = bj;
-    if (threadIdx.x == 0) {
-      a.top_ids[row * a.top + i] = bad ? -1 : bj;
-      a.top_lp[row * a.top + i] = bad ? nan : empty ? -INFINITY : (bv - mx) * a.inv_t - logs;
+      __syncthreads();
+      float v[kCand / kT];
+      int j[kCand / kT], rank[kCand / kT];
+#pragma unroll
+      for (int q = 0; q < kCand / kT; ++q) {
+        const int i = tid + q * kT;
+        rank[q] = kMaxTop;
+        if (i < ng) {
+          v[q] = sh.cv[i];
+          j[q] = sh.cj[i];
+          int r = 0;
+#pragma unroll 2
+          for (int o = 0; o < (ng + 3) / 4; ++o) {
+            const f32x4 ov = reinterpret_cast<const f32x4*>(sh.cv)[o];
+            const u32x4 oj = reinterpret_cast<const u32x4*>(sh.cj)[o];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) r += before(ov[u], (int)oj[u], v[q], j[q]) ? 1 : 0;
+          }
+          rank[q] = r;
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < kCand / kT; ++q)
+        if (rank[q] < top) {
+          sh.cv[rank[q]] = v[q];
+          sh.cj[rank[q]] = j[q];
+        }
+      for (int i = ng + tid; i < top; i += kT) {
+        const bool have = i - ng < nt;
+        sh.cv[i] = have ? tau : -INFINITY;
+        sh.cj[i] = have ? sh.tie[i - ng] : 0x7FFFFFFF;
+      }
+      __syncthreads();
+      return;
+    }
+    // Too many above the threshold (a few threads hold most large logits): the k-th largest of
+    // those held is a higher threshold that still k logits reach; read again with that one.
+    __syncthreads();
+    kth_largest(sh.cv, kCand, top, sh);
+    __syncthreads();
+  }
+}
+
+// One part of one row (parts == 1: a whole row, finished here).
+template <int DT>
+__global__ __launch_bounds__(kT) void tok_kernel(TokArgs a, int parts, int seg, Part* __restrict__ ps,
+                                                 float* __restrict__ pv, int* __restrict__ pj) {
+  typedef typename Elem<DT>::type E;
+  constexpr int kU = DT == W4_DT_F32 ? 2 : 4;  // chunks of eight a thread has in flight
+  __shared__ Stat ws[kT / 64];
+  __shared__ TopShared sh;
+  const int64_t row = blockIdx.x / (unsigned)parts;
+  const int part = blockIdx.x - (unsigned)row * parts;
+  const int tid = threadIdx.x;
+  const int j0 = part * seg;
+  const int n = min(seg, (int)a.V - j0);
+  const E* z = static_cast<const E*>(a.z) + row * a.ld + j0;
+  const float c = a.inv_t * kLog2e;
+  Stat st = {-INFINITY, 0.0f, 0.0f};
+  // whole groups, the next one's loads in flight during the present one's exponentials
+  const int groups = n / (kT * kU * 8);
+  const E* p = z + tid * 8;
+  Raw8<DT> next[kU];
+  if (groups > 0)
+#pragma unroll
+    for (int u = 0; u < kU; ++u) next[u] = load_raw8<DT>(p + u * kT * 8);
+  for (int g = 0; g < groups; ++g) {
+    float v[kU * 8];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      float w[8];
+      widen8<DT>(next[u], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[u * 8 + j] = w[j];
+    }
+    p += kT * kU * 8;
+    if (g + 1 < groups)
+#pragma unroll
+      for (int u = 0; u < kU; ++u) next[u] = load_raw8<DT>(p + u * kT * 8);
+    take(st, v, c);
+  }
+  // the rest, chunk by chunk; logits past the end count as masked
+  for (int j = groups * kT * kU * 8 + tid * 8; j < n; j += kT * 8) {
+    float w[8];
+    const uint32_t masked = DT == W4_DT_F32 ? 0xFF800000u : DT == W4_DT_F16 ? 0xFC00u : 0xFF80u;
+    widen8<DT>(j + 8 <= n ? load_raw8<DT>(z + j) : load_raw8_part<DT>(z + j, n - j, masked), w);
+    take(st, w, c);
+  }
+  const float tm = st.m;
+  st = wave_join(st, c);
+  if ((tid & 63) == 0) ws[tid >> 6] = st;
+  __syncthreads();
+  st = ws[0];
+#pragma unroll
+  for (int w = 1; w < kT / 64; ++w) st = join(st, ws[w], c);
+  const RowOut r = row_out(st);
+  if (parts == 1) {
+    if (tid == 0) write_row<DT>(a, row, r);
+    if (a.top == 0) return;
+    if (!r.bad) top_of<DT>(z, n, a.top, tm, sh);
+    if (tid < a.top) {
+      a.top_lp[row * a.top + tid] = r.bad ? r.mx : row_logprob(r, sh.cv[tid], a.inv_t);
+      a.top_ids[row * a.top + tid] = r.bad ? -1 : sh.cj[tid];
+    }
+  } else {
+    if (tid == 0) ps[blockIdx.x].st = st;
+    if (a.top == 0 || r.bad) return;
+    top_of<DT>(z, n, a.top, tm, sh);
+    if (tid < a.top) {
+      pv[(size_t)blockIdx.x * a.top + tid] = sh.cv[tid];
+      pj[(size_t)blockIdx.x * a.top + tid] = sh.cj[tid] == 0x7FFFFFFF ? 0x7FFFFFFF : j0 + sh.cj[tid];
     }
   }
 }
 
+// Joins a row's parts: the statistics with one lane a part, then the alternatives as a merge
+// of the parts' sorted lists, read into LDS by the workgroup and merged by its first wave.
+// The parts are in order of ids, so of equal heads the lowest lane's goes first; a list that
+// has run out holds NaN, which no maximum takes.
 template <int DT>
-__device__ __forceinline__ typename Elem<DT>::type from_f32(float v) {
-  if constexpr (DT == W4_DT_F32) return v;
-  else if constexpr (DT == W4_DT_F16) return f32_to_f16_bits(v);
-  else return (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+__global__ __launch_bounds__(kT) void tok_join_kernel(TokArgs a, int parts, const Part* __restrict__ ps,
+                                                      const float* __restrict__ pv, const int* __restrict__ pj) {
+  extern __shared__ float lists[];  // [parts][top] logits, then ids
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const float c = a.inv_t * kLog2e;
+  const int n = parts * a.top;
+  int* ids = reinterpret_cast<int*>(lists + n);
+  Stat st = {-INFINITY, 0.0f, 0.0f};
+  if (lane < parts) st = ps[(size_t)row * parts + lane].st;
+  for (int i = tid; i < n; i += kT) {
+    const int j = pj[(size_t)row * n + i];
+    lists[i] = j == 0x7FFFFFFF ? __uint_as_float(0x7FC00000u) : pv[(size_t)row * n + i];
+    ids[i] = j;
+  }
+  const RowOut r = row_out(wave_join(st, c));
+  __syncthreads();
+  if (tid >= 64) return;
+  if (lane == 0) write_row<DT>(a, row, r);
+  if (a.top == 0) return;
+  float keep_v = r.mx;
+  int keep_j = -1;
+  if (!r.bad) {
+    const float nan = __uint_as_float(0x7FC00000u);
+    int at = lane * a.top;
+    const int end = lane < parts ? at + a.top : at;
+    float v = at < end ? lists[at] : nan;
+    for (int i = 0; i < a.top; ++i) {
+      const float m = wave_max(__builtin_fmaxf(v, -INFINITY));  // NaN counts as -infinity here
+      const int win = __ffsll((unsigned long long)__ballot(v == m)) - 1;
+      if (lane == i) keep_v = m;
+      const int j = win >= 0 ? ids[__builtin_amdgcn_readlane(at, win)] : -1;
+      if (lane == i) keep_j = j;
+      if (lane == win) {
+        ++at;
+        v = at < end ? lists[at] : nan;
+      }
+    }
+  }
+  if (lane < a.top) {
+    a.top_lp[row * a.top + lane] = r.bad ? r.mx : row_logprob(r, keep_v, a.inv_t);
+    a.top_ids[row * a.top + lane] = keep_j;
+  }
+}
+
+// Eight results as the logits' type, one store (two for fp32) at the element's alignment.
+template <int DT>
+__device__ __forceinline__ void store8(typename Elem<DT>::type* p, const float (&d)[8]) {
+  typedef typename Elem<DT>::loose loose;
+  u32x4 q[DT == W4_DT_F32 ? 2 : 1];
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    if constexpr (DT == W4_DT_F32) {
+      q[j >> 2][j & 3] = __float_as_uint(d[j]);
+      q[j >> 2][(j & 3) + 1] = __float_as_uint(d[j + 1]);
+    } else {
+      q[0][j >> 1] = DT == W4_DT_F16 ? pack_f16x2(d[j], d[j + 1]) : pack_bf16x2(d[j], d[j + 1]);
+    }
+  }
+  *reinterpret_cast<loose*>(p) = q[0];
+  if constexpr (DT == W4_DT_F32) *reinterpret_cast<loose*>(p + 4) = q[1];
 }
 
 template <int DT>
-__global__ __launch_bounds__(kT) void tok_grad_kernel(TokGradArgs a) {
+__device__ __forceinline__ void store1(typename Elem<DT>::type* p, float d) {
+  if constexpr (DT == W4_DT_F32) *p = d;
+  else if constexpr (DT == W4_DT_F16) *p = f32_to_f16_bits(d);
+  else *p = (uint16_t)(pack_bf16x2(d, 0.0f) & 0xFFFFu);
+}
+
+// Gradient of one part of a row: dz_j = -p_j (A + B log2 p_j) / T at every logit, with
+// log2 p_j = (z_j - mx) c - L, then the few logits that have a gradient of their own (the
+// target and the alternatives) written once more by the same workgroup.  Their logits are
+// read before the part is written, so dz may be z.
+template <int DT>
+__global__ __launch_bounds__(kT) void tok_grad_kernel(TokGradArgs a, int parts, int seg) {
   typedef typename Elem<DT>::type E;
-  const int64_t row = blockIdx.x;
-  const E* z = static_cast<const E*>(a.z) + row * a.ld;
-  E* dz = static_cast<E*>(a.dz) + row * a.ldd;
-  const int V = (int)a.V;
+  constexpr int kU = DT == W4_DT_F32 ? 2 : 4;
+  __shared__ float av[kMaxTop];
+  __shared__ int aj[kMaxTop];
+  const int64_t row = blockIdx.x / (unsigned)parts;
+  const int part = blockIdx.x - (unsigned)row * parts;
+  const int tid = threadIdx.x;
+  const int j0 = part * seg;
+  const int n = min(seg, (int)a.V - j0);
+  const E* z = static_cast<const E*>(a.z) + row * a.ld + j0;
+  E* dz = static_cast<E*>(a.dz) + row * a.ldd + j0;
   const float mx = a.stats[2 * row], logs = a.stats[2 * row + 1], ent = a.ent[row];
   const int64_t t = a.targets[row];
-  const bool has_t = t != a.ignore && t >= 0 && t < V;
+  const bool has_t = t != a.ignore && t >= 0 && t < a.V;
   const float g = has_t && a.g != nullptr ? a.g[row] : 0.0f;
   const float h = a.h != nullptr ? a.h[row] : 0.0f;
-  float all = g;
-  if (a.a != nullptr)
-    for (int i = 0; i < a.top; ++i) all += a.a[row * a.top + i];
-  for (int j = threadIdx.x; j < V; j += kT) {
-    float d = 0.0f;
-    if (mx != -INFINITY) {
-      const float r = fmaxf((elem_to_f32<DT>(z[j]) - mx) * a.inv_t - logs, kFloor);
-      d = -__builtin_amdgcn_exp2f(r * kLog2e) * (all + h * (r + ent));
-      if (has_t && j == t) d += g;
-      if (a.a != nullptr)
-        for (int i = 0; i < a.top; ++i)
-          if (a.top_ids[row * a.top + i] == j) d += a.a[row * a.top + i];
-      d *= a.inv_t;
-      if (mx != mx) d = mx;
-    }
-    dz[j] = from_f32<DT>(d);
+  const int top = a.a != nullptr ? a.top : 0;
+  if (tid < top) {
+    av[tid] = a.a[row * a.top + tid];
+    aj[tid] = (int)a.top_ids[row * a.top + tid];
   }
+  __syncthreads();
+  float all = g;
+  for (int i = 0; i < top; ++i) all += av[i];
+  const bool empty = mx == -INFINITY;
+  const float nan = mx != mx ? mx : 0.0f;  // a row that scored NaN has NaN gradients
+  const float base = empty ? 0.0f : mx;
+  const float c = a.inv_t * kLog2e, L = logs * kLog2e;
+  // all + h (log p + ent), in units of log2 p, over T; an empty row has none
+  const float A = empty ? 0.0f : (all + h * ent) * a.inv_t + nan, B = empty ? 0.0f : h * kLn2 * a.inv_t;
+  auto at = [&](float v) {
+    const float x = __builtin_fmaxf((v - base) * c - L, kFloor);
+    return -__builtin_amdgcn_exp2f(x) * __builtin_fmaf(B, x, A);
+  };
+  // this thread's special logit, if it lies in this part: the target (thread 0) with what the
+  // alternatives add to it, or an alternative that is not the target
+  int sj = -1;
+  float sg = 0.0f;
+  if (tid == 0 && has_t) {
+    sj = (int)t;
+    sg = g;
+    for (int i = 0; i < top; ++i) sg += aj[i] == sj ? av[i] : 0.0f;
+  } else if (tid > 0 && tid <= top && !(has_t && aj[tid - 1] == t)) {
+    sj = aj[tid - 1];
+    sg = av[tid - 1];
+  }
+  sj -= j0;
+  const bool special = sj >= 0 && sj < n && !empty;
+  const float sz = special ? elem_to_f32<DT>(z[sj]) : 0.0f;
+  __syncthreads();
+  const int groups = n / (kT * kU * 8);
+  const E* p = z + tid * 8;
+  E* q = dz + tid * 8;
+  Raw8<DT> next[kU];
+  if (groups > 0)
+#pragma unroll
+    for (int u = 0; u < kU; ++u) next[u] = load_raw8<DT>(p + u * kT * 8);
+  for (int i = 0; i < groups; ++i) {
+    Raw8<DT> now[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) now[u] = next[u];
+    p += kT * kU * 8;
+    if (i + 1 < groups)
+#pragma unroll
+      for (int u = 0; u < kU; ++u) next[u] = load_raw8<DT>(p + u * kT * 8);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      float w[8], d[8];
+      widen8<DT>(now[u], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = at(w[j]);
+      store8<DT>(q + u * kT * 8, d);
+    }
+    q += kT * kU * 8;
+  }
+  for (int j = groups * kT * kU * 8 + tid * 8; j < n; j += kT * 8) {
+    if (j + 8 <= n) {
+      float w[8], d[8];
+      widen8<DT>(load_raw8<DT>(z + j), w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = at(w[i]);
+      store8<DT>(dz + j, d);
+    } else {
+      for (int i = j; i < n; ++i) store1<DT>(dz + i, at(elem_to_f32<DT>(z[i])));
+    }
+  }
+  __syncthreads();
+  if (special) store1<DT>(dz + sj, at(sz) + sg * a.inv_t);
 }
+
+// Parts of a row: one when the rows alone fill the device eight workgroups deep, else enough
+// to come near that, of at least one chunk a thread (the launch that joins them takes one
+// lane a part).
+int parts_of(int64_t M, int64_t V, const DeviceCaps& caps, int most) {
+  const int64_t want = (int64_t)caps.cus * 8;
+  int64_t p = M >= want / 2 ? 1 : want / M;
+  p = std::min<int64_t>(p, std::max<int64_t>(1, V / kMinSeg));
+  return (int)std::min<int64_t>(p, most);
+}
+// Columns of a part: whole chunks, so that parts of aligned rows are aligned.
+int seg_of(int64_t V, int parts) { return (int)(((V + parts - 1) / parts + 63) / 64 * 64); }
 
 }  // namespace
 
-size_t tok_ws_bytes(int64_t, int64_t, int, const DeviceCaps&) { return 0; }
+size_t tok_ws_bytes(int64_t M, int64_t V, int top, const DeviceCaps& caps) {
+  const int parts = parts_of(M, V, caps, kMaxParts);
+  return parts == 1 ? 0 : (size_t)M * parts * (sizeof(Part) + 8 * (size_t)top);
+}
 
-hipError_t launch_tok(const TokArgs& a, const DeviceCaps&, void*, hipStream_t st) {
-  const unsigned g = (unsigned)a.M;
+hipError_t launch_tok(const TokArgs& a, const DeviceCaps& caps, void* ws, hipStream_t st) {
+  int parts = parts_of(a.M, a.V, caps, kMaxParts);
+  const int seg = seg_of(a.V, parts);
+  Part* ps = static_cast<Part*>(ws);
+  float* pv = reinterpret_cast<float*>(ps + (size_t)a.M * parts);
+  parts = (int)((a.V + seg - 1) / seg);  // rounding the columns up may leave fewer
+  int* pj = reinterpret_cast<int*>(pv + (size_t)a.M * parts * a.top);
+  const unsigned g = (unsigned)(a.M * parts);
   switch (a.dt) {
-    case W4_DT_F32: tok_kernel<W4_DT_F32><<<g, kT, 0, st>>>(a); break;
-    case W4_DT_F16: tok_kernel<W4_DT_F16><<<g, kT, 0, st>>>(a); break;
-    default: tok_kernel<W4_DT_BF16><<<g, kT, 0, st>>>(a); break;
+    case W4_DT_F32: tok_kernel<W4_DT_F32><<<g, kT, 0, st>>>(a, parts, seg, ps, pv, pj); break;
+    case W4_DT_F16: tok_kernel<W4_DT_F16><<<g, kT, 0, st>>>(a, parts, seg, ps, pv, pj); break;
+    default: tok_kernel<W4_DT_BF16><<<g, kT, 0, st>>>(a, parts, seg, ps, pv, pj); break;
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || parts == 1) return e;
+  const size_t lds = (size_t)parts * a.top * 8;  // at most 64 x 64 pairs: 32 KB
+  switch (a.dt) {
+    case W4_DT_F32: tok_join_kernel<W4_DT_F32><<<(unsigned)a.M, kT, lds, st>>>(a, parts, ps, pv, pj); break;
+    case W4_DT_F16: tok_join_kernel<W4_DT_F16><<<(unsigned)a.M, kT, lds, st>>>(a, parts, ps, pv, pj); break;
+    default: tok_join_kernel<W4_DT_BF16><<<(unsigned)a.M, kT, lds, st>>>(a, parts, ps, pv, pj); break;
   }
   return hipGetLastError();
 }
 
-hipError_t launch_tok_grad(const TokGradArgs& a, const DeviceCaps&, hipStream_t st) {
-  const unsigned g = (unsigned)a.M;
+hipError_t launch_tok_grad(const TokGradArgs& a, const DeviceCaps& caps, hipStream_t st) {
+  int parts = parts_of(a.M, a.V, caps, 1 << 20);
+  const int seg = seg_of(a.V, parts);
+  parts = (int)((a.V + seg - 1) / seg);
+  const unsigned g = (unsigned)(a.M * parts);
   switch (a.dt) {
-    case W4_DT_F32: tok_grad_kernel<W4_DT_F32><<<g, kT, 0, st>>>(a); break;
-    case W4_DT_F16: tok_grad_kernel<W4_DT_F16><<<g, kT, 0, st>>>(a); break;
-    default: tok_grad_kernel<W4_DT_BF16><<<g, kT, 0, st>>>(a); break;
+    case W4_DT_F32: tok_grad_kernel<W4_DT_F32><<<g, kT, 0, st>>>(a, parts, seg); break;
+    case W4_DT_F16: tok_grad_kernel<W4_DT_F16><<<g, kT, 0, st>>>(a, parts, seg); break;
+    default: tok_grad_kernel<W4_DT_BF16><<<g, kT, 0, st>>>(a, parts, seg); break;
   }
   return hipGetLastError();
 }
