@@ -115,6 +115,7 @@ int w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K, int x_dtype, size_t* b
   if (!bytes) return fail(W4_ERR_INVALID, "bytes is NULL");
   if (x_dtype >= 0 && !is_dtype(x_dtype)) return fail(W4_ERR_INVALID, "x_dtype = %d is unknown", x_dtype);
   if (M == 0) *bytes = 0;
+  else if (x_dtype >= 0 && w4::w8_fused(M, K)) *bytes = 0;
   else if (x_dtype < 0) *bytes = w4::w8_mm_workspace_bytes(M, N, K, device_caps());
   else *bytes = linear_ws(M, N, K).total;
   return ok();
@@ -159,6 +160,20 @@ int w8a8_linear(const void* X, int x_dtype, int64_t ldx, int64_t M, const int8_t
   s = check_weight(W, w_scales);
   if (s == W4_OK) s = check_ws(ws);
   if (s != W4_OK) return s;
+  if (w4::w8_fused(M, K)) {
+    w4::W8Args a = {};
+    a.X = X;
+    a.x_dt = x_dtype;
+    a.ldx = ldx;
+    a.W = W;
+    a.w_scales = w_scales;
+    a.ep = ep;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.pitch = pitch_of(K);
+    return launched(w4::launch_w8_decode(a, device_caps(), static_cast<hipStream_t>(stream)), "w8a8_linear");
+  }
   const LinearWs l = linear_ws(M, N, K);
   if (ws == nullptr || ws_bytes < l.total)
     return fail(W4_ERR_RESOURCE, "w8a8_linear needs a workspace of %zu bytes (got %zu)", l.total,

@@ -137,6 +137,10 @@ struct W8Args {
 size_t w8_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps);
 const char* w8_mm_name(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps);
 hipError_t launch_w8_mm(const W8Args& a, const DeviceCaps& caps, void* ws, size_t ws_bytes, hipStream_t st);
+// Few tokens (w8_decode.hip); w8_fused: float tokens are quantized inside that launch.
+bool w8_fused(int64_t M, int64_t K);
+bool w8_decode_supported(int64_t M);
+hipError_t launch_w8_decode(const W8Args& a, const DeviceCaps& caps, hipStream_t st);
 
 // dY [M][N] 16-bit, row stride ld -> out [M][npad], zeros past column N.
 hipError_t launch_pad_rows(const uint16_t* dY, int64_t M, int64_t N, int64_t ld, uint16_t* out, int64_t npad,

@@ -33,11 +33,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void quantize_rows_kernel(co
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) m = absmax8<DT>(r[c], m);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const uint32_t p = __shfl_xor(m, o);
-    m = p > m ? p : m;
-  }
+  m = wave_umax(m);
   if constexpr (TPR > 64) {
     __shared__ uint32_t part[TPR / 64];
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
@@ -74,11 +70,7 @@ __global__ __launch_bounds__(1024) void quantize_long_rows_kernel(const void* __
   };
   uint32_t m = 0;
   for (int col = threadIdx.x * 8; col < cols; col += 8192) m = absmax8<DT>(load(col), m);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const uint32_t p = __shfl_xor(m, o);
-    m = p > m ? p : m;
-  }
+  m = wave_umax(m);
   __shared__ uint32_t part[16];
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
   __syncthreads();
