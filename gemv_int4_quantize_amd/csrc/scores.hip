@@ -11,11 +11,12 @@
 // results a second, one-wave launch joins, when there are few rows.
 //
 // Alternatives: the maxima of 128 pairs of threads are on hand after the pass, and the k-th
-// largest of them is a threshold that at least k logits reach, while only the chunks of
-// those pairs can hold one that does.  These few chunks are read again (from cache).
-// Logits above the threshold are collected and ranked by counting; of those equal to it the
-// lowest ids are kept, in order.  So rows with many equal logits, or with fewer unmasked
-// logits than alternatives, cost the same few chunks.
+// largest of them is a threshold that at least k logits reach.  Each thread has also kept the
+// maximum of each of (up to) 16 runs of its chunks, so that only the few runs that reach the
+// threshold are read again; what reaches it in them is ranked by counting.  (Reading all of
+// the pairs' chunks again cost 17 us of 112 at M = 2048, V = 128256 bf16.)  Rows with too many
+// logits at the threshold (many equal ones, or fewer unmasked than alternatives) collect
+// those above it, and of those equal to it the lowest ids in order, from the pairs' chunks.
 #include <algorithm>
 
 #include "api_common.h"
@@ -34,10 +35,11 @@ constexpr float kFloor = -1.0e4f;
 
 constexpr int kT = 256;       // threads
 constexpr int kPairs = kT / 2;
+constexpr int kRuns = 16;     // runs of a thread's chunks whose maxima are kept
 constexpr int kMaxTop = 64;
 constexpr int kCand = 1024;   // logits above the threshold that are held at a time
 constexpr int kMaxParts = 64; // parts of a row, one per lane of the joining wave
-constexpr int kMinSeg = kT * 8;
+constexpr int kMinSeg = kT * 32;  // measured against 8 and 16 a thread: 16 rows, top 20, 19.4 -> 16.4 us
 
 // Running softmax statistics: the largest logit, S and sum e^d d (in units of log2) relative
 // to it.  m is -infinity while only masked logits were seen.
@@ -67,12 +69,14 @@ __device__ __forceinline__ Stat wave_join(Stat st, float c) {
   return st;
 }
 
-// One group of N logits into the running statistics.
+// One group of N logits into the running statistics; their maximum is joined to `run`.
 template <int N>
-__device__ __forceinline__ void take(Stat& st, const float (&v)[N], float c) {
-  float m = st.m;
+__device__ __forceinline__ void take(Stat& st, const float (&v)[N], float c, float& run) {
+  float m = v[0];
 #pragma unroll
-  for (int j = 0; j < N; j += 2) m = __builtin_fmaxf(__builtin_fmaxf(m, v[j]), v[j + 1]);
+  for (int j = 1; j < N; j += 2) m = __builtin_fmaxf(__builtin_fmaxf(m, v[j]), v[j + 1 < N ? j + 1 : j]);
+  run = __builtin_fmaxf(run, m);
+  m = __builtin_fmaxf(m, st.m);
   const float base = __builtin_fmaxf(m, kLowest);
   const float d = __builtin_fminf((base - __builtin_fmaxf(st.m, kLowest)) * c, 1e30f);
   const float e = __builtin_amdgcn_exp2f(-d);
@@ -112,16 +116,27 @@ __device__ __forceinline__ float row_logprob(const RowOut& r, float z, float inv
 // Largest first, then the lower id.
 __device__ __forceinline__ bool before(float va, int ja, float vb, int jb) { return va > vb || (va == vb && ja < jb); }
 
+// A row's target and its logit, read early: the two loads depend on one another.
+struct Target {
+  int64_t t;
+  float z;
+};
 template <int DT>
-__device__ void write_row(const TokArgs& a, int64_t row, const RowOut& r) {
+__device__ __forceinline__ Target load_target(const TokArgs& a, int64_t row) {
   typedef typename Elem<DT>::type E;
-  const E* z = static_cast<const E*>(a.z) + row * a.ld;
+  Target r;
+  r.t = a.targets[row];
+  const bool in = r.t >= 0 && r.t < a.V;
+  r.z = elem_to_f32<DT>((static_cast<const E*>(a.z) + row * a.ld)[in ? r.t : 0]);
+  return r;
+}
+
+__device__ __forceinline__ void write_row(const TokArgs& a, int64_t row, const RowOut& r, const Target& t) {
   a.ent[row] = r.ent;
   a.stats[2 * row] = r.mx;
   a.stats[2 * row + 1] = r.logs;
-  const int64_t t = a.targets[row];
   const float nan = __uint_as_float(0x7FC00000u);
-  a.lp[row] = t == a.ignore ? 0.0f : t < 0 || t >= a.V ? nan : row_logprob(r, elem_to_f32<DT>(z[t]), a.inv_t);
+  a.lp[row] = t.t == a.ignore ? 0.0f : t.t < 0 || t.t >= a.V ? nan : row_logprob(r, t.z, a.inv_t);
 }
 
 // One part of a row's results, for the joining launch: statistics, then `top` (logit, id)
@@ -131,12 +146,21 @@ struct Part {
   float pad;
 };
 
+// A float's upper half, rounded towards +infinity: not below the float, and the float itself
+// for bf16 values.
+__device__ __forceinline__ uint16_t up16(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return (uint16_t)((u + (u >> 31 ? 0u : 0xFFFFu)) >> 16);
+}
+
 struct __attribute__((aligned(16))) TopShared {
   float gm[kPairs];
   float cv[kCand];  // logits above the threshold and their ids; then the result
   int cj[kCand];
   float tau;
   int ng;                // logits above the threshold that were seen
+  int nl;                // entries of runs
+  uint16_t runs[kT];     // runs to read again: run * kT + thread
   uint8_t list[kPairs];  // pairs whose maximum reaches the threshold, in order
   int tie[kMaxTop];
   int wsum[kT / 64];
@@ -162,19 +186,141 @@ __device__ __forceinline__ void kth_largest(const float* v, int n, int k, TopSha
   }
 }
 
+// The same of the kPairs pair maxima, to sh.tau.  For small k one wave takes the largest off
+// until k are gone: less work in all than counting, which tells where every workgroup of a CU
+// does this at about the same time.  Larger k count, two threads a value: 20 rounds of the
+// former took 4 us of a launch for few rows.
+__device__ __forceinline__ void kth_pair(int k, TopShared& sh) {
+  const int tid = threadIdx.x;
+  if (k > 8) {
+    const float x = sh.gm[tid >> 1];
+    const f32x4* v4 = reinterpret_cast<const f32x4*>(sh.gm) + (tid & 1) * (kPairs / 8);
+    int n = 0;  // values above x, and equal ones in the upper half
+#pragma unroll
+    for (int j = 0; j < kPairs / 8; ++j) {
+      const f32x4 o = v4[j];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) n += o[u] > x ? 1 : o[u] == x ? 0x10000 : 0;
+    }
+    n += __shfl_xor(n, 1);
+    const int above = n & 0xFFFF;
+    if (above < k && above + (n >> 16) >= k) sh.tau = x;
+    return;
+  }
+  if (tid >= 64) return;
+  const float nan = __uint_as_float(0x7FC00000u);
+  float a = sh.gm[tid], b = sh.gm[tid + 64];
+  for (;;) {
+    const float m = wave_max(__builtin_fmaxf(__builtin_fmaxf(a, b), -INFINITY));
+    k -= __popcll(__ballot(a == m)) + __popcll(__ballot(b == m));
+    if (k <= 0) {
+      if (tid == 0) sh.tau = m;
+      return;
+    }
+    a = a == m ? nan : a;
+    b = b == m ? nan : b;
+  }
+}
+
+// The `top` best of the ng (<= kCand) pairs in sh.cv / sh.cj, in order, to their front: ranked by
+// counting, in any order (the last group of four is filled up with pairs that come after
+// every other).  Entries past ng are left to the caller.
+__device__ __forceinline__ void rank_top(int ng, int top, TopShared& sh) {
+  const int tid = threadIdx.x;
+  if (tid < 3 && ng + tid < kCand) {
+    sh.cv[ng + tid] = -INFINITY;
+    sh.cj[ng + tid] = 0x7FFFFFFF;
+  }
+  __syncthreads();
+  float v[kCand / kT];
+  int j[kCand / kT], rank[kCand / kT];
+#pragma unroll
+  for (int q = 0; q < kCand / kT; ++q) {
+    const int i = tid + q * kT;
+    rank[q] = kMaxTop;
+    if (i < ng) {
+      v[q] = sh.cv[i];
+      j[q] = sh.cj[i];
+      int r = 0;
+#pragma unroll 2
+      for (int o = 0; o < (ng + 3) / 4; ++o) {
+        const f32x4 ov = reinterpret_cast<const f32x4*>(sh.cv)[o];
+        const u32x4 oj = reinterpret_cast<const u32x4*>(sh.cj)[o];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) r += before(ov[u], (int)oj[u], v[q], j[q]) ? 1 : 0;
+      }
+      rank[q] = r;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kCand / kT; ++q)
+    if (rank[q] < top) {
+      sh.cv[rank[q]] = v[q];
+      sh.cj[rank[q]] = j[q];
+    }
+}
+
 // The `top` best (logit, id) pairs of the n logits from z, in order, to sh.cv / sh.cj [top]
 // (ids from z; past n: -infinity and INT_MAX).  tm: the maximum of the chunks that this
-// thread read.  Chunk ch (eight logits) was read by thread ch % kT.
+// thread read.  Chunk ch (eight logits) was read by thread ch % kT; run r of a thread is its
+// `width` chunks from r * width on, with the (rounded up) maximum rmax[r][thread].
 template <int DT>
-__device__ void top_of(const typename Elem<DT>::type* z, int n, int top, float tm, TopShared& sh) {
+__device__ void top_of(const typename Elem<DT>::type* z, int n, int top, float tm, const uint16_t (*rmax)[kT], int nruns,
+                       int width, TopShared& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int chunks = (n + 7) >> 3, rounds = (chunks + kT - 1) / kT;
   const float pm = fmaxf(tm, __shfl_xor(tm, 1));
   __syncthreads();
   if ((tid & 1) == 0) sh.gm[tid >> 1] = pm;
+  if (tid == 0) sh.nl = sh.ng = 0;
   __syncthreads();
-  kth_largest(sh.gm, kPairs, top, sh);
+  kth_pair(top, sh);
   __syncthreads();
+  {
+    const float tau = sh.tau;
+    if (tm >= tau)
+      for (int r = 0; r < nruns; ++r)
+        if (__uint_as_float((uint32_t)rmax[r][tid] << 16) >= tau) {
+          const int at = atomicAdd(&sh.nl, 1);
+          if (at < kT) sh.runs[at] = (uint16_t)(r * kT + tid);
+        }
+    __syncthreads();
+    const int nl = sh.nl;
+    if (nl <= kT) {
+      for (int f = tid; f < nl * width; f += kT) {
+        const int e = f / width, run = sh.runs[e];
+        const int j0 = (((run / kT) * width + f - e * width) * kT + run % kT) * 8;
+        float v[8];
+        if (j0 + 8 <= n) widen8<DT>(load_raw8<DT>(z + j0), v);
+        else
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = j0 + j < n ? elem_to_f32<DT>(z[j0 + j]) : __uint_as_float(0x7FC00000u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (v[j] >= tau) {
+            const int at = atomicAdd(&sh.ng, 1);
+            if (at < kCand) {
+              sh.cv[at] = v[j];
+              sh.cj[at] = j0 + j;
+            }
+          }
+      }
+      __syncthreads();
+      const int ng = sh.ng;
+      if (ng <= kCand) {
+        rank_top(ng, top, sh);
+        // fewer only where the part has fewer logits
+        for (int i = ng + tid; i < top; i += kT) {
+          sh.cv[i] = -INFINITY;
+          sh.cj[i] = 0x7FFFFFFF;
+        }
+        __syncthreads();
+        return;
+      }
+    }
+    __syncthreads();
+  }
   for (;;) {
     const float tau = sh.tau;
     // the pairs to read again, in order (two waves' worth of flags)
@@ -243,40 +389,7 @@ __device__ void top_of(const typename Elem<DT>::type* z, int n, int top, float t
     __syncthreads();
     const int ng = sh.ng;
     if (ng <= kCand) {
-      // rank by counting; the order of the list does not matter (its last group of four is
-      // filled up with entries that come after every other)
-      if (tid < 3 && ng + tid < kCand) {
-        sh.cv[ng + tid] = -INFINITY;
-        sh.cj[ng + tid] = 0x7FFFFFFF;
-      }
-      __syncthreads();
-      float v[kCand / kT];
-      int j[kCand / kT], rank[kCand / kT];
-#pragma unroll
-      for (int q = 0; q < kCand / kT; ++q) {
-        const int i = tid + q * kT;
-        rank[q] = kMaxTop;
-        if (i < ng) {
-          v[q] = sh.cv[i];
-          j[q] = sh.cj[i];
-          int r = 0;
-#pragma unroll 2
-          for (int o = 0; o < (ng + 3) / 4; ++o) {
-            const f32x4 ov = reinterpret_cast<const f32x4*>(sh.cv)[o];
-            const u32x4 oj = reinterpret_cast<const u32x4*>(sh.cj)[o];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) r += before(ov[u], (int)oj[u], v[q], j[q]) ? 1 : 0;
-          }
-          rank[q] = r;
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int q = 0; q < kCand / kT; ++q)
-        if (rank[q] < top) {
-          sh.cv[rank[q]] = v[q];
-          sh.cj[rank[q]] = j[q];
-        }
+      rank_top(ng, top, sh);
       for (int i = ng + tid; i < top; i += kT) {
         const bool have = i - ng < nt;
         sh.cv[i] = have ? tau : -INFINITY;
@@ -301,6 +414,7 @@ __global__ __launch_bounds__(kT) void tok_kernel(TokArgs a, int parts, int seg, 
   constexpr int kU = DT == W4_DT_F32 ? 2 : 4;  // chunks of eight a thread has in flight
   __shared__ Stat ws[kT / 64];
   __shared__ TopShared sh;
+  __shared__ uint16_t rmax[kRuns][kT];
   const int64_t row = blockIdx.x / (unsigned)parts;
   const int part = blockIdx.x - (unsigned)row * parts;
   const int tid = threadIdx.x;
@@ -309,8 +423,13 @@ __global__ __launch_bounds__(kT) void tok_kernel(TokArgs a, int parts, int seg, 
   const E* z = static_cast<const E*>(a.z) + row * a.ld + j0;
   const float c = a.inv_t * kLog2e;
   Stat st = {-INFINITY, 0.0f, 0.0f};
+  Target target = {0, 0.0f};
+  if (parts == 1 && tid == 0) target = load_target<DT>(a, row);
   // whole groups, the next one's loads in flight during the present one's exponentials
   const int groups = n / (kT * kU * 8);
+  const int gpr = (groups + kRuns) / kRuns;  // groups a run (the rest counts as one)
+  float run = -INFINITY;
+  int left = gpr, r_at = 0;
   const E* p = z + tid * 8;
   Raw8<DT> next[kU];
   if (groups > 0)
@@ -329,15 +448,21 @@ __global__ __launch_bounds__(kT) void tok_kernel(TokArgs a, int parts, int seg, 
     if (g + 1 < groups)
 #pragma unroll
       for (int u = 0; u < kU; ++u) next[u] = load_raw8<DT>(p + u * kT * 8);
-    take(st, v, c);
+    take(st, v, c, run);
+    if (--left == 0) {
+      rmax[r_at++][tid] = up16(run);
+      run = -INFINITY;
+      left = gpr;
+    }
   }
   // the rest, chunk by chunk; logits past the end count as masked
   for (int j = groups * kT * kU * 8 + tid * 8; j < n; j += kT * 8) {
     float w[8];
     const uint32_t masked = DT == W4_DT_F32 ? 0xFF800000u : DT == W4_DT_F16 ? 0xFC00u : 0xFF80u;
     widen8<DT>(j + 8 <= n ? load_raw8<DT>(z + j) : load_raw8_part<DT>(z + j, n - j, masked), w);
-    take(st, w, c);
+    take(st, w, c, run);
   }
+  rmax[r_at][tid] = up16(run);
   const float tm = st.m;
   st = wave_join(st, c);
   if ((tid & 63) == 0) ws[tid >> 6] = st;
@@ -347,9 +472,9 @@ __global__ __launch_bounds__(kT) void tok_kernel(TokArgs a, int parts, int seg, 
   for (int w = 1; w < kT / 64; ++w) st = join(st, ws[w], c);
   const RowOut r = row_out(st);
   if (parts == 1) {
-    if (tid == 0) write_row<DT>(a, row, r);
+    if (tid == 0) write_row(a, row, r, target);
     if (a.top == 0) return;
-    if (!r.bad) top_of<DT>(z, n, a.top, tm, sh);
+    if (!r.bad) top_of<DT>(z, n, a.top, tm, rmax, r_at + 1, gpr * kU, sh);
     if (tid < a.top) {
       a.top_lp[row * a.top + tid] = r.bad ? r.mx : row_logprob(r, sh.cv[tid], a.inv_t);
       a.top_ids[row * a.top + tid] = r.bad ? -1 : sh.cj[tid];
@@ -357,7 +482,7 @@ __global__ __launch_bounds__(kT) void tok_kernel(TokArgs a, int parts, int seg, 
   } else {
     if (tid == 0) ps[blockIdx.x].st = st;
     if (a.top == 0 || r.bad) return;
-    top_of<DT>(z, n, a.top, tm, sh);
+    top_of<DT>(z, n, a.top, tm, rmax, r_at + 1, gpr * kU, sh);
     if (tid < a.top) {
       pv[(size_t)blockIdx.x * a.top + tid] = sh.cv[tid];
       pj[(size_t)blockIdx.x * a.top + tid] = sh.cj[tid] == 0x7FFFFFFF ? 0x7FFFFFFF : j0 + sh.cj[tid];
@@ -365,53 +490,82 @@ __global__ __launch_bounds__(kT) void tok_kernel(TokArgs a, int parts, int seg, 
   }
 }
 
-// Joins a row's parts: the statistics with one lane a part, then the alternatives as a merge
-// of the parts' sorted lists, read into LDS by the workgroup and merged by its first wave.
-// The parts are in order of ids, so of equal heads the lowest lane's goes first; a list that
-// has run out holds NaN, which no maximum takes.
+// Joins a row's parts: the statistics with one lane a part, then the alternatives from the
+// parts' sorted lists.  The first ceil(top / parts) of each list are a pool of at least `top`
+// logits, whose top-th largest is a threshold; what reaches it is ranked by counting.  Where
+// that is too much (rows with very many equal logits), the lists are merged one by one: the
+// parts are in order of ids, so of equal heads the lowest lane's goes first.  Entries that a
+// short last part could not fill hold NaN, which no comparison or maximum takes.
 template <int DT>
 __global__ __launch_bounds__(kT) void tok_join_kernel(TokArgs a, int parts, const Part* __restrict__ ps,
                                                       const float* __restrict__ pv, const int* __restrict__ pj) {
   extern __shared__ float lists[];  // [parts][top] logits, then ids
+  __shared__ TopShared sh;
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63;
   const float c = a.inv_t * kLog2e;
-  const int n = parts * a.top;
+  const int top = a.top, n = parts * top;
+  const float nan = __uint_as_float(0x7FC00000u);
   int* ids = reinterpret_cast<int*>(lists + n);
   Stat st = {-INFINITY, 0.0f, 0.0f};
+  Target target = {0, 0.0f};
+  if (tid == 0) target = load_target<DT>(a, row);
   if (lane < parts) st = ps[(size_t)row * parts + lane].st;
+#pragma unroll 4
   for (int i = tid; i < n; i += kT) {
     const int j = pj[(size_t)row * n + i];
-    lists[i] = j == 0x7FFFFFFF ? __uint_as_float(0x7FC00000u) : pv[(size_t)row * n + i];
+    const float v = pv[(size_t)row * n + i];
+    lists[i] = j == 0x7FFFFFFF ? nan : v;
     ids[i] = j;
   }
   const RowOut r = row_out(wave_join(st, c));
-  __syncthreads();
-  if (tid >= 64) return;
-  if (lane == 0) write_row<DT>(a, row, r);
-  if (a.top == 0) return;
-  float keep_v = r.mx;
-  int keep_j = -1;
+  if (tid == 0) write_row(a, row, r, target);
+  if (top == 0) return;
   if (!r.bad) {
-    const float nan = __uint_as_float(0x7FC00000u);
-    int at = lane * a.top;
-    const int end = lane < parts ? at + a.top : at;
-    float v = at < end ? lists[at] : nan;
-    for (int i = 0; i < a.top; ++i) {
-      const float m = wave_max(__builtin_fmaxf(v, -INFINITY));  // NaN counts as -infinity here
-      const int win = __ffsll((unsigned long long)__ballot(v == m)) - 1;
-      if (lane == i) keep_v = m;
-      const int j = win >= 0 ? ids[__builtin_amdgcn_readlane(at, win)] : -1;
-      if (lane == i) keep_j = j;
-      if (lane == win) {
-        ++at;
-        v = at < end ? lists[at] : nan;
+    __syncthreads();
+    const int depth = (top + parts - 1) / parts, pool = parts * depth, pool4 = (pool + 3) & ~3;  // below 2 * 64
+    if (tid < pool4) {
+      const float v = tid < pool ? lists[tid / depth * top + tid % depth] : nan;
+      sh.cv[tid] = v == v ? v : -INFINITY;
+    }
+    if (tid == 0) sh.ng = 0;
+    __syncthreads();
+    kth_largest(sh.cv, pool4, top, sh);
+    __syncthreads();
+    const float tau = sh.tau;
+    for (int i = tid; i < n; i += kT)
+      if (lists[i] >= tau) {
+        const int at = atomicAdd(&sh.ng, 1);
+        if (at < kCand) {
+          sh.cv[at] = lists[i];
+          sh.cj[at] = ids[i];
+        }
+      }
+    __syncthreads();
+    const int ng = sh.ng;
+    if (ng <= kCand) {
+      rank_top(ng, top, sh);
+      __syncthreads();
+    } else if (tid < 64) {
+      int at = lane * top;
+      const int end = lane < parts ? at + top : at;
+      float v = at < end ? lists[at] : nan;
+      for (int i = 0; i < top; ++i) {
+        const float m = wave_max(__builtin_fmaxf(v, -INFINITY));  // NaN counts as -infinity here
+        const int win = __ffsll((unsigned long long)__ballot(v == m)) - 1;
+        if (lane == win) {
+          sh.cv[i] = m;
+          sh.cj[i] = ids[at];
+          ++at;
+          v = at < end ? lists[at] : nan;
+        }
       }
     }
+    if (tid >= 64) return;  // the first wave has written or (behind the barrier) sees the result
   }
-  if (lane < a.top) {
-    a.top_lp[row * a.top + lane] = r.bad ? r.mx : row_logprob(r, keep_v, a.inv_t);
-    a.top_ids[row * a.top + lane] = keep_j;
+  if (tid < top) {
+    a.top_lp[row * top + tid] = r.bad ? r.mx : row_logprob(r, sh.cv[tid], a.inv_t);
+    a.top_ids[row * top + tid] = r.bad ? -1 : sh.cj[tid];
   }
 }
 
@@ -429,8 +583,9 @@ __device__ __forceinline__ void store8(typename Elem<DT>::type* p, const float (
       q[0][j >> 1] = DT == W4_DT_F16 ? pack_f16x2(d[j], d[j + 1]) : pack_bf16x2(d[j], d[j + 1]);
     }
   }
-  *reinterpret_cast<loose*>(p) = q[0];
-  if constexpr (DT == W4_DT_F32) *reinterpret_cast<loose*>(p + 4) = q[1];
+  // written once and not read here again
+  __builtin_nontemporal_store(q[0], reinterpret_cast<loose*>(p));
+  if constexpr (DT == W4_DT_F32) __builtin_nontemporal_store(q[1], reinterpret_cast<loose*>(p + 4));
 }
 
 template <int DT>

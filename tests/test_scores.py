@@ -187,6 +187,24 @@ def test_ordered_rows(m):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 1100])
+def test_large_logits_in_few_places(m):
+    """Most of the large logits of a row where few threads read them: runs of eight logits every
+    2048, more of them above any group's maximum than are ranked at a time."""
+    v = 130001
+    z = torch.arange(v, device=DEV).float().mul_(1e-5)
+    j = torch.arange(v, device=DEV)
+    few = (j % 2048) < 8 * 12
+    z = torch.where(few, 50.0 + z, z)
+    z = z[torch.arange(v, device=DEV)].expand(m, v).contiguous()
+    t = torch.full((m,), 7, device=DEV)
+    r = w4.token_logprobs(z, t, top=64)
+    ids = torch.sort(z[0].double(), descending=True, stable=True).indices[:64]
+    assert (r.top_ids == ids).all()
+    assert torch.allclose(r.logprobs, torch.log_softmax(z[:1].double(), 1)[0, 7].float().expand(m), atol=1e-4)
+
+
+@pytest.mark.gpu
 def test_temperature_overflow():
     """Logits that the temperature would take past fp32 are compared before it is applied."""
     z = torch.zeros(2, 10, device=DEV)
