@@ -10,6 +10,7 @@ include/w8a8.h for the contract).
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -38,33 +39,46 @@ def _pitch(cols: int) -> int:
     return (cols + 63) // 64 * 64
 
 
-class on_device:
-    """The device of a call's tensors as the current one, where it is not already."""
-
-    def __init__(self, *tensors):
-        dev = None
-        for t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
+def check_device(*tensors) -> int:
+    """The index of the one HIP device that the tensors (None among them) are on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.device
+        if dev is None:
+            if d.type != "cuda":
                 raise ValueError("tensors must be on a HIP device")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"tensors on {dev} and {t.device}: one device is wanted")
-        self.device = dev
-        self.back = None
+            dev = d
+        elif d != dev:
+            if d.type != "cuda":
+                raise ValueError("tensors must be on a HIP device")
+            raise ValueError(f"tensors on {dev} and {d}: one device is wanted")
+    return dev.index
+
+
+class on_device:
+    """Device `index` as the current one (launches go to the current device) for a call."""
+
+    __slots__ = ("index", "back")
+
+    def __init__(self, index: int):
+        self.index = index
 
     def __enter__(self):
-        now = torch.cuda.current_device()
-        if self.device.index != now:
-            self.back = now
-            torch.cuda.set_device(self.device)
-        return self
+        now = torch._C._cuda_getDevice()
+        self.back = now if now != self.index else None
+        if self.back is not None:
+            torch.cuda.set_device(self.index)
 
     def __exit__(self, *exc):
         if self.back is not None:
             torch.cuda.set_device(self.back)
+
+
+def space(nbytes: int, device):
+    """A call's workspace (None for none) from torch's allocator, in the current stream's order."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 def float_rows(x: torch.Tensor, what: str) -> torch.Tensor:
@@ -96,7 +110,7 @@ def quantize_int8(x: torch.Tensor) -> Int8Rows:
     gets a NaN scale."""
     x = float_rows(x, "x")
     rows, cols = x.shape
-    with on_device(x):
+    with on_device(check_device(x)):
         out = Int8Rows(torch.empty((rows, _pitch(cols)), dtype=torch.int8, device=x.device),
                        torch.empty(rows, dtype=torch.float32, device=x.device), rows, cols)
         check(lib().w8_quantize_rows(x.data_ptr(), _WDT[x.dtype], rows, cols, _row_stride(x), out.codes.data_ptr(),
@@ -107,51 +121,63 @@ def quantize_int8(x: torch.Tensor) -> Int8Rows:
 def _segments(outs, M: int, width: int, dt: torch.dtype):
     if dt not in _ODT:
         raise ValueError(f"outputs must be float32, float16 or bfloat16 (got {dt})")
-    if sum(o.shape[-1] for o in outs) != width:
-        raise ValueError(f"the outputs' columns must sum to {width}")
     segs = (_lib.W4OutSeg * len(outs))()
+    cols = 0
     for i, o in enumerate(outs):
         if o.dtype != dt or o.dim() != 2 or o.shape[0] != M or (o.shape[1] > 1 and o.stride(1) != 1):
             raise ValueError(f"each output must be a 2-D [{M}][cols] {dt} tensor with contiguous rows")
-        segs[i].Y = o.data_ptr()
-        segs[i].cols = o.shape[1]
-        segs[i].ld = o.stride(0) if M > 1 else o.shape[1]
+        n = o.shape[1]
+        cols += n
+        segs[i] = _lib.W4OutSeg(o.data_ptr(), n, o.stride(0) if M > 1 else n)
+    if cols != width:
+        raise ValueError(f"the outputs' columns must sum to {width}")
     return segs
 
 
-def _space(size: ctypes.c_size_t, device):
-    return torch.empty(size.value, dtype=torch.uint8, device=device) if size.value else None
+# workspace sizes depend on the sizes alone
+@functools.lru_cache(maxsize=4096)
+def _product_bytes(M: int, N: int, K: int, x_dtype: int) -> int:
+    size = ctypes.c_size_t(0)
+    check(lib().w8a8_workspace_bytes(M, N, K, x_dtype, ctypes.byref(size)))
+    return size.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _gradient_bytes(M: int, N: int, K: int, ld: int) -> int:
+    size = ctypes.c_size_t(0)
+    check(lib().w8a16_mm_t_workspace_bytes(M, N, K, ld, ctypes.byref(size)))
+    return size.value
 
 
 def _product(a, w: Int8Rows, bias, outs, dt: torch.dtype):
     """One product written to `outs`, which cover its columns in order."""
-    L = lib()
     N, K = w.rows, w.cols
-    size = ctypes.c_size_t(0)
     _check_rows(w, "weight")
     if bias is not None and (bias.dtype != dt or bias.numel() != N or not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous {dt} vector of length {N}")
     ready = isinstance(a, Int8Rows)
     if ready:
         _check_rows(a, "activations")
-        M, width = a.rows, a.cols
+        M, width, x, xs, xdt = a.rows, a.cols, a.codes, a.scales, -1
     else:
         M, width = a.shape
+        x, xs, xdt = a, None, _WDT[a.dtype]
     if width != K:
         raise ValueError(f"activation width {width} does not match the weight ({N}x{K})")
     segs = _segments(outs, M, N, dt)
-    x = a.codes if ready else a
-    with on_device(x, a.scales if ready else None, w.codes, w.scales, bias, *outs):
+    L = lib()
+    with on_device(check_device(x, xs, w.codes, w.scales, bias, *outs)):
+        size = _product_bytes(M, N, K, xdt)
+        ws = space(size, x.device)
         bp = bias.data_ptr() if bias is not None else None
-        check(L.w8a8_workspace_bytes(M, N, K, -1 if ready else _WDT[a.dtype], ctypes.byref(size)))
-        ws = _space(size, x.device)
         wp = ws.data_ptr() if ws is not None else None
         if ready:
-            check(L.w8a8_mm(x.data_ptr(), a.scales.data_ptr(), M, w.codes.data_ptr(), w.scales.data_ptr(), N, K, bp,
-                            _ODT[dt], segs, len(outs), wp, size.value, _stream(x.device)))
+            status = L.w8a8_mm(x.data_ptr(), xs.data_ptr(), M, w.codes.data_ptr(), w.scales.data_ptr(), N, K, bp,
+                               _ODT[dt], segs, len(outs), wp, size, _stream(x.device))
         else:
-            check(L.w8a8_linear(x.data_ptr(), _WDT[a.dtype], _row_stride(a), M, w.codes.data_ptr(), w.scales.data_ptr(),
-                                N, K, bp, _ODT[dt], segs, len(outs), wp, size.value, _stream(x.device)))
+            status = L.w8a8_linear(x.data_ptr(), xdt, _row_stride(x), M, w.codes.data_ptr(), w.scales.data_ptr(), N, K,
+                                   bp, _ODT[dt], segs, len(outs), wp, size, _stream(x.device))
+    check(status)
 
 
 def mm_int8(a, w: Int8Rows, bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
@@ -207,13 +233,13 @@ def mm_int8_t(dy: torch.Tensor, w: Int8Rows, out: torch.Tensor | None = None,
         raise ValueError(f"out must be a {dt} tensor of shape ({M}, {K})")
     segs = _segments([out], M, K, dt)
     ld = _row_stride(dy)
-    size = ctypes.c_size_t(0)
-    with on_device(dy, w.codes, w.scales, out):
-        L = lib()
-        check(L.w8a16_mm_t_workspace_bytes(M, N, K, ld if dy.data_ptr() % 16 == 0 else -1, ctypes.byref(size)))
-        ws = _space(size, dy.device)
-        check(L.w8a16_mm_t(dy.data_ptr(), _WDT[dy.dtype], ld, M, w.codes.data_ptr(), w.scales.data_ptr(), N, K, _ODT[dt],
-                           segs, 1, ws.data_ptr() if ws is not None else None, size.value, _stream(dy.device)))
+    with on_device(check_device(dy, w.codes, w.scales, out)):
+        size = _gradient_bytes(M, N, K, ld if dy.data_ptr() % 16 == 0 else -1)
+        ws = space(size, dy.device)
+        status = lib().w8a16_mm_t(dy.data_ptr(), _WDT[dy.dtype], ld, M, w.codes.data_ptr(), w.scales.data_ptr(), N, K,
+                                  _ODT[dt], segs, 1, ws.data_ptr() if ws is not None else None, size,
+                                  _stream(dy.device))
+    check(status)
     return out
 
 

@@ -70,6 +70,16 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="2-D"):
         w4.token_logprobs(z[0], torch.zeros(3, dtype=torch.int64))
 
+    def grad(t=torch.zeros(3, dtype=torch.int64), stats=torch.zeros(3, 2), ent=torch.zeros(3),
+             ids=torch.zeros(3, 4, dtype=torch.int64), g=None, a=None, out=None):
+        w4.token_logprobs_grad(z, t, stats, ent, ids, g, None, a, out=out)
+
+    for bad in (dict(t=torch.zeros(2, dtype=torch.int64)), dict(stats=torch.zeros(3, 3)), dict(ent=torch.zeros(3).double()),
+                dict(ids=torch.zeros(3, 4, dtype=torch.int32)), dict(ids=torch.zeros(3, dtype=torch.int64)),
+                dict(g=torch.zeros(4)), dict(a=torch.zeros(3, 5)), dict(out=torch.zeros(3, 11)), dict()):
+        with pytest.raises(ValueError):  # the last: not on a device
+            grad(**bad)
+
 
 # ---------------------------------------------------------------- GPU
 
