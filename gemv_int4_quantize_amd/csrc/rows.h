@@ -63,6 +63,8 @@ __device__ __forceinline__ void widen8(const Raw8<DT>& r, float v[8]) {
   }
 }
 
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
 // Maximum over the wave in every lane, without LDS round trips: partners lane ^ 32 and ^ 16
 // by permlane swaps, then row mirror, half-row mirror and quad permutes.
 __device__ __forceinline__ float wave_max(float v) {
@@ -75,8 +77,6 @@ __device__ __forceinline__ float wave_max(float v) {
   v = __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false)));
   return __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false)));
 }
-
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // wave_max of unsigned integers.
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
@@ -97,18 +97,32 @@ __device__ __forceinline__ float elem_to_f32(typename Elem<DT>::type x) {
   else return bf16_bits_to_f32(x);
 }
 
-// Row quantization to int8 (w8_quantize_rows).  The largest magnitude is kept as the bits
-// of |x| in fp32, compared as integers: they order finite values, then infinity, then NaN.
+// Row quantization to int8 (w8_quantize_rows).  The largest magnitude is kept as the bits of
+// |x|, compared as integers: they order finite values, then infinity, then NaN.  16-bit types
+// are compared as they are, two at a time (v_pk_max_u16); absmax_bits gives the maximum as fp32
+// bits.
 template <int DT>
 __device__ __forceinline__ uint32_t absmax8(const Raw8<DT>& r, uint32_t m) {
-  float v[8];
-  widen8<DT>(r, v);
+  if constexpr (DT == W4_DT_F32) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-    m = b > m ? b : m;
+    for (int j = 0; j < 8; ++j) m = umax(m, r.q[j >> 2][j & 3] & 0x7FFFFFFFu);
+    return m;
+  } else {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 v = __builtin_bit_cast(u16x2, m);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v = __builtin_elementwise_max(v, __builtin_bit_cast(u16x2, r.q[0][j] & 0x7FFF7FFFu));
+    return __builtin_bit_cast(uint32_t, v);
   }
-  return m;
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t absmax_bits(uint32_t m) {
+  if constexpr (DT == W4_DT_F32) return m;
+  const uint32_t b = umax(m & 0xFFFFu, m >> 16);
+  if constexpr (DT == W4_DT_BF16) return b << 16;
+  else return __float_as_uint(f16_bits_to_f32(b));
 }
 
 struct RowScale {

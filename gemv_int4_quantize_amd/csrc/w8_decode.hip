@@ -3,11 +3,13 @@
 // are quantized by the same launch.
 //
 // A workgroup of NW waves owns 16 channels; its waves share out the contraction in contiguous
-// runs of 64-column units and add their sums through LDS.
+// runs of 128-column units and add their sums through LDS.
 // v_mfma_i32_16x16x64_i8 with channels as rows and tokens as columns: lane l supplies 16 bytes
-// of channel l % 16 and of token l % 16 (columns 16 (l / 16) .. of the unit) and holds token
-// l % 16 of channels 4 (l / 16) .. + 3.  The products cost 16 cycles for 1 KB of weight, so
-// that most of the 16 token columns are idle does not matter.
+// of channel l % 16 and of token l % 16, the same columns of both, and holds token l % 16 of
+// channels 4 (l / 16) .. + 3.  Lane l takes the 32 bytes from column 32 (l / 16) of a unit for
+// two products, so that each of its two loads touches whole 128-byte lines (half a line at a
+// time, 64-column units, was slower).  The products cost 16 cycles for 1 KB of weight, so that
+// most of the 16 token columns are idle does not matter.
 #include <algorithm>
 
 #include "api_common.h"
@@ -54,19 +56,25 @@ __global__ __launch_bounds__(NW * 64) void w8_decode_kernel(const int8_t* __rest
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = blockIdx.x * 16;
-  const int units = pitch >> 6;
+  const int units = (pitch + 127) >> 7;
   const int per = (units + NW - 1) / NW;
   const int u0 = min(wave * per, units), u1 = min(u0 + per, units);
   const int r16 = lane & 15, q4 = lane >> 4;
 
   const uint32_t wbytes = (uint32_t)min(16, N - n0) * (uint32_t)pitch;
-  const int ow = r16 * pitch + q4 * 16;
-  const int oa = min(r16, M - 1) * pitch + q4 * 16;
-  i32x4 w[D], x[D];
+  const int ow = r16 * pitch + q4 * 32;
+  const int oa = min(r16, M - 1) * pitch + q4 * 32;
+  i32x4 w[D][2], x[D][2];
   auto load = [&](int d, int u) {
     const bool in = u < u1;
-    w[d] = load16<kNonTemporal>(make_rsrc(W + (size_t)n0 * pitch, in ? wbytes : 0u), ow, u * 64);
-    if constexpr (XDT < 0) x[d] = load16<0>(make_rsrc(A, in ? (uint32_t)M * (uint32_t)pitch : 0u), oa, u * 64);
+    const rsrc_t rw = make_rsrc(W + (size_t)n0 * pitch, in ? wbytes : 0u);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) w[d][h] = load16<kNonTemporal>(rw, ow + h * 16, u * 128);
+    if constexpr (XDT < 0) {
+      const rsrc_t ra = make_rsrc(A, in ? (uint32_t)M * (uint32_t)pitch : 0u);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) x[d][h] = load16<0>(ra, oa + h * 16, u * 128);
+    }
   };
 
   if constexpr (XDT >= 0) {
@@ -100,7 +108,7 @@ __global__ __launch_bounds__(NW * 64) void w8_decode_kernel(const int8_t* __rest
       if (m >= M) break;
 #pragma unroll
       for (int c = 0; c < C; ++c) am[m] = absmax8<XDT>(held[m][c], am[m]);
-      const uint32_t a = wave_umax(am[m]);
+      const uint32_t a = wave_umax(absmax_bits<XDT>(am[m]));
       if (lane == 0) part[m * NW + wave] = a;
     }
     __syncthreads();
@@ -128,12 +136,23 @@ __global__ __launch_bounds__(NW * 64) void w8_decode_kernel(const int8_t* __rest
   }
 
   i32x4 acc = {0, 0, 0, 0};
-  const char* xl = smem + min(r16, M - 1) * (pitch + 16) + q4 * 16;
+  const char* xl = smem + min(r16, M - 1) * (pitch + 16) + q4 * 32;
+  // the last unit of a pitch that is not a multiple of 128 holds 64 columns: past them the
+  // weight's bytes are the next channel's, and the tokens are taken as 0
+  const int cut = (pitch & 64) != 0 && q4 >= 2 ? units - 1 : units;
   for (int u = u0; u < u1; u += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      if constexpr (XDT >= 0) x[d] = *reinterpret_cast<const i32x4*>(xl + min(u + d, units - 1) * 64);
-      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[d], x[d], acc, 0, 0, 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (XDT >= 0) {
+          // past the wave's run the weight is 0; the address stays inside the codes
+          const int at = min(u + d, cut - 1);
+          x[d][h] = *reinterpret_cast<const i32x4*>(xl + at * 128 + h * 16);
+        }
+        const i32x4 t = u + d < cut ? x[d][h] : i32x4{0, 0, 0, 0};
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[d][h], t, acc, 0, 0, 0);
+      }
       load(d, u + D + d);
     }
   }
@@ -164,9 +183,9 @@ hipError_t run(const W8Args& a, hipStream_t st) {
 template <int XDT>
 hipError_t run_x(const W8Args& a, const DeviceCaps& caps, hipStream_t st) {
   const bool few = a.N < 16 * 2 * (int64_t)caps.cus;
-  if (XDT < 0) return few ? run<16, 8, XDT, 1>(a, st) : run<8, 8, XDT, 1>(a, st);
-  if (few) return a.pitch <= 8192 ? run<16, 8, XDT, 1>(a, st) : run<16, 8, XDT, 2>(a, st);
-  return a.pitch <= 4096 ? run<8, 8, XDT, 1>(a, st) : run<8, 8, XDT, 3>(a, st);
+  if (XDT < 0) return few ? run<16, 4, XDT, 1>(a, st) : run<8, 4, XDT, 1>(a, st);
+  if (few) return a.pitch <= 8192 ? run<16, 4, XDT, 1>(a, st) : run<16, 4, XDT, 2>(a, st);
+  return a.pitch <= 4096 ? run<8, 4, XDT, 1>(a, st) : run<8, 4, XDT, 3>(a, st);
 }
 
 }  // namespace

@@ -33,7 +33,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void quantize_rows_kernel(co
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) m = absmax8<DT>(r[c], m);
-  m = wave_umax(m);
+  m = wave_umax(absmax_bits<DT>(m));
   if constexpr (TPR > 64) {
     __shared__ uint32_t part[TPR / 64];
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
@@ -70,7 +70,7 @@ __global__ __launch_bounds__(1024) void quantize_long_rows_kernel(const void* __
   };
   uint32_t m = 0;
   for (int col = threadIdx.x * 8; col < cols; col += 8192) m = absmax8<DT>(load(col), m);
-  m = wave_umax(m);
+  m = wave_umax(absmax_bits<DT>(m));
   __shared__ uint32_t part[16];
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
   __syncthreads();
