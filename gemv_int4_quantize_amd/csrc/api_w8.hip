@@ -18,7 +18,8 @@ using w4::make_epi;
 using w4::ok;
 
 constexpr int64_t kMaxK = (int64_t)1 << 17;    // int32 sums: 128 * 128 * K < 2^31
-constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 65536;
+constexpr int64_t kMaxScored = ((int64_t)1 << 31) - 65536;  // rows and columns of scores
+constexpr int64_t kMaxRows = (int64_t)1 << 30;   // a launch holds fewer than 2^32 threads
 constexpr int64_t kMaxTop = 64;
 
 int64_t pitch_of(int64_t cols) { return (cols + 63) / 64 * 64; }
@@ -31,7 +32,7 @@ int check_sizes(int64_t M, int64_t N, int64_t K) {
   if (M < 0) return fail(W4_ERR_INVALID, "M = %lld must be >= 0", (long long)M);
   if (N < 1 || K < 1) return fail(W4_ERR_INVALID, "N = %lld and K = %lld must be >= 1", (long long)N, (long long)K);
   if (K >= kMaxK) return fail(W4_ERR_UNSUPPORTED, "K = %lld must be below 2^17 (int32 sums)", (long long)K);
-  if (M > kMaxRows || N > kMaxRows) return fail(W4_ERR_UNSUPPORTED, "M and N must fit in int32");
+  if (M > kMaxRows || N > kMaxRows) return fail(W4_ERR_UNSUPPORTED, "M and N must be at most 2^30");
   return W4_OK;
 }
 
@@ -250,7 +251,7 @@ int tok_workspace_bytes(int64_t M, int64_t V, int top, size_t* bytes) {
   if (M < 0 || V < 1 || top < 0 || top > kMaxTop || top > V)
     return fail(W4_ERR_INVALID, "M = %lld, V = %lld, top = %d: need M >= 0, V >= 1, 0 <= top <= min(V, %d)",
                 (long long)M, (long long)V, top, (int)kMaxTop);
-  if (V > kMaxRows || M > kMaxRows) return fail(W4_ERR_UNSUPPORTED, "M and V must fit in int32");
+  if (V > kMaxScored || M > kMaxScored) return fail(W4_ERR_UNSUPPORTED, "M and V must fit in int32");
   if (!bytes) return fail(W4_ERR_INVALID, "bytes is NULL");
   *bytes = M == 0 ? 0 : w4::tok_ws_bytes(M, V, top, device_caps());
   return ok();

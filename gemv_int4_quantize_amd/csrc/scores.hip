@@ -710,7 +710,30 @@ size_t tok_ws_bytes(int64_t M, int64_t V, int top, const DeviceCaps& caps) {
   return parts == 1 ? 0 : (size_t)M * parts * (sizeof(Part) + 8 * (size_t)top);
 }
 
-hipError_t launch_tok(const TokArgs& a, const DeviceCaps& caps, void* ws, hipStream_t st) {
+// A launch holds fewer than 2^32 threads: rows are launched in runs of at most kRows.
+constexpr int64_t kRows = (int64_t)1 << 23;
+
+static size_t elem_bytes(int dt) { return dt == W4_DT_F32 ? 4 : 2; }
+
+hipError_t launch_tok(const TokArgs& all, const DeviceCaps& caps, void* ws, hipStream_t st) {
+  TokArgs a = all;
+  if (a.M > kRows) {
+    for (int64_t r = 0; r < all.M; r += kRows) {
+      a.M = std::min(kRows, all.M - r);
+      const hipError_t e = launch_tok(a, caps, ws, st);  // rows enough for one part: no workspace
+      if (e != hipSuccess) return e;
+      a.z = static_cast<const char*>(a.z) + (size_t)(kRows * a.ld) * elem_bytes(a.dt);
+      a.targets += kRows;
+      a.lp += kRows;
+      a.ent += kRows;
+      a.stats += 2 * kRows;
+      if (a.top > 0) {
+        a.top_lp += kRows * a.top;
+        a.top_ids += kRows * a.top;
+      }
+    }
+    return hipSuccess;
+  }
   int parts = parts_of(a.M, a.V, caps, kMaxParts);
   const int seg = seg_of(a.V, parts);
   Part* ps = static_cast<Part*>(ws);
@@ -734,7 +757,27 @@ hipError_t launch_tok(const TokArgs& a, const DeviceCaps& caps, void* ws, hipStr
   return hipGetLastError();
 }
 
-hipError_t launch_tok_grad(const TokGradArgs& a, const DeviceCaps& caps, hipStream_t st) {
+hipError_t launch_tok_grad(const TokGradArgs& all, const DeviceCaps& caps, hipStream_t st) {
+  TokGradArgs a = all;
+  if (a.M > kRows) {
+    for (int64_t r = 0; r < all.M; r += kRows) {
+      a.M = std::min(kRows, all.M - r);
+      const hipError_t e = launch_tok_grad(a, caps, st);
+      if (e != hipSuccess) return e;
+      a.z = static_cast<const char*>(a.z) + (size_t)(kRows * a.ld) * elem_bytes(a.dt);
+      a.dz = static_cast<char*>(a.dz) + (size_t)(kRows * a.ldd) * elem_bytes(a.dt);
+      a.targets += kRows;
+      a.stats += 2 * kRows;
+      a.ent += kRows;
+      if (a.g != nullptr) a.g += kRows;
+      if (a.h != nullptr) a.h += kRows;
+      if (a.top > 0) {
+        a.top_ids += kRows * a.top;
+        if (a.a != nullptr) a.a += kRows * a.top;
+      }
+    }
+    return hipSuccess;
+  }
   int parts = parts_of(a.M, a.V, caps, 1 << 20);
   const int seg = seg_of(a.V, parts);
   parts = (int)((a.V + seg - 1) / seg);

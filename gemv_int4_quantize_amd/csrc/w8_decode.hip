@@ -47,7 +47,7 @@ template <int NW, int D, int XDT, int C>
 __global__ __launch_bounds__(NW * 64) void w8_decode_kernel(const int8_t* __restrict__ W, const float* __restrict__ sw,
                                                             const int8_t* __restrict__ A, const float* __restrict__ sa,
                                                             const void* __restrict__ X, int64_t ldx, int M, int N, int K,
-                                                            int pitch, const Epi ep) {
+                                                            int pitch, int first, const Epi ep) {
   constexpr int T = NW * 64;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ int sums[NW][kMaxM][16 + 4];
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(NW * 64) void w8_decode_kernel(const int8_t* __rest
   __shared__ uint32_t part[XDT >= 0 ? kMaxM * NW : 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n0 = blockIdx.x * 16;
+  const int n0 = first + blockIdx.x * 16;
   const int units = (pitch + 127) >> 7;
   const int per = (units + NW - 1) / NW;
   const int u0 = min(wave * per, units), u1 = min(u0 + per, units);
@@ -174,9 +174,16 @@ hipError_t run(const W8Args& a, hipStream_t st) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  k<<<(unsigned)((a.N + 15) / 16), NW * 64, lds, st>>>(a.W, a.w_scales, a.A, a.a_scales, a.X, a.ldx, (int)a.M, (int)a.N,
-                                                       (int)a.K, (int)a.pitch, a.ep);
-  return hipGetLastError();
+  // a launch holds fewer than 2^32 threads
+  constexpr int64_t kChannels = (int64_t)1 << 25;
+  for (int64_t n = 0; n < a.N; n += kChannels) {
+    const int64_t wgs = (std::min(kChannels, a.N - n) + 15) / 16;
+    k<<<(unsigned)wgs, NW * 64, lds, st>>>(a.W, a.w_scales, a.A, a.a_scales, a.X, a.ldx, (int)a.M, (int)a.N, (int)a.K,
+                                           (int)a.pitch, (int)n, a.ep);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Sixteen waves a workgroup where there are few workgroups (less than two a CU), else eight.

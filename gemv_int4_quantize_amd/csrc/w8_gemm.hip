@@ -216,13 +216,13 @@ __global__ __launch_bounds__(WM * WN * 64) void w8_ring_kernel(const int8_t* __r
     return;
   }
   const bool wide = epi_wide(ep, N) != 0;
-  const rsrc_t rs = make_rsrc(sa, (uint32_t)M * 4u);
+  const rsrc_t rs = make_rsrc(sa + m0, (uint32_t)min(BM, M - m0) * 4u);
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     float s[16];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (rbase + i * 32 + g * 8) * 4, 0, 0));
+      const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (rbase - m0 + i * 32 + g * 8) * 4, 0, 0));
 #pragma unroll
       for (int q = 0; q < 4; ++q) s[g * 4 + q] = __uint_as_float(v[q]);
     }

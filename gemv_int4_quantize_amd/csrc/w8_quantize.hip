@@ -2,6 +2,8 @@
 //   a = max |x|,  s = max(a / 127, 2^-126),  q = rint(x * fp32(1 / s)).
 // An HBM stream that needs the whole row's maximum before its first code: a row is held in
 // the registers of TPR threads (C chunks of eight elements each), so it is read once.
+#include <algorithm>
+
 #include "api_common.h"
 #include "launch.h"
 #include "rows.h"
@@ -108,6 +110,16 @@ hipError_t launch_dt(const void* X, int64_t rows, int cols, int64_t ld, int pitc
 hipError_t launch_quantize_rows(const void* X, int dt, int64_t rows, int64_t cols, int64_t ld, int8_t* codes,
                                 float* scales, hipStream_t st) {
   const int pitch = (int)((cols + 63) / 64 * 64);
+  // a launch holds fewer than 2^32 threads, a row takes at most 1024
+  constexpr int64_t kRows = (int64_t)1 << 21;
+  if (rows > kRows) {
+    for (int64_t r = 0; r < rows; r += kRows) {
+      const hipError_t e = launch_quantize_rows(static_cast<const char*>(X) + (size_t)(r * ld) * (dt == W4_DT_F32 ? 4 : 2), dt,
+                                                std::min(kRows, rows - r), cols, ld, codes + (size_t)r * pitch, scales + r, st);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
   switch (dt) {
     case W4_DT_F32: return launch_dt<W4_DT_F32>(X, rows, (int)cols, ld, pitch, codes, scales, st);
     case W4_DT_F16: return launch_dt<W4_DT_F16>(X, rows, (int)cols, ld, pitch, codes, scales, st);

@@ -401,3 +401,17 @@ def test_graph_replays(m):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.gpu
+def test_more_rows_than_a_launch_holds():
+    """Rows and channels past one launch's: every row the same as its copy among the first."""
+    x = torch.randn(64, 64, device="cuda").bfloat16()
+    n = (1 << 21) + 192
+    few, many = w4.quantize_int8(x), w4.quantize_int8(x.repeat(n // 64, 1))
+    assert (many.codes.view(-1, 64, 64) == few.codes).all() and (many.scales.view(-1, 64) == few.scales).all()
+    n = (1 << 25) + 64
+    w = w4.Int8Rows(few.codes.repeat(n // 64, 1), few.scales.repeat(n // 64), n, 64)
+    for a in (x[:3], w4.Int8Rows(few.codes[:3], few.scales[:3], 3, 64)):
+        y = w4.mm_int8(a, w, out_dtype=torch.bfloat16).view(3, -1, 64)
+        assert torch.equal(y[:, 0], w4.mm_int8(a, few, out_dtype=torch.bfloat16)) and (y == y[:, :1]).all()

@@ -376,3 +376,23 @@ def test_graph_replays(m, v):
         torch.cuda.synchronize()
         for x, y in zip(want, r):
             assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+def test_more_rows_than_a_launch_holds():
+    """2^24 + 3 rows of two logits: log p of the first is -log(1 + e^d) exactly, d = z1 - z0."""
+    M = (1 << 24) + 3
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    z = torch.randn(M, 2, device="cuda", generator=gen).requires_grad_()
+    t = torch.randint(2, (M,), device="cuda", generator=gen)
+    s = w4.token_logprobs(z, t, top=1)
+    d = z.detach().double()
+    d = (d[:, 0] - d[:, 1]) * (2 * t - 1)  # other minus target
+    ref = -torch.nn.functional.softplus(d)
+    # fp32: the difference (2^-24 of it), exp2, a sum of two and a logarithm, each some 2^-22
+    assert (s.logprobs.double() - ref).abs().max() < 1e-5
+    assert torch.equal(s.top_ids[:, 0], (z.detach()[:, 1] > z.detach()[:, 0]).long())
+    s.logprobs.sum().backward()
+    q = torch.sigmoid(d)  # the other's probability
+    ref = torch.stack([torch.where(t == 0, q, -q), torch.where(t == 1, q, -q)], 1)
+    assert (z.grad.double() - ref).abs().max() < 1e-5
