@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libw4a16.so")
 SOURCES = ["api.hip", "quantize.hip", "gemv.hip", "gemm.hip", "gemm_nt.hip", "skinny.hip",
-           "api_w8.hip", "w8_quantize.hip", "w8_gemm.hip", "w8_decode.hip", "scores.hip"]
+           "api_w8.hip", "w8_quantize.hip", "w8_gemm.hip", "w8_decode.hip", "w8_grad.hip", "scores.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

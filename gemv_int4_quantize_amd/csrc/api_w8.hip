@@ -70,27 +70,6 @@ LinearWs linear_ws(int64_t M, int64_t N, int64_t K) {
   return w;
 }
 
-w4::MmArgs t_args(const void* dY, int dtype, int64_t ld, int64_t M, const int8_t* W, const float* w_scales, int64_t N,
-                  int64_t K, const w4::Epi& ep) {
-  w4::MmArgs a;
-  a.A = static_cast<const uint16_t*>(dY);
-  a.packed = reinterpret_cast<const int32_t*>(W);
-  a.scales = nullptr;
-  a.zeros = nullptr;
-  a.ep = ep;
-  a.M = M;
-  a.N = N;
-  a.K = K;
-  a.mode = W4_MODE_ROWWISE;
-  a.group = (int)K;
-  a.transposed = true;
-  a.a_f16 = dtype == W4_DT_F16;
-  a.scales8 = w_scales;
-  a.wpitch = pitch_of(K);
-  a.lda = ld;
-  return a;
-}
-
 }  // namespace
 
 extern "C" {
@@ -201,10 +180,8 @@ int w8a16_mm_t_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ld, size
   if (!bytes) return fail(W4_ERR_INVALID, "bytes is NULL");
   *bytes = 0;
   if (M == 0) return ok();
-  const w4::Epi ep = {};
-  const w4::MmArgs a = t_args(nullptr, W4_DT_BF16, N, M, nullptr, reinterpret_cast<const float*>(bytes), N, K, ep);
   if (ld < 0 || ld % 8 != 0 || N % 8 != 0) *bytes = up256((size_t)M * pitch_of(N) * 2);
-  *bytes += w4::gemm_workspace_bytes(a, device_caps());
+  *bytes += w4::w8_grad_workspace_bytes(M, N, K, device_caps());
   return ok();
 }
 
@@ -218,9 +195,8 @@ int w8a16_mm_t(const void* dY, int dtype, int64_t ld, int64_t M, const int8_t* W
   w4::Epi ep;
   s = make_epi(K, M, nullptr, out_dtype, segs, nsegs, &ep);
   if (s != W4_OK) return s;
-  // the GEMM addresses a 256-row dY tile with 32-bit offsets, and 32-row tiles in grid.y
+  // the kernel addresses a 256-row dY tile with 32-bit offsets
   if (N >= ((int64_t)1 << 22)) return fail(W4_ERR_UNSUPPORTED, "N = %lld must be below 2^22", (long long)N);
-  if (M > (int64_t)65535 * 32) return fail(W4_ERR_UNSUPPORTED, "M = %lld must be at most %d", (long long)M, 65535 * 32);
   if (M == 0) return ok();
   s = check_weight(W, w_scales);
   if (s == W4_OK) s = check_ws(ws);
@@ -229,7 +205,7 @@ int w8a16_mm_t(const void* dY, int dtype, int64_t ld, int64_t M, const int8_t* W
   if (M == 1) ld = N;
   size_t wsb = ws != nullptr ? ws_bytes : 0;
   char* w = static_cast<char*>(ws);
-  w4::MmArgs a = t_args(dY, dtype, ld, M, W, w_scales, N, K, ep);
+  w4::W8GradArgs a = {static_cast<const uint16_t*>(dY), dtype == W4_DT_F16, ld, N, W, w_scales, ep, M, N, K, pitch_of(K)};
   if (ld % 8 != 0 || N % 8 != 0 || ld >= ((int64_t)1 << 22) || !aligned(dY, 16)) {
     const int64_t npad = pitch_of(N);
     const size_t need = up256((size_t)M * npad * 2);
@@ -238,13 +214,12 @@ int w8a16_mm_t(const void* dY, int dtype, int64_t ld, int64_t M, const int8_t* W
     s = launched(w4::launch_pad_rows(static_cast<const uint16_t*>(dY), M, N, ld, reinterpret_cast<uint16_t*>(w), npad, st),
                  "pad_rows");
     if (s != W4_OK) return s;
-    a.A = reinterpret_cast<const uint16_t*>(w);
-    a.lda = npad;
-    a.a_zeros = true;
+    a.dY = reinterpret_cast<const uint16_t*>(w);
+    a.ld = a.L = npad;
     w += need;
     wsb -= need;
   }
-  return launched(w4::launch_gemm(a, device_caps(), wsb > 0 ? w : nullptr, wsb, st), "w8a16_mm_t");
+  return launched(w4::launch_w8_grad(a, device_caps(), wsb > 0 ? w : nullptr, wsb, st), "w8a16_mm_t");
 }
 
 int tok_workspace_bytes(int64_t M, int64_t V, int top, size_t* bytes) {

@@ -165,31 +165,6 @@ __device__ __forceinline__ void dq_rows_op(uint32_t w0, const DqConst& c0, uint3
   for (int j = 0; j < 8; ++j) out[j] = F16 ? pack_f16x2(v0[j], v1[j]) : pack_bf16x2(v0[j], v1[j]);
 }
 
-// Eight int8 codes of a row in bytes 0..3 of w[0] and w[1] -> the fp32 values code * s, each
-// rounded once: with the sign bits flipped the bytes are u = code + 128 (v_cvt_f32_ubyte),
-// and fma(u, s, -128 s) = fp32(code * s) as -128 s is exact.
-__device__ __forceinline__ void dq_bytes_f32(const u32x2& w, float s, float v[8]) {
-  const float n = -128.0f * s;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t u = w[h] ^ 0x80808080u;
-    v[4 * h] = __builtin_fmaf((float)(u & 0xFFu), s, n);
-    v[4 * h + 1] = __builtin_fmaf((float)((u >> 8) & 0xFFu), s, n);
-    v[4 * h + 2] = __builtin_fmaf((float)((u >> 16) & 0xFFu), s, n);
-    v[4 * h + 3] = __builtin_fmaf((float)(u >> 24), s, n);
-  }
-}
-
-// dq_rows_op for eight int8 codes of each of two consecutive rows.
-template <bool F16>
-__device__ __forceinline__ void dq_byte_rows_op(const u32x2& w0, float s0, const u32x2& w1, float s1, uint32_t out[8]) {
-  float v0[8], v1[8];
-  dq_bytes_f32(w0, s0, v0);
-  dq_bytes_f32(w1, s1, v1);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) out[j] = F16 ? pack_f16x2(v0[j], v1[j]) : pack_bf16x2(v0[j], v1[j]);
-}
-
 // acc += a.lo * b.lo + a.hi * b.hi on fp16 pairs, fp32 accumulate (v_dot2_f32_f16).
 __device__ __forceinline__ float dot2_f16(uint32_t a, uint32_t b, float acc) {
   typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));

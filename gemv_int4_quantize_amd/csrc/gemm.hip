@@ -62,20 +62,14 @@ constexpr int lds_row() { return BK + 8; }
 // F16: fp16 activations and weight operand (v_mfma_f32_32x32x16_f16), else bf16.
 // DMA (transposed, STAGES = 4, N % BK == 0): the dY tile goes global -> LDS with direct
 // loads instead of through the staging registers.
-// W8 (transposed, STAGES = 4, META_ROW): the weight is int8 rows, `scales` pointing to one
-// fp32 scale per row, with wpitch bytes a row; a word column is then eight bytes, and the
-// weight operand rne16(code * scale).  lda: dY's row stride.
-template <bool TRANS, int WM, int WN, int FM, int FN, int BK, int META, int MPT, int STAGES, bool F16, bool DMA,
-          bool W8 = false>
+template <bool TRANS, int WM, int WN, int FM, int FN, int BK, int META, int MPT, int STAGES, bool F16, bool DMA>
 __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(const uint16_t* __restrict__ A,
                                                             const int32_t* __restrict__ packed,
                                                             const uint16_t* __restrict__ scales,
                                                             const uint16_t* __restrict__ zeros,
                                                             const Epi ep,
                                                             int M, int N, int K, int log2g, int kt_per_slice,
-                                                            int ct0, int pw, float* __restrict__ part,
-                                                            int lda, int wpitch) {
-  static_assert(!W8 || (TRANS && STAGES == 4 && META == META_ROW), "int8 rows: the interleaved transposed tiles");
+                                                            int ct0, int pw, float* __restrict__ part) {
   constexpr int T = WM * WN * 64;
   constexpr int BM = WM * FM * 32;
   constexpr int BN = WN * FN * 32;
@@ -108,7 +102,7 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(const uint16_t* __re
 
   const int L = TRANS ? N : K;      // contraction length
   const int OUTC = TRANS ? K : N;   // output columns
-  const int KW = W8 ? wpitch >> 3 : K >> 3;  // packed words (W8: 8-byte units) per weight row
+  const int KW = K >> 3;            // packed words per weight row
   const int gpr = META == META_GROUP ? K >> log2g : 1;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -127,14 +121,6 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(const uint16_t* __re
     uint32_t w[W_PER_T];
     uint16_t s[W_PER_T], z[W_PER_T];
     uint32_t sv[4], zv[4];  // transposed rowwise: the W_PER_T rows' pairs as loaded
-    u32x2 w8[W8 ? W_PER_T : 1];
-    float s8[W8 ? W_PER_T : 1];
-  };
-  // two consecutive staged rows i, i + 1 of the word column as operand pairs (transposed)
-  auto dq_pair = [](const Regs& R, int i, int i1, auto s_of, auto z_of, uint32_t out[8]) {
-    if constexpr (W8) dq_byte_rows_op<F16>(R.w8[i], R.s8[i], R.w8[i1], R.s8[i1], out);
-    else dq_rows_op<F16>(R.w[i], dq_const_mix(s_of(R, i), z_of(R, i)), R.w[i1],
-                         dq_const_mix(s_of(R, i1), z_of(R, i1)), out);
   };
   // scale / zero bits of staged row i: transposed rowwise ones are split out of the loaded
   // words only where they are used, so the loads do not have to land when issued
@@ -165,24 +151,22 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(const uint16_t* __re
   uint16_t t_gs = 0, t_gz = 0;
   if constexpr (TRANS) {
     // N < 2^22 and K <= 2^21 (checked at the boundary) keep every offset below 2^32
-    t_ar = make_rsrc(A + (size_t)m0 * lda,
-                     ((uint32_t)(__builtin_amdgcn_readfirstlane(min(BM, M - m0)) - 1) * (uint32_t)lda +
-                      (uint32_t)(DMA && W8 ? min(lda, KT_ALL * BK) : L)) * 2u);
+    t_ar = make_rsrc(A + (size_t)m0 * L, (uint32_t)__builtin_amdgcn_readfirstlane(min(BM, M - m0)) * (uint32_t)L * 2u);
 #pragma unroll
     for (int i = 0; i < A_UNITS; ++i) {
       const int u = tid + i * T;
       const int row = u / SLOTS;
       const int ch = DMA ? ((u % SLOTS) ^ ((row >> ASH) & (SLOTS - 1))) : u % SLOTS;
-      t_aoff[i] = ((uint32_t)row * (uint32_t)lda + (uint32_t)ch * 8u) * 2u;
+      t_aoff[i] = ((uint32_t)row * (uint32_t)L + (uint32_t)ch * 8u) * 2u;
     }
     const int wc = tid % WCOLS, rb = tid / WCOLS;
     const int wcol = min((c0 >> 3) + wc, KW - 1);
-    t_woff = ((uint32_t)(rb * W_PER_T) * (uint32_t)KW + (uint32_t)wcol) * (W8 ? 8u : 4u);
+    t_woff = ((uint32_t)(rb * W_PER_T) * (uint32_t)KW + (uint32_t)wcol) * 4u;
     // groupwise: row rb * W_PER_T's pair of the word column's group; rowwise: that row's pair
     if constexpr (META == META_GROUP)
       t_moff = ((uint32_t)(rb * W_PER_T) * (uint32_t)gpr + (uint32_t)((wcol * 8) >> log2g)) * 2u;
     else
-      t_moff = (uint32_t)(rb * W_PER_T) * (W8 ? 4u : 2u);
+      t_moff = (uint32_t)(rb * W_PER_T) * 2u;
     if constexpr (META == META_GLOBAL) {
       t_gs = scales[0];
       t_gz = zeros[0];
@@ -201,28 +185,6 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(const uint16_t* __re
       // resource descriptor per-lane and every load a waterfall loop)
       const int rows = __builtin_amdgcn_readfirstlane(max(0, min(BK, N - l0)));
       const int nb = __builtin_amdgcn_readfirstlane(min(l0, N - 1));
-      if constexpr (W8) {
-        const rsrc_t pr = make_rsrc(packed + (size_t)nb * KW * 2, (uint32_t)rows * (uint32_t)KW * 8u);
-        const rsrc_t sr = make_rsrc(reinterpret_cast<const float*>(scales) + nb, (uint32_t)(rows * 4));
-#pragma unroll
-        for (int i = 0; i < W_PER_T; ++i)
-          R.w8[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(pr, t_woff + (uint32_t)(i * KW * 8), 0, 0));
-        // the W_PER_T consecutive rows' scales
-        if constexpr (W_PER_T % 4 == 0) {
-#pragma unroll
-          for (int h = 0; h < W_PER_T / 4; ++h) {
-            const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(sr, t_moff + 16u * h, 0, 0));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) R.s8[4 * h + q] = __uint_as_float(v[q]);
-          }
-        } else {
-          static_assert(!W8 || W_PER_T % 4 == 0 || W_PER_T == 2, "2, 4 or 8 rows per thread");
-          const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(sr, t_moff, 0, 0));
-          R.s8[0] = __uint_as_float(v[0]);
-          R.s8[1] = __uint_as_float(v[1]);
-        }
-        return;
-      }
       const rsrc_t pr = make_rsrc(packed + (size_t)nb * KW, (uint32_t)rows * (uint32_t)KW * 4u);
 #pragma unroll
       for (int i = 0; i < W_PER_T; ++i)
@@ -357,7 +319,8 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(const uint16_t* __re
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         const int i1 = 2 * p + 1 < W_PER_T ? 2 * p + 1 : 2 * p;
-        dq_pair(R, 2 * p, i1, s_of, z_of, pk[p]);
+        dq_rows_op<F16>(R.w[2 * p], dq_const_mix(s_of(R, 2 * p), z_of(R, 2 * p)), R.w[i1],
+                        dq_const_mix(s_of(R, i1), z_of(R, i1)), pk[p]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -459,7 +422,8 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(const uint16_t* __re
       for (int pp = 0; pp < W_PER_T / 2; ++pp) {
         const int i = 2 * pp;  // rows i, i + 1 of the word column, in slice pp * KK / pairs
         if (pp * KK / (W_PER_T / 2) == kk)
-          dq_pair(R, i, i + 1, s_of, z_of, pk[i / 2]);
+          dq_rows_op<F16>(R.w[i], dq_const_mix(s_of(R, i), z_of(R, i)), R.w[i + 1],
+                          dq_const_mix(s_of(R, i + 1), z_of(R, i + 1)), pk[i / 2]);
       }
     }
 #pragma unroll
@@ -479,8 +443,7 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(const uint16_t* __re
     // weight loads of the step are outstanding means the tile has landed, while those
     // weights keep two steps to arrive.  The barrier carries no fence (a workgroup fence
     // would wait for every load in flight), so the wait also covers the LDS stores.
-    constexpr int NW = W8 ? W_PER_T + (W_PER_T + 3) / 4
-                          : W_PER_T + (META == META_GROUP ? 2 * W_PER_T : META == META_ROW ? 2 : 0);
+    constexpr int NW = W_PER_T + (META == META_GROUP ? 2 * W_PER_T : META == META_ROW ? 2 : 0);
     typedef __attribute__((address_space(3))) void lds_void;
     auto dma_a = [&](int kt, int buf) {
       const uint32_t l0 = (uint32_t)((KB + kt) * BK);
@@ -910,46 +873,10 @@ hipError_t run_k(const MmArgs& a, const GemmPart& gp, float* part, hipStream_t s
   const dim3 grid((unsigned)nct, (unsigned)((a.M + BM - 1) / BM), (unsigned)splits);
   const int log2g = 31 - __builtin_clz((unsigned)a.group);
   k<<<grid, WM * WN * 64, lds, st>>>(a.A, a.packed, a.scales, a.zeros, a.ep, (int)a.M, (int)a.N, (int)a.K,
-                                      log2g, kts, gp.ct0, pw, splits > 1 ? part : nullptr, (int)L, 0);
+                                      log2g, kts, gp.ct0, pw, splits > 1 ? part : nullptr);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   return launch_splitk_reduce(part, splits, a.M, c_lo, pw, a.ep, st);
-}
-
-// run_k for the transposed product on int8 rows.
-template <int WM, int WN, int FM, int FN, int BK, bool F16>
-hipError_t run_k8(const MmArgs& a, const GemmPart& gp, float* part, hipStream_t st) {
-  constexpr int BM = WM * FM * 32, BN = WN * FN * 32;
-  // direct dY loads want no columns past N to zero: whole steps, or an aligned copy that holds zeros there
-  const bool dma = a.a_zeros || a.N % BK == 0;
-  auto k = dma ? gemm_kernel<true, WM, WN, FM, FN, BK, META_ROW, 1, 4, F16, true, true>
-               : gemm_kernel<true, WM, WN, FM, FN, BK, META_ROW, 1, 4, F16, false, true>;
-  const size_t lds = (size_t)2 * (BM * (dma ? BK : BK + 8) + BN * (BK + 8)) * 2;
-  if (lds > 64 * 1024) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)lds);
-    if (e != hipSuccess) return e;
-  }
-  const int kt_all = (int)((a.N + BK - 1) / BK);
-  const int kts = (kt_all + gp.splits - 1) / gp.splits;
-  const int splits = (kt_all + kts - 1) / kts;  // every slice gets at least one contraction step
-  const int tn_all = (int)((a.K + BN - 1) / BN);
-  const int nct = gp.nct > 0 ? gp.nct : tn_all - gp.ct0;
-  const int64_t c_lo = (int64_t)gp.ct0 * BN;
-  const int pw = (int)(std::min<int64_t>(a.K, c_lo + (int64_t)nct * BN) - c_lo);
-  const dim3 grid((unsigned)nct, (unsigned)((a.M + BM - 1) / BM), (unsigned)splits);
-  k<<<grid, WM * WN * 64, lds, st>>>(a.A, a.packed, reinterpret_cast<const uint16_t*>(a.scales8), nullptr, a.ep,
-                                     (int)a.M, (int)a.N, (int)a.K, 0, kts, gp.ct0, pw, splits > 1 ? part : nullptr,
-                                     (int)a.lda, (int)a.wpitch);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || splits == 1) return e;
-  return launch_splitk_reduce(part, splits, a.M, c_lo, pw, a.ep, st);
-}
-
-template <int WM, int WN, int FM, int FN, int BK>
-hipError_t run8(const MmArgs& a, const GemmPart& gp, float* part, hipStream_t st) {
-  return a.a_f16 ? run_k8<WM, WN, FM, FN, BK, true>(a, gp, part, st)
-                 : run_k8<WM, WN, FM, FN, BK, false>(a, gp, part, st);
 }
 
 template <bool TRANS, int WM, int WN, int FM, int FN, int BK, int STAGES, int META>
@@ -968,15 +895,6 @@ hipError_t run_meta(const MmArgs& a, const GemmPart& gp, float* part, hipStream_
 }
 
 hipError_t run_cfg(const MmArgs& a, int cfg, const GemmPart& gp, float* part, hipStream_t st) {
-  if (a.scales8 != nullptr) {
-    switch (cfg) {
-      case 0: return run8<2, 2, 4, 4, 64>(a, gp, part, st);
-      case 1: return run8<4, 2, 2, 2, 64>(a, gp, part, st);
-      case 8: return run8<1, 4, 1, 1, 64>(a, gp, part, st);
-      case 11: return run8<2, 4, 4, 2, 64>(a, gp, part, st);
-      default: return run8<2, 2, 2, 2, 32>(a, gp, part, st);
-    }
-  }
   if (a.transposed) {
     switch (cfg) {
       case 0: return run_meta<true, 2, 2, 4, 4, 64, 4>(a, gp, part, st);

@@ -43,13 +43,6 @@ struct MmArgs {
   int group;  // GROUPWISE g, else K
   bool transposed;
   bool a_f16;  // activations (and the weight operand) fp16 instead of bf16
-  // Transposed product on int8 rows (w8a16_mm_t): `packed` holds int8 codes with wpitch bytes a
-  // row and scales8 one fp32 scale a row (mode ROWWISE).  dY rows are lda elements apart
-  // (0: N, contiguous); a_zeros: lda is N rounded up to 64 and the columns past N hold zeros.
-  const float* scales8 = nullptr;
-  int64_t wpitch = 0;
-  int64_t lda = 0;
-  bool a_zeros = false;
 };
 
 // Properties of the current device that kernel plans depend on.
@@ -141,6 +134,20 @@ hipError_t launch_w8_mm(const W8Args& a, const DeviceCaps& caps, void* ws, size_
 bool w8_fused(int64_t M, int64_t K);
 bool w8_decode_supported(int64_t M);
 hipError_t launch_w8_decode(const W8Args& a, const DeviceCaps& caps, hipStream_t st);
+
+// Input gradient (w8_grad.hip): dY [M][N] 16-bit, row stride ld (a multiple of 8, as N), 16-byte
+// aligned.  L: columns of dY to read, N or (zeros past N) N rounded up to 64.
+struct W8GradArgs {
+  const uint16_t* dY;
+  bool f16;
+  int64_t ld, L;
+  const int8_t* W;
+  const float* w_scales;
+  Epi ep;
+  int64_t M, N, K, pitch;
+};
+size_t w8_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps);
+hipError_t launch_w8_grad(const W8GradArgs& a, const DeviceCaps& caps, void* ws, size_t ws_bytes, hipStream_t st);
 
 // dY [M][N] 16-bit, row stride ld -> out [M][npad], zeros past column N.
 hipError_t launch_pad_rows(const uint16_t* dY, int64_t M, int64_t N, int64_t ld, uint16_t* out, int64_t npad,

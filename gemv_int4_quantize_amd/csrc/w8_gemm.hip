@@ -277,19 +277,6 @@ __global__ __launch_bounds__(256) void w8_reduce_kernel(const int* __restrict__ 
   }
 }
 
-// dY rows copied to an aligned pitch, zeros past column N (w8a16_mm_t).
-__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ x, int64_t N, int64_t ld,
-                                                       uint16_t* __restrict__ out, int64_t npad) {
-  const int64_t row = blockIdx.y;
-  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (c >= npad) return;
-  const uint16_t* p = x + row * ld + c;
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (c + 8 <= N) v = load_raw8<W4_DT_BF16>(p).q[0];
-  else if (c < N) v = load_raw8_part<W4_DT_BF16>(p, (int)(N - c), 0u).q[0];
-  *reinterpret_cast<u32x4*>(out + row * npad + c) = v;
-}
-
 }  // namespace
 
 namespace {
@@ -395,19 +382,6 @@ hipError_t launch_w8_mm(const W8Args& a, const DeviceCaps& caps, void* ws, size_
     case 3: return run_ring<2, 2, 2, 1, 3>(a, p.splits, part, st);
     default: return run_ring<2, 2, 1, 1, 4>(a, p.splits, part, st);
   }
-}
-
-hipError_t launch_pad_rows(const uint16_t* dY, int64_t M, int64_t N, int64_t ld, uint16_t* out, int64_t npad,
-                           hipStream_t st) {
-  // grid.y is limited to 65535 rows a launch
-  for (int64_t m = 0; m < M; m += 32768) {
-    const int64_t n = M - m < 32768 ? M - m : 32768;
-    pad_rows_kernel<<<dim3((unsigned)((npad / 8 + 255) / 256), (unsigned)n), 256, 0, st>>>(dY + m * ld, N, ld,
-                                                                                           out + m * npad, npad);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
 }
 
 }  // namespace w4

@@ -317,6 +317,16 @@ def test_gradient_formula(m, n, k, pad, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k,pad,dtype", [
+    (700, 200, 23000, 0, torch.bfloat16),   # whole rounds of tall tiles, the columns left in lower ones
+    (513, 72, 33000, 8, torch.float16), (2048, 136, 11008, 0, torch.float16),
+    (300, 1000, 5000, 0, torch.bfloat16), (33, 4104, 2080, 0, torch.float16),  # split contractions
+    (130, 2027, 515, 3, torch.bfloat16), (1, 8192, 64, 0, torch.bfloat16), (65, 8, 257, 0, torch.float16)])
+def test_gradient_plans(m, n, k, pad, dtype):
+    test_gradient_formula(m, n, k, pad, dtype)
+
+
+@pytest.mark.gpu
 def test_gradient_misaligned():
     w, _, _ = _weight(11, 200, 96)
     buf = torch.randn(50 * 200 + 8, device=DEV).to(torch.bfloat16)
