@@ -19,7 +19,7 @@ using w4::ok;
 
 constexpr int64_t kMaxK = (int64_t)1 << 17;    // int32 sums: 128 * 128 * K < 2^31
 constexpr int64_t kMaxScored = ((int64_t)1 << 31) - 65536;  // rows and columns of scores
-constexpr int64_t kMaxRows = (int64_t)1 << 30;   // a launch holds fewer than 2^32 threads
+constexpr int64_t kMaxRows = ((int64_t)1 << 30) - 1;   // a launch holds fewer than 2^32 threads
 constexpr int64_t kMaxTop = 64;
 
 int64_t pitch_of(int64_t cols) { return (cols + 63) / 64 * 64; }
@@ -32,7 +32,7 @@ int check_sizes(int64_t M, int64_t N, int64_t K) {
   if (M < 0) return fail(W4_ERR_INVALID, "M = %lld must be >= 0", (long long)M);
   if (N < 1 || K < 1) return fail(W4_ERR_INVALID, "N = %lld and K = %lld must be >= 1", (long long)N, (long long)K);
   if (K >= kMaxK) return fail(W4_ERR_UNSUPPORTED, "K = %lld must be below 2^17 (int32 sums)", (long long)K);
-  if (M > kMaxRows || N > kMaxRows) return fail(W4_ERR_UNSUPPORTED, "M and N must be at most 2^30");
+  if (M > kMaxRows || N > kMaxRows) return fail(W4_ERR_UNSUPPORTED, "M and N must be below 2^30");
   return W4_OK;
 }
 

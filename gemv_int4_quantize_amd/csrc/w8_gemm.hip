@@ -46,43 +46,19 @@ constexpr int BK = 128;
 // What bounds it: at 8192^3 2359 TOP/s; the matrix cores are busy 68% of the cycles and the
 // clock is down to 1.65 GHz under the load (the same product of zeros runs 1.2 times faster).
 template <int WM, int WN, int FM, int FN, int NB>
-__global__ __launch_bounds__(WM * WN * 64) void w8_ring_kernel(const int8_t* __restrict__ A, const float* __restrict__ sa,
-                                                               const int8_t* __restrict__ W, const float* __restrict__ sw,
-                                                               const Epi ep, int M, int N, int pitch, int tm, int tn,
-                                                               int kt_per_slice, int* __restrict__ part) {
+__device__ __forceinline__ void ring_tile(char* smem, const int8_t* __restrict__ A, const float* __restrict__ sa,
+                                          const int8_t* __restrict__ W, const float* __restrict__ sw, const Epi& ep, int M,
+                                          int N, int pitch, int m0, int n0, int slice, int kt_per_slice,
+                                          int* __restrict__ part) {
   constexpr int T = WM * WN * 64, BM = WM * FM * 32, BN = WN * FN * 32;
   constexpr int CH = BK / 16, UA = BM * CH / T, UB = BN * CH / T;  // chunks a thread loads of each tile in a stage
   constexpr int STAGE = (BM + BN) * BK;
   constexpr int SUB = BK / 32;  // products along a stage
   auto swz = [](int row) { return (row >> 1) & 7; };
   static_assert(BM * CH % T == 0 && BN * CH % T == 0, "tile split");
-  extern __shared__ __attribute__((aligned(16))) char smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  // Workgroups go to the eight XCDs (each with an L2 of its own) in turn.  The smaller tiles,
-  // which the L2 feeds, give each XCD a contiguous part of the work, in the order: slices, groups
-  // of eight tile rows, tile columns, rows of the group, so that the 32 tiles of an XCD at a
-  // time are about 8 x 4 (measured, 128 x 128 tiles: M = 1024, (4096, 4096) 32 -> 22 us,
-  // M = 512, (8192, 2048) 19 -> 15 us).  The 256 x 256 tiles, bound by the matrix cores, are
-  // 2-3% faster in plain order.
-  int slice, ti, tj;
-  if constexpr (BM * BN == 256 * 256) {
-    slice = blockIdx.x / (unsigned)(tm * tn);
-    const int tile = blockIdx.x - slice * tm * tn;
-    ti = tile % tm;
-    tj = tile / tm;
-  } else {
-    const int per_xcd = gridDim.x >> 3, left = gridDim.x & 7, xcd = blockIdx.x & 7;
-    const int work = xcd * per_xcd + min(xcd, left) + (blockIdx.x >> 3);
-    slice = work / (tm * tn);
-    const int tile = work - slice * tm * tn;
-    const int grp = tile / (8 * tn), in_grp = tile - grp * 8 * tn, rows_grp = min(8, tm - grp * 8);
-    ti = grp * 8 + in_grp % rows_grp;
-    tj = in_grp / rows_grp;
-  }
-  const int m0 = ti * BM, n0 = tj * BN;
-
   const rsrc_t ra = make_rsrc(A + (size_t)m0 * pitch, (uint32_t)min(BM, M - m0) * (uint32_t)pitch);
   const rsrc_t rb = make_rsrc(W + (size_t)n0 * pitch, (uint32_t)min(BN, N - n0) * (uint32_t)pitch);
   int oa[UA], ob[UB];
@@ -216,13 +192,13 @@ __global__ __launch_bounds__(WM * WN * 64) void w8_ring_kernel(const int8_t* __r
     return;
   }
   const bool wide = epi_wide(ep, N) != 0;
-  const rsrc_t rs = make_rsrc(sa + m0, (uint32_t)min(BM, M - m0) * 4u);
+  const rsrc_t rs = make_rsrc(sa, (uint32_t)M * 4u);  // M < 2^30
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     float s[16];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (rbase - m0 + i * 32 + g * 8) * 4, 0, 0));
+      const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)((uint32_t)(rbase + i * 32 + g * 8) * 4u), 0, 0));
 #pragma unroll
       for (int q = 0; q < 4; ++q) s[g * 4 + q] = __uint_as_float(v[q]);
     }
@@ -244,6 +220,48 @@ __global__ __launch_bounds__(WM * WN * 64) void w8_ring_kernel(const int8_t* __r
         }
       }
     }
+  }
+}
+
+// Tiles of one kind (tm x tn), all of them once for each slice of kt_per_slice stages.
+// Workgroups go to the eight XCDs (each with an L2 of its own) in turn.  These tiles, which the L2
+// feeds, give each XCD a contiguous part of the work, in the order: slices, groups of eight tile
+// rows, tile columns, rows of the group, so that the 32 tiles of an XCD at a time are about
+// 8 x 4 (measured, 128 x 128 tiles: M = 1024, (4096, 4096) 32 -> 22 us, M = 512, (8192, 2048)
+// 19 -> 15 us).
+template <int WM, int WN, int FM, int FN, int NB>
+__global__ __launch_bounds__(WM * WN * 64) void w8_ring_kernel(const int8_t* __restrict__ A, const float* __restrict__ sa,
+                                                               const int8_t* __restrict__ W, const float* __restrict__ sw,
+                                                               const Epi ep, int M, int N, int pitch, int tm, int tn,
+                                                               int kt_per_slice, int* __restrict__ part) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int per_xcd = gridDim.x >> 3, left = gridDim.x & 7, xcd = blockIdx.x & 7;
+  const int work = xcd * per_xcd + min(xcd, left) + (blockIdx.x >> 3);
+  const int slice = work / (tm * tn), tile = work - slice * tm * tn;
+  const int grp = tile / (8 * tn), in_grp = tile - grp * 8 * tn, rows_grp = min(8, tm - grp * 8);
+  const int ti = grp * 8 + in_grp % rows_grp, tj = in_grp / rows_grp;
+  ring_tile<WM, WN, FM, FN, NB>(smem, A, sa, W, sw, ep, M, N, pitch, ti * WM * FM * 32, tj * WN * FN * 32, slice,
+                                kt_per_slice, part);
+}
+
+// The first `full` of tn column tiles in `high` 256-row tiles each, the columns left in `low`
+// (FL 64)-row tiles.  In plain order: these tiles, bound by the matrix cores, are 2-3% faster so.
+template <int FL>
+__global__ __launch_bounds__(512) void w8_mixed_kernel(const int8_t* __restrict__ A, const float* __restrict__ sa,
+                                                       const int8_t* __restrict__ W, const float* __restrict__ sw,
+                                                       const Epi ep, int M, int N, int pitch, int full, int tn, int high,
+                                                       int low, int kt_per_slice, int* __restrict__ part) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int n_high = full * high, n_all = n_high + (tn - full) * low;
+  const int slice = blockIdx.x / (unsigned)n_all;
+  const int tile = blockIdx.x - slice * n_all;
+  if (tile < n_high) {
+    ring_tile<2, 4, 4, 2, 2>(smem, A, sa, W, sw, ep, M, N, pitch, tile % high * 256, tile / high * 256, slice,
+                             kt_per_slice, part);
+  } else {
+    const int t = tile - n_high;
+    ring_tile<2, 4, FL, 2, 2>(smem, A, sa, W, sw, ep, M, N, pitch, t % low * FL * 64, (t / low + full) * 256, slice,
+                              kt_per_slice, part);
   }
 }
 
@@ -281,23 +299,41 @@ __global__ __launch_bounds__(256) void w8_reduce_kernel(const int* __restrict__ 
 
 namespace {
 
-template <int WM, int WN, int FM, int FN, int NB>
-hipError_t run_ring(const W8Args& a, int splits, int* part, hipStream_t st) {
-  constexpr int BM = WM * FM * 32, BN = WN * FN * 32;
-  auto k = w8_ring_kernel<WM, WN, FM, FN, NB>;
+struct W8Plan {
+  int tile = 0, full = 0, splits = 1;
+};
+
+// FL > 0: the 256 x 256 tiles mixed with (FL 64) x 256 ones.
+template <int WM, int WN, int FM, int FN, int NB, int FL = 0>
+hipError_t run_ring(const W8Args& a, const W8Plan& p, int* part, hipStream_t st) {
+  static_assert(FL == 0 || (WM == 2 && WN == 4 && FM == 4 && FN == 2 && NB == 2), "w8_mixed_kernel's tile");
+  constexpr int BM = WM * FM * 32, BN = WN * FN * 32, T = WM * WN * 64;
   constexpr int lds = NB * (BM + BN) * BK;
-  if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  const int M = (int)a.M, N = (int)a.N, pitch = (int)a.pitch;
+  const int tm = (M + BM - 1) / BM, tn = (N + BN - 1) / BN;
+  const int kt = (pitch + BK - 1) / BK;
+  const int per = (kt + p.splits - 1) / p.splits;
+  const int splits = (kt + per - 1) / per;  // every slice gets at least one stage
+  if (splits == 1) part = nullptr;
+  auto prepare = [](auto k) {
+    if (lds <= 64 * 1024) return hipSuccess;
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  };
+  hipError_t e;
+  if constexpr (FL > 0) {
+    e = prepare(w8_mixed_kernel<FL>);
     if (e != hipSuccess) return e;
+    const int low = (M + FL * 64 - 1) / (FL * 64);
+    const int64_t wgs = ((int64_t)p.full * tm + (int64_t)(tn - p.full) * low) * splits;
+    w8_mixed_kernel<FL><<<(unsigned)wgs, T, lds, st>>>(a.A, a.a_scales, a.W, a.w_scales, a.ep, M, N, pitch, p.full, tn, tm,
+                                                       low, per, part);
+  } else {
+    e = prepare(w8_ring_kernel<WM, WN, FM, FN, NB>);
+    if (e != hipSuccess) return e;
+    w8_ring_kernel<WM, WN, FM, FN, NB><<<(unsigned)((int64_t)tm * tn * splits), T, lds, st>>>(
+        a.A, a.a_scales, a.W, a.w_scales, a.ep, M, N, pitch, tm, tn, per, part);
   }
-  const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
-  const int kt = (int)((a.pitch + BK - 1) / BK);
-  const int per = (kt + splits - 1) / splits;
-  splits = (kt + per - 1) / per;  // every slice gets at least one stage
-  k<<<(unsigned)(tm * tn * splits), WM * WN * 64, lds, st>>>(a.A, a.a_scales, a.W, a.w_scales, a.ep, (int)a.M, (int)a.N,
-                                                             (int)a.pitch, (int)tm, (int)tn, per,
-                                                             splits > 1 ? part : nullptr);
-  hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   const size_t total = (size_t)a.M * a.N;
   if (a.N % 4 == 0)
@@ -310,43 +346,53 @@ hipError_t run_ring(const W8Args& a, int splits, int* part, hipStream_t st) {
 // Tiles, and what one stage of them takes, in us on MI355X (fitted to some 20 sizes from
 // (M, N, K) = (20, 2048, 2048) to 8192^3): lat, the least time of a stage; mfma, a workgroup's
 // share of the CU's matrix cores; bw, the LDS fill rate of the whole device in TB/s; and t0, a
-// launch's start, first loads and stores.
+// launch's start, first loads and stores.  bl: rows of the lower tiles that the 256-row ones are
+// mixed with, and low: a stage of theirs.
 struct Tile {
   const char* name;
   int bm, bn, slots;  // slots: workgroups that a CU's LDS holds
   double t0, lat, mfma, bw;
+  int bl;
+  double low;
 };
 constexpr Tile kTiles[] = {
-    {"w8_256x256", 256, 256, 1, 9.0, 1.45, 1.80, 18.0}, {"w8_256x128", 256, 128, 1, 6.5, 0.75, 1.03, 18.0},
-    {"w8_128x128", 128, 128, 1, 5.2, 0.47, 0.55, 18.0}, {"w8_128x64", 128, 64, 2, 4.7, 0.38, 0.33, 18.0},
-    {"w8_64x64", 64, 64, 2, 4.4, 0.22, 0.23, 12.0},
-};
-
-struct W8Plan {
-  int tile = 0, splits = 1;
+    {"w8_256x256", 256, 256, 1, 9.0, 1.45, 1.80, 18.0, 192, 1.42},
+    {"w8_256x256", 256, 256, 1, 9.0, 1.45, 1.80, 18.0, 128, 1.03},
+    {"w8_256x128", 256, 128, 1, 6.5, 0.75, 1.03, 18.0, 0, 0.0},
+    {"w8_128x128", 128, 128, 1, 5.2, 0.47, 0.55, 18.0, 0, 0.0},
+    {"w8_128x64", 128, 64, 2, 4.7, 0.38, 0.33, 18.0, 0, 0.0},
+    {"w8_64x64", 64, 64, 2, 4.4, 0.22, 0.23, 12.0, 0, 0.0},
 };
 
 // The plan with the least estimated time: rounds of workgroups, each the contraction's stages at
 // the longest of the three figures above; a split adds a launch (3 us) and the write and read of
-// its int32 planes (8 TB/s: they fit the caches).
+// its int32 planes (8 TB/s: they fit the caches).  The 256 x 256 tiles take all of the columns, or
+// those that make whole rounds, or none, and the lower tiles the others in a shorter last round
+// (M = 3000, (8192, 2048) 62.9 -> 58.8 us, M = 2048, (11008, 4096) 100.5 -> 97.9).
 W8Plan pick(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps, bool allow_split) {
   const int64_t cus = caps.cus > 0 ? caps.cus : 256, kt = ((K + 63) / 64 * 64 + BK - 1) / BK;
   W8Plan best;
   double best_t = 1e30;
   for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
     const Tile& c = kTiles[i];
-    const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+    const int64_t rows = (M + c.bm - 1) / c.bm, tn = (N + c.bn - 1) / c.bn;
     for (int sp = 1; sp <= (allow_split ? 8 : 1); sp *= 2) {
       if (sp > 1 && kt / sp < 4) break;
-      const int64_t wgs = tiles * sp, steps = (kt + sp - 1) / sp;
-      const int64_t rounds = (wgs + cus * c.slots - 1) / (cus * c.slots);
-      const int64_t resident = std::min(wgs, cus * c.slots), per_cu = (resident + cus - 1) / cus;
-      const double fill = (double)resident * (c.bm + c.bn) * BK / c.bw * 1e-6;
-      const double stage = std::max(std::max(c.lat, c.mfma * per_cu), fill);
-      const double t = c.t0 + rounds * steps * stage + (sp > 1 ? 3.0 + sp * M * N * 8.0 / 8.0 * 1e-6 : 0.0);
-      if (t < best_t) {
-        best_t = t;
-        best = W8Plan{i, sp};
+      const int64_t steps = (kt + sp - 1) / sp;
+      for (const int64_t full : {tn, rows * tn / cus * cus / rows, (int64_t)0}) {
+        if (full < tn && c.bl == 0) break;
+        const int64_t wgs = rows * full * sp;
+        const int64_t rounds = (wgs + cus * c.slots - 1) / (cus * c.slots);
+        const int64_t resident = std::min(wgs, cus * c.slots), per_cu = (resident + cus - 1) / cus;
+        const double fill = (double)resident * (c.bm + c.bn) * BK / c.bw * 1e-6;
+        const double stage = std::max(std::max(c.lat, c.mfma * per_cu), fill);
+        const int64_t lows = full < tn ? (tn - full) * ((M + c.bl - 1) / c.bl) * sp : 0;
+        const double t = c.t0 + rounds * steps * stage + (double)((lows + cus - 1) / cus * steps) * c.low +
+                         (sp > 1 ? 3.0 + sp * M * N * 8.0 / 8.0 * 1e-6 : 0.0);
+        if (t < best_t) {
+          best_t = t;
+          best = W8Plan{i, (int)full, sp};
+        }
       }
     }
   }
@@ -362,11 +408,13 @@ size_t w8_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceCaps& 
 }
 
 const char* w8_mm_name(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps) {
-  static thread_local char buf[32];
+  static thread_local char buf[48];
   if (w8_decode_supported(M)) return w8_fused(M, K) ? "w8_decode_fused" : "w8_decode";
   const W8Plan p = pick(M, N, K, caps, true);
-  if (p.splits == 1) return kTiles[p.tile].name;
-  snprintf(buf, sizeof(buf), "%s_splitk%d", kTiles[p.tile].name, p.splits);
+  const Tile& c = kTiles[p.tile];
+  int at = snprintf(buf, sizeof(buf), "%s", c.name);
+  if (p.full < (N + c.bn - 1) / c.bn) at += snprintf(buf + at, sizeof(buf) - at, "+%dx256", c.bl);
+  if (p.splits > 1) snprintf(buf + at, sizeof(buf) - at, "_splitk%d", p.splits);
   return buf;
 }
 
@@ -376,11 +424,12 @@ hipError_t launch_w8_mm(const W8Args& a, const DeviceCaps& caps, void* ws, size_
   if (plan_bytes(a.M, a.N, p) > ws_bytes) p = pick(a.M, a.N, a.K, caps, false);
   int* part = static_cast<int*>(ws);
   switch (p.tile) {
-    case 0: return run_ring<2, 4, 4, 2, 2>(a, p.splits, part, st);
-    case 1: return run_ring<4, 2, 2, 2, 3>(a, p.splits, part, st);
-    case 2: return run_ring<4, 2, 1, 2, 3>(a, p.splits, part, st);
-    case 3: return run_ring<2, 2, 2, 1, 3>(a, p.splits, part, st);
-    default: return run_ring<2, 2, 1, 1, 4>(a, p.splits, part, st);
+    case 0: return run_ring<2, 4, 4, 2, 2, 3>(a, p, part, st);
+    case 1: return run_ring<2, 4, 4, 2, 2, 2>(a, p, part, st);
+    case 2: return run_ring<4, 2, 2, 2, 3>(a, p, part, st);
+    case 3: return run_ring<4, 2, 1, 2, 3>(a, p, part, st);
+    case 4: return run_ring<2, 2, 2, 1, 3>(a, p, part, st);
+    default: return run_ring<2, 2, 1, 1, 4>(a, p, part, st);
   }
 }
 

@@ -49,7 +49,7 @@ constexpr int BK = 64;  // contraction rows of a stage
 template <int WN, int FM, bool F16>
 __device__ __forceinline__ void grad_tile(char* smem, const uint16_t* __restrict__ dY, const int8_t* __restrict__ W,
                                           const float* __restrict__ sw, const Epi& ep, int M, int N, int L, int K, int ld,
-                                          int pitch, int m0, int c0, int k0, int KT, float* __restrict__ part) {
+                                          int pitch, int m0, int c0, int slice, int per, float* __restrict__ part) {
   constexpr int T = WN * 64, BM = FM * 32, BN = WN * 32, NB = 3;
   constexpr int UA = BM * 8 / T, CB = BN / 16, UB = BK * CB / T;  // chunks a thread loads in a stage
   static_assert(BM * 8 % T == 0 && BK * CB % T == 0, "tile split");
@@ -70,6 +70,7 @@ __device__ __forceinline__ void grad_tile(char* smem, const uint16_t* __restrict
     const int u = tid + i * T, row = u / CB;
     ob[i] = row * pitch + c0 + (((u % CB) ^ (2 * (row & 7) & (CB - 1))) << 4);
   }
+  const int k0 = slice * per, KT = min((N + BK - 1) / BK - k0, per);  // this slice's stages
   // loads [lo, hi) of stage kt into ring slot `slot`; past the end the last stage again, never
   // read.  dY's columns past its last one are asked for out of range and so 0.
   constexpr int UL = UA + UB + 1;
@@ -191,12 +192,13 @@ __device__ __forceinline__ void grad_tile(char* smem, const uint16_t* __restrict
   }
   if (c >= K) return;
   if (part != nullptr) {  // a slice's sums go to its own [M][K] plane
+    float* out = part + (size_t)slice * M * K + c;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int m = mbase + i * 32 + (r >> 2) * 8 + (r & 3);
-        if (m < M) part[(size_t)m * K + c] = acc[i][r];
+        if (m < M) out[(size_t)m * K] = acc[i][r];
       }
     return;
   }
@@ -236,14 +238,12 @@ __global__ __launch_bounds__(WN * 64) void w8_grad_kernel(const uint16_t* __rest
   const int tile = high ? at : xcd * per_xcd + min(xcd, left) + (at >> 3);
   const int grp = tile / (8 * cols), in_grp = tile - grp * 8 * cols, rows_grp = min(8, rows - grp * 8);
   const int tr = grp * 8 + in_grp % rows_grp, tc = in_grp / rows_grp + (high ? 0 : g.full);
-  const int k0 = slice * g.per, KT = min((N + BK - 1) / BK - k0, g.per);
-  float* plane = part == nullptr ? nullptr : part + (size_t)slice * M * K;
   if constexpr (FB > 0)
     if (high) {
-      grad_tile<WN, FB, F16>(smem, dY, W, sw, ep, M, N, L, K, ld, pitch, tr * FB * 32, tc * WN * 32, k0, KT, plane);
+      grad_tile<WN, FB, F16>(smem, dY, W, sw, ep, M, N, L, K, ld, pitch, tr * FB * 32, tc * WN * 32, slice, g.per, part);
       return;
     }
-  grad_tile<WN, FM, F16>(smem, dY, W, sw, ep, M, N, L, K, ld, pitch, tr * FM * 32, tc * WN * 32, k0, KT, plane);
+  grad_tile<WN, FM, F16>(smem, dY, W, sw, ep, M, N, L, K, ld, pitch, tr * FM * 32, tc * WN * 32, slice, g.per, part);
 }
 
 // Tiles of WN * 32 columns: FB * 32 rows (0: none) and FM * 32 rows, and what one stage of them

@@ -32,7 +32,7 @@ int64_t w8_pitch(int64_t cols);
  * in IEEE fp32, ties to even, so |q| <= 127 and |x - q s| <= s / 2 up to fp32 rounding.
  * The floor on s keeps 1 / s finite; a row of zeros gets codes 0.  A row that holds a NaN
  * or an infinity gets scale NaN and codes 0, so its products are NaN.  Columns
- * cols .. P-1 of codes are written as 0.  rows == 0 is a no-op; rows <= 2^30, 1 <= cols < 2^17. */
+ * cols .. P-1 of codes are written as 0.  rows == 0 is a no-op; rows < 2^30, 1 <= cols < 2^17. */
 int w8_quantize_rows(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld, int8_t* codes, float* scales,
                      void* stream);
 
@@ -44,7 +44,7 @@ int w8a16_mm_t_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ld, size
 /* Y[m][n] = out_rne((fp32(sum_k A[m][k] W[n][k]) * w_scales[n]) * a_scales[m] + bias[n]) on
  * int8 rows A [M][K] and W [N][K]; the sum is exact in int32.  Output dtype, bias and
  * segments as for w4a16_mm_out (the segment columns sum to N).  M == 0 is a no-op.
- * M, N <= 2^30, 1 <= K < 2^17.  The workspace is optional: with the bytes that w8a8_workspace_bytes
+ * M, N < 2^30, 1 <= K < 2^17.  The workspace is optional: with the bytes that w8a8_workspace_bytes
  * reports (16-byte aligned) a product with few output tiles splits its contraction; the
  * result is the same, bit for bit. */
 int w8a8_mm(const int8_t* A, const float* a_scales, int64_t M, const int8_t* W, const float* w_scales, int64_t N,

@@ -241,6 +241,25 @@ def test_product(m, n, k, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(700, 23000, 640), (3000, 8192, 2048), (1500, 8600, 1030), (2048, 11008, 4096),
+                                   (2060, 9000, 520)])
+def test_product_mixed_tiles(m, n, k):
+    """Whole rounds of 256-row tiles and lower ones for the columns left, where the plan says so."""
+    g = torch.Generator(device=DEV).manual_seed(m + n)
+    a, w = (w4.quantize_int8(torch.randn(r, k, device=DEV, generator=g)) for r in (m, n))
+    y = w4.mm_int8(a, w)
+    # exact in double
+    ref = (a.codes.double() @ w.codes.double().t()) * a.scales.double()[:, None] * w.scales.double()
+    assert ((y.double() - ref).abs() <= ref.abs() * 2.0**-22).all()  # three fp32 roundings
+    assert torch.equal(w4.mm_int8(a, w), y)
+
+
+def test_product_plans():
+    names = [w4.int8_kernel_for(*s) for s in ((3000, 8192, 2048), (2048, 11008, 4096), (8192, 8192, 8192))]
+    assert "+" in names[0] and "+" in names[1] and names[2] == "w8_256x256"
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("m", [1, 2, 20, 130])
 def test_product_extreme_codes(m):
     """Sums near the int32 limit: K = 131071 codes of -128 and 127."""
