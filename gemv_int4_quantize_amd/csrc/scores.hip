@@ -17,6 +17,11 @@
 // the pairs' chunks again cost 17 us of 112 at M = 2048, V = 128256 bf16.)  Rows with too many
 // logits at the threshold (many equal ones, or fewer unmasked than alternatives) collect
 // those above it, and of those equal to it the lowest ids in order, from the pairs' chunks.
+//
+// Both directions are bound by memory.  Measured at M = 2048, V = 128256 bf16: forward without
+// alternatives 98 us, with five 104 (5.1 TB/s), gradient 205 us (5.1 TB/s of reads and
+// writes; stores that bypass the caches, 319 -> 302 us for the pair).  Four fp32 rows with
+// twenty alternatives: 10 us and 5 for the join, both mostly latency.
 #include <algorithm>
 
 #include "api_common.h"

