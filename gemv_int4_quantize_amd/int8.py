@@ -118,6 +118,17 @@ def quantize_int8(x: torch.Tensor) -> Int8Rows:
     return out
 
 
+_ONE = _lib.W4OutSeg * 1
+
+
+def _new_output(M: int, width: int, dt: torch.dtype, device):
+    """A tensor [M][width] for a result, and its segment."""
+    if dt not in _ODT:
+        raise ValueError(f"outputs must be float32, float16 or bfloat16 (got {dt})")
+    out = torch.empty((M, width), dtype=dt, device=device)
+    return out, _ONE((out.data_ptr(), width, width))
+
+
 def _segments(outs, M: int, width: int, dt: torch.dtype):
     if dt not in _ODT:
         raise ValueError(f"outputs must be float32, float16 or bfloat16 (got {dt})")
@@ -149,8 +160,8 @@ def _gradient_bytes(M: int, N: int, K: int, ld: int) -> int:
     return size.value
 
 
-def _product(a, w: Int8Rows, bias, outs, dt: torch.dtype):
-    """One product written to `outs`, which cover its columns in order."""
+def _product(a, w: Int8Rows, bias, outs, dt: torch.dtype, segs=None):
+    """One product written to `outs`, which cover its columns in order (segs: theirs, if made)."""
     N, K = w.rows, w.cols
     _check_rows(w, "weight")
     if bias is not None and (bias.dtype != dt or bias.numel() != N or not bias.is_contiguous()):
@@ -164,7 +175,8 @@ def _product(a, w: Int8Rows, bias, outs, dt: torch.dtype):
         x, xs, xdt = a, None, _WDT[a.dtype]
     if width != K:
         raise ValueError(f"activation width {width} does not match the weight ({N}x{K})")
-    segs = _segments(outs, M, N, dt)
+    if segs is None:
+        segs = _segments(outs, M, N, dt)
     L = lib()
     with on_device(check_device(x, xs, w.codes, w.scales, bias, *outs)):
         size = _product_bytes(M, N, K, xdt)
@@ -193,11 +205,12 @@ def mm_int8(a, w: Int8Rows, bias: torch.Tensor | None = None, out: torch.Tensor 
     dev = w.codes.device
     M = a.rows if isinstance(a, Int8Rows) else a.shape[0]
     dt = out_dtype if out_dtype is not None else (out.dtype if out is not None else torch.float32)
+    segs = None
     if out is None:
-        out = torch.empty((M, w.rows), dtype=dt, device=dev)
+        out, segs = _new_output(M, w.rows, dt, dev)
     elif out.shape != (M, w.rows) or out.dtype != dt:
         raise ValueError(f"out must be a {dt} tensor of shape ({M}, {w.rows})")
-    _product(a, w, bias, [out], dt)
+    _product(a, w, bias, (out,), dt, segs)
     return out
 
 
@@ -228,10 +241,11 @@ def mm_int8_t(dy: torch.Tensor, w: Int8Rows, out: torch.Tensor | None = None,
     _check_rows(w, "weight")
     dt = out_dtype if out_dtype is not None else (out.dtype if out is not None else torch.float32)
     if out is None:
-        out = torch.empty((M, K), dtype=dt, device=dy.device)
+        out, segs = _new_output(M, K, dt, dy.device)
     elif out.shape != (M, K) or out.dtype != dt:
         raise ValueError(f"out must be a {dt} tensor of shape ({M}, {K})")
-    segs = _segments([out], M, K, dt)
+    else:
+        segs = _segments((out,), M, K, dt)
     ld = _row_stride(dy)
     with on_device(check_device(dy, w.codes, w.scales, out)):
         size = _gradient_bytes(M, N, K, ld if dy.data_ptr() % 16 == 0 else -1)
