@@ -247,7 +247,7 @@ __global__ __launch_bounds__(WN * 64) void w8_grad_kernel(const uint16_t* __rest
 }
 
 // Tiles of WN * 32 columns: FB * 32 rows (0: none) and FM * 32 rows, and what one stage of them
-// takes, in us on MI355X (fitted to M = 32, 131, 512 and 2048): high, of an FB tile; lat, the
+// takes, in us on MI355X (fitted to some 20 sizes, M = 8 to 5000): high, of an FB tile; lat, the
 // least time of a stage of an FM tile; mfma, a workgroup's share of the CU's matrix cores; and t0,
 // a launch's start, first loads and stores.
 struct Tile {
@@ -255,10 +255,10 @@ struct Tile {
   double t0, high, lat, mfma;
 };
 constexpr Tile kTiles[] = {
-    {8, 8, 4, 1, 9.0, 1.70, 0.95, 0.95},
+    {8, 8, 4, 1, 9.0, 1.70, 0.78, 0.95},
     {4, 0, 4, 2, 6.0, 0.00, 0.56, 0.50},
     {4, 0, 2, 3, 5.0, 0.00, 0.48, 0.32},
-    {4, 0, 1, 4, 5.0, 0.00, 0.46, 0.22},
+    {4, 0, 1, 4, 5.0, 0.00, 0.46, 0.28},
 };
 
 struct GradPlan {
@@ -285,7 +285,9 @@ GradPlan pick(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps, bool allo
       for (const int64_t full : {(int64_t)0, some, high > 0 ? tn : 0}) {
         const int64_t a = full * high * sp, b = (tn - full) * low * sp;
         const int64_t rounds = (b + cus * c.slots - 1) / (cus * c.slots);
-        const int64_t per_cu = (std::min(b, cus * c.slots) + cus - 1) / cus;
+        // workgroups of the fullest CU; a round that leaves CUs idle runs at a higher clock
+        const int64_t resident = std::min(b, cus * c.slots);
+        const double per_cu = resident <= cus ? (double)resident / cus : (double)((resident + cus - 1) / cus);
         const double t = c.t0 + (double)((a + cus - 1) / cus * steps) * c.high +
                          (double)(rounds * steps) * std::max(c.lat, c.mfma * per_cu) +
                          (sp > 1 ? 3.0 + sp * M * K * 8.0 / 8.0 * 1e-6 : 0.0);
