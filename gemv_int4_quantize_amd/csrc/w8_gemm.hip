@@ -343,11 +343,12 @@ hipError_t run_ring(const W8Args& a, const W8Plan& p, int* part, hipStream_t st)
   return hipGetLastError();
 }
 
-// Tiles, and what one stage of them takes, in us on MI355X (fitted to some 20 sizes from
-// (M, N, K) = (20, 2048, 2048) to 8192^3): lat, the least time of a stage; mfma, a workgroup's
-// share of the CU's matrix cores; bw, the LDS fill rate of the whole device in TB/s; and t0, a
-// launch's start, first loads and stores.  bl: rows of the lower tiles that the 256-row ones are
-// mixed with, and low: a stage of theirs.
+// Tiles, and what one stage of them takes, in us on MI355X (fitted to 33 sizes from
+// (M, N, K) = (8, 4096, 4096) to (2048, 12288, 4096), where the plan is within 1% of the best of
+// all tiles and splits): lat, the least time of a stage; mfma, a workgroup's share of the CU's
+// matrix cores; bw, the LDS fill rate of the whole device in TB/s; and t0, a launch's start,
+// first loads and stores.  bl: rows of the lower tiles that the 256-row ones are mixed with, and
+// low: a stage of theirs.
 struct Tile {
   const char* name;
   int bm, bn, slots;  // slots: workgroups that a CU's LDS holds
@@ -356,19 +357,20 @@ struct Tile {
   double low;
 };
 constexpr Tile kTiles[] = {
-    {"w8_256x256", 256, 256, 1, 9.0, 1.45, 1.80, 18.0, 192, 1.42},
-    {"w8_256x256", 256, 256, 1, 9.0, 1.45, 1.80, 18.0, 128, 1.03},
-    {"w8_256x128", 256, 128, 1, 6.5, 0.75, 1.03, 18.0, 0, 0.0},
-    {"w8_128x128", 128, 128, 1, 5.2, 0.47, 0.55, 18.0, 0, 0.0},
-    {"w8_128x64", 128, 64, 2, 4.7, 0.38, 0.33, 18.0, 0, 0.0},
-    {"w8_64x64", 64, 64, 2, 4.4, 0.22, 0.23, 12.0, 0, 0.0},
+    {"w8_256x256", 256, 256, 1, 8.0, 1.35, 1.81, 18.0, 192, 1.25},
+    {"w8_256x256", 256, 256, 1, 8.0, 1.35, 1.81, 18.0, 128, 1.03},
+    {"w8_256x128", 256, 128, 1, 6.5, 0.74, 1.02, 18.0, 0, 0.0},
+    {"w8_128x128", 128, 128, 1, 5.5, 0.45, 0.56, 18.0, 0, 0.0},
+    {"w8_128x64", 128, 64, 2, 4.7, 0.37, 0.33, 18.0, 0, 0.0},
+    {"w8_64x64", 64, 64, 2, 4.3, 0.19, 0.23, 16.0, 0, 0.0},
 };
 
 // The plan with the least estimated time: rounds of workgroups, each the contraction's stages at
-// the longest of the three figures above; a split adds a launch (3 us) and the write and read of
-// its int32 planes (8 TB/s: they fit the caches).  The 256 x 256 tiles take all of the columns, or
-// those that make whole rounds, or none, and the lower tiles the others in a shorter last round
-// (M = 3000, (8192, 2048) 62.9 -> 58.8 us, M = 2048, (11008, 4096) 100.5 -> 97.9).
+// the longest of the three figures above; a split adds a launch (4.5 us of the host's time) and
+// the write and read of its int32 planes (8 TB/s: they fit the caches).  The 256 x 256 tiles take
+// all of the columns, or those that make whole rounds, or none, and the lower tiles the others in
+// a shorter last round (M = 3000, (8192, 2048) 62.9 -> 58.8 us, M = 2048, (11008, 4096)
+// 100.5 -> 97.9).
 W8Plan pick(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps, bool allow_split) {
   const int64_t cus = caps.cus > 0 ? caps.cus : 256, kt = ((K + 63) / 64 * 64 + BK - 1) / BK;
   W8Plan best;
@@ -383,12 +385,14 @@ W8Plan pick(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps, bool allow_
         if (full < tn && c.bl == 0) break;
         const int64_t wgs = rows * full * sp;
         const int64_t rounds = (wgs + cus * c.slots - 1) / (cus * c.slots);
-        const int64_t resident = std::min(wgs, cus * c.slots), per_cu = (resident + cus - 1) / cus;
+        // workgroups of the fullest CU; a round that leaves CUs idle runs at a higher clock
+        const int64_t resident = std::min(wgs, cus * c.slots);
+        const double per_cu = resident <= cus ? (double)resident / cus : (double)((resident + cus - 1) / cus);
         const double fill = (double)resident * (c.bm + c.bn) * BK / c.bw * 1e-6;
         const double stage = std::max(std::max(c.lat, c.mfma * per_cu), fill);
         const int64_t lows = full < tn ? (tn - full) * ((M + c.bl - 1) / c.bl) * sp : 0;
         const double t = c.t0 + rounds * steps * stage + (double)((lows + cus - 1) / cus * steps) * c.low +
-                         (sp > 1 ? 3.0 + sp * M * N * 8.0 / 8.0 * 1e-6 : 0.0);
+                         (sp > 1 ? 4.5 + sp * M * N * 8.0 / 8.0 * 1e-6 : 0.0);
         if (t < best_t) {
           best_t = t;
           best = W8Plan{i, (int)full, sp};
