@@ -9,7 +9,6 @@
 // products and in reads behind barriers was slower (126 us), as was each weight widened by two
 // waves, with fewer reads of dY (120).
 #include <algorithm>
-#include <cstdio>
 #include <type_traits>
 
 #include "api_common.h"

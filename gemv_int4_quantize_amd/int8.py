@@ -220,6 +220,8 @@ def mm_int8_split(a, w: Int8Rows, outs: list[torch.Tensor], bias: torch.Tensor |
     they may be row-strided views.  The bias, if any, spans all output columns in that dtype."""
     if not isinstance(a, Int8Rows):
         a = float_rows(a, "activations")
+    if not outs:
+        raise ValueError("at least one output is wanted")
     _product(a, w, bias, list(outs), outs[0].dtype)
     return list(outs)
 

@@ -254,6 +254,12 @@ def test_product_mixed_tiles(m, n, k):
     assert torch.equal(w4.mm_int8(a, w), y)
 
 
+def test_split_without_outputs():
+    w = w4.Int8Rows(torch.zeros(8, 64, dtype=torch.int8), torch.ones(8), 8, 64)
+    with pytest.raises(ValueError, match="at least one output"):
+        w4.mm_int8_split(torch.zeros(2, 64), w, [])
+
+
 def test_product_plans():
     names = [w4.int8_kernel_for(*s) for s in ((3000, 8192, 2048), (2048, 11008, 4096), (8192, 8192, 8192))]
     assert "+" in names[0] and "+" in names[1] and names[2] == "w8_256x256"
