@@ -3,6 +3,14 @@
 // 16-bit operands, fp32 accumulation.  The contraction runs across the weight's rows, so its
 // operand has to be transposed: ds_read_b64_tr_b8 hands each lane eight bytes of one column.
 //
+// Why w is rounded to dY's type: the scales belong to the contraction, so none of them can wait
+// for the sums, and the matrix cores take 16-bit operands; a second product with what the rounding
+// leaves over would double the work.  The error is that of a weight stored in that type (8 bits of
+// bf16, 11 of fp16).  fp16's short range is not w's: a power of two takes the largest scale of the
+// contraction to [2^7, 2^8) (codes to at most 2^15) and the sums are taken back by it, both
+// exactly.  Scales 2^21 times smaller than the largest one begin to lose bits.  (Measured: 1% at
+// M = 2048, (4096, 11008), 184 -> 186 us; 1 us of the scales' latency at M = 32, 17.4 -> 18.3.)
+//
 // What bounds it: at M = 2048, (N, K) = (4096, 8192) 118 us, 1165 TFLOP/s, where a bf16 product
 // whose weight needs no widening (the library's) takes 111.  The matrix cores are busy 57% of
 // the cycles, LDS 38%, and the clock is down to 1.85 GHz; that two waves a SIMD take turns in
@@ -122,12 +130,14 @@ __device__ __forceinline__ void grad_tile(char* smem, const uint16_t* __restrict
 #pragma unroll
     for (int h = 0; h < 2; ++h) s[h] = *reinterpret_cast<const f32x4*>(base + OS + (16 * p + 8 * hi + 4 * h) * 4);
   };
+  // fp16: the powers of two that take the largest finite scale of this slice to [2^7, 2^8), and back
+  float up = 1.0f, down = 1.0f;
   auto widen = [&](const i32x2& v, const f32x4 (&s)[2], u32x4& o) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float f[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) f[b] = (float)(int8_t)(v[h] >> (8 * b)) * s[h][b];
+      for (int b = 0; b < 4; ++b) f[b] = (float)(int8_t)(v[h] >> (8 * b)) * (F16 ? s[h][b] * up : s[h][b]);
       o[2 * h] = F16 ? pack_f16x2(f[0], f[1]) : pack_bf16x2(f[0], f[1]);
       o[2 * h + 1] = F16 ? pack_f16x2(f[2], f[3]) : pack_bf16x2(f[2], f[3]);
     }
@@ -140,6 +150,32 @@ __device__ __forceinline__ void grad_tile(char* smem, const uint16_t* __restrict
 
 #pragma unroll
   for (int k = 0; k < NB - 1; ++k) dma(k, k, 0, UL);
+  if constexpr (F16) {
+    __shared__ uint32_t peaks[WN];
+    uint32_t m = 0;
+    const int n_end = min(N, (k0 + KT) * BK);
+    auto take = [&](uint32_t u) { m = umax(m, (u & 0x7FFFFFFFu) < 0x7F800000u ? u & 0x7FFFFFFFu : 0u); };
+#pragma unroll 4
+    for (int n = k0 * BK + tid * 8; n < n_end; n += T * 8) {
+      if (n + 8 <= n_end) {
+        const Raw8<W4_DT_F32> s8 = load_raw8<W4_DT_F32>(sw + n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) take(s8.q[j >> 2][j & 3]);
+      } else {
+        for (int j = n; j < n_end; ++j) take(__float_as_uint(sw[j]));
+      }
+    }
+    m = wave_umax(m);
+    if (lane == 0) peaks[wave] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WN; ++i) m = umax(m, peaks[i]);
+    const int e = min(134 - (int)(__builtin_amdgcn_readfirstlane(m) >> 23), 126);
+    if (m != 0) {
+      up = __uint_as_float((uint32_t)(127 + e) << 23);
+      down = __uint_as_float((uint32_t)(127 - e) << 23);
+    }
+  }
   sync(std::integral_constant<int, NB - 2>());
   read_x(smem, 0, x[0]);
   read_raw(smem, raw);
@@ -170,7 +206,7 @@ __device__ __forceinline__ void grad_tile(char* smem, const uint16_t* __restrict
       for (int i = 0; i < FM; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                     // product
         __builtin_amdgcn_sched_group_barrier(0x100, (FM + 1 + FM) / FM, 0);    // LDS reads
-        __builtin_amdgcn_sched_group_barrier(0x002, (19 + FM) / FM, 0);        // widening
+        __builtin_amdgcn_sched_group_barrier(0x002, ((F16 ? 27 : 19) + FM) / FM, 0);  // widening
         if (p >= 2) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);         // direct loads
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -181,6 +217,11 @@ __device__ __forceinline__ void grad_tile(char* smem, const uint16_t* __restrict
   }
   // no direct LDS load may land after the workgroup's LDS is handed on
   __builtin_amdgcn_s_waitcnt(0x0070);
+  if constexpr (F16)
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][r] *= down;
 
   const int cbase = c0 + wave * 32, mbase = m0 + hi * 4, c = cbase + lr;
   if (part == nullptr && epi_wide(ep, K) != 0) {

@@ -231,8 +231,8 @@ def mm_int8_t(dy: torch.Tensor, w: Int8Rows, out: torch.Tensor | None = None,
     """dX = dY @ W, the input gradient of ``mm_int8``, on the same int8 weight.
 
     dY [M][N] is bfloat16 or float16 (rows may be strided); the weight operand is codes * scale
-    rounded to that dtype, sums are fp32 and the result is rounded once to `out_dtype` (fp32
-    unless given)."""
+    rounded to that dtype (float16: to its precision, whatever the size of the scales), sums are
+    fp32 and the result is rounded once to `out_dtype` (fp32 unless given)."""
     if dy.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"dY must be bfloat16 or float16 (got {dy.dtype})")
     dy = float_rows(dy, "dY")

@@ -61,8 +61,9 @@ int w8a8_linear(const void* X, int x_dtype, int64_t ldx, int64_t M, const int8_t
 
 /* The input gradient of the product, on the same int8 rows W [N][K]:
  *   dX[m][k] = out_rne(sum_n dY[m][n] * w[n][k]),  w = rne16(W[n][k] * w_scales[n])
- * dY [M][N] BF16 or F16 (row stride ld), w rounded to dY's dtype, fp32 accumulation.  The
- * segments cover K columns.  N < 2^22, K < 2^17.  The workspace that
+ * dY [M][N] BF16 or F16 (row stride ld), w rounded to dY's dtype (F16: to its eleven bits at any
+ * size of the scales, down to channels whose scale is 2^-21 of the largest), fp32 accumulation.
+ * The segments cover K columns.  N < 2^22, K < 2^17.  The workspace that
  * w8a16_mm_t_workspace_bytes reports is required when ld or N is not a multiple of 8 or dY
  * is not 16-byte aligned (it holds an aligned copy of dY), else optional (a split
  * contraction, summed in a fixed order). */

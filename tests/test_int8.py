@@ -450,3 +450,49 @@ def test_more_rows_than_a_launch_holds():
     for a in (x[:3], w4.Int8Rows(few.codes[:3], few.scales[:3], 3, 64)):
         y = w4.mm_int8(a, w, out_dtype=torch.bfloat16).view(3, -1, 64)
         assert torch.equal(y[:, 0], w4.mm_int8(a, few, out_dtype=torch.bfloat16)) and (y == y[:, :1]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(5, 40, 70), (131, 515, 128), (33, 4104, 2080), (513, 72, 33000)])
+@pytest.mark.parametrize("power", [-100, -40, -24, 12, 24, 100])
+def test_gradient_of_any_scale(m, n, k, power):
+    """A power of two in all of the weight's scales is one in the result, bit for bit: fp16 gradients
+    of weights whose values fp16 does not hold."""
+    dy, _ = _rows(m + n, m, n, torch.float16, scale=0.1)
+    w, _, _ = _weight(k, n, k)
+    other = w4.Int8Rows(w.codes, w.scales * 2.0**power, n, k)
+    want = w4.mm_int8_t(dy, w).double() * 2.0**power
+    assert torch.equal(w4.mm_int8_t(dy, other).double(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(7, 200, 96), (64, 1000, 257), (300, 4104, 520)])
+def test_gradient_of_mixed_scales(m, n, k):
+    """Channels whose scales are up to 2^20 apart: every operand keeps fp16's eleven bits."""
+    dy, dy32 = _rows(m * n, m, n, torch.float16, scale=0.1)
+    w, codes, s = _weight(n, n, k)
+    w.scales *= torch.from_numpy(2.0 ** -np.random.default_rng(n).integers(0, 20, n).astype(np.float32)).to(DEV) * 2.0**-6
+    w.scales[3] = 0.0
+    s = w.scales.double().cpu().numpy()
+    ref = dy32.astype(np.float64) @ (codes * s[:, None])
+    size = np.abs(dy32).astype(np.float64) @ np.abs(codes * s[:, None])
+    # the operand's rounding (2^-11), n products and as many additions in fp32
+    _check_rounded(w4.mm_int8_t(dy, w), ref, size, torch.float32, f"{m}x{n}x{k}", steps=2.0**13 + n + 2)
+    # the small channels alone: the large ones' gradients are 0
+    small = torch.from_numpy(s < s.max() * 2.0**-12).to(DEV)
+    alone = torch.where(small, dy, torch.zeros_like(dy))
+    a64 = alone.double().cpu().numpy()
+    ref, size = a64 @ (codes * s[:, None]), np.abs(a64) @ np.abs(codes * s[:, None])
+    _check_rounded(w4.mm_int8_t(alone, w), ref, size, torch.float32, f"small {m}x{n}x{k}", steps=2.0**13 + n + 2)
+
+
+@pytest.mark.gpu
+def test_gradient_of_bad_scales():
+    """A NaN among a weight's scales makes every result NaN, whatever the other channels hold."""
+    for dtype in (torch.float16, torch.bfloat16):
+        w, _, _ = _weight(4, 100, 70)
+        dy, _ = _rows(1, 9, 100, dtype)
+        w.scales[7] = float("nan")
+        assert torch.isnan(w4.mm_int8_t(dy, w)).all()
+        w.scales[:] = 0.0
+        assert not w4.mm_int8_t(dy, w).any()
