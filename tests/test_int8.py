@@ -496,3 +496,45 @@ def test_gradient_of_bad_scales():
         assert torch.isnan(w4.mm_int8_t(dy, w)).all()
         w.scales[:] = 0.0
         assert not w4.mm_int8_t(dy, w).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("x_dtype", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.bfloat16])
+def test_layer_gradient_keeps_its_type(x_dtype, out_dtype):
+    """A 16-bit gradient is multiplied as it is, whatever the activations' type."""
+    w, _, _ = _weight(41, 72, 130)
+    x = torch.randn(9, 130, device=DEV).to(x_dtype).requires_grad_()
+    gy = (torch.randn(9, 72, device=DEV) * 0.1).to(out_dtype)
+    w4.w8a8_linear(x, w, out_dtype=out_dtype).backward(gy)
+    assert torch.equal(x.grad, w4.mm_int8_t(gy, w, out_dtype=x_dtype))
+
+
+@pytest.mark.gpu
+def test_layer_gradient_range():
+    """fp16 activations with an fp32 output: rows of its gradient far below and above fp16's range."""
+    m, n, k = 24, 515, 130
+    w, codes, _ = _weight(43, n, k)
+    x = torch.randn(m, k, device=DEV).half().requires_grad_()
+    power = np.linspace(-33, 33, m).round()
+    gy = np.random.default_rng(2).standard_normal((m, n)) * 2.0 ** power[:, None]
+    gy[5], gy[6, 1:] = 0, 0
+    gy = torch.from_numpy(gy.astype(np.float32))
+    op = codes * w.scales.double().cpu().numpy()[:, None]
+    for row in range(m):  # a weight that brings the row's result back into fp16's range
+        wr = w4.Int8Rows(w.codes, w.scales * 2.0 ** -power[row], n, k)
+        x.grad = None
+        w4.w8a8_linear(x[row:row + 1], wr).backward(gy[row:row + 1].to(DEV))
+        r64, o64 = gy[row:row + 1].double().numpy(), op * 2.0 ** -power[row]
+        ref, size = r64 @ o64, np.abs(r64) @ np.abs(o64)
+        # dY's and the weight's rounding (2^-11 each) and 2^-39 of the row's largest dY, n products and sums in fp32
+        floor = np.abs(r64).max() * np.abs(o64).sum(0) * 2.0**-39
+        _check_rounded(x.grad[row:row + 1], ref, size + floor * 2.0**11, torch.float16, f"row {row}", steps=2.0**14 + n + 2)
+    x.grad = None
+    gy[3, 7], gy[4, 8] = float("nan"), float("inf")
+    w4.w8a8_linear(x, w).backward(gy.to(DEV))
+    bad = ~torch.isfinite(gy).all(1)
+    assert not torch.isfinite(x.grad[bad]).any() and not x.grad[5].any()
+    x0 = torch.empty(0, k, device=DEV, dtype=torch.float16, requires_grad=True)
+    w4.w8a8_linear(x0, w).backward(torch.empty(0, n, device=DEV))
+    assert x0.grad.shape == (0, k)
