@@ -715,84 +715,80 @@ size_t tok_ws_bytes(int64_t M, int64_t V, int top, const DeviceCaps& caps) {
   return parts == 1 ? 0 : (size_t)M * parts * (sizeof(Part) + 8 * (size_t)top);
 }
 
-// A launch holds fewer than 2^32 threads: rows are launched in runs of at most kRows.
+// A launch holds fewer than 2^32 threads: rows are launched in runs of at most kRows.  How a row is
+// cut is decided from all rows, as the workspace is, never from the rows of a run: a last run of
+// few rows would take parts that no workspace was given for.
 constexpr int64_t kRows = (int64_t)1 << 23;
 
 static size_t elem_bytes(int dt) { return dt == W4_DT_F32 ? 4 : 2; }
 
 hipError_t launch_tok(const TokArgs& all, const DeviceCaps& caps, void* ws, hipStream_t st) {
   TokArgs a = all;
-  if (a.M > kRows) {
-    for (int64_t r = 0; r < all.M; r += kRows) {
-      a.M = std::min(kRows, all.M - r);
-      const hipError_t e = launch_tok(a, caps, ws, st);  // rows enough for one part: no workspace
-      if (e != hipSuccess) return e;
-      a.z = static_cast<const char*>(a.z) + (size_t)(kRows * a.ld) * elem_bytes(a.dt);
-      a.targets += kRows;
-      a.lp += kRows;
-      a.ent += kRows;
-      a.stats += 2 * kRows;
-      if (a.top > 0) {
-        a.top_lp += kRows * a.top;
-        a.top_ids += kRows * a.top;
-      }
+  const int most = parts_of(all.M, all.V, caps, kMaxParts);
+  const int seg = seg_of(all.V, most);
+  const int parts = (int)((all.V + seg - 1) / seg);  // rounding the columns up may leave fewer
+  // more than one part only of rows that are far fewer than kRows: one run
+  Part* ps = most > 1 ? static_cast<Part*>(ws) : nullptr;
+  float* pv = most > 1 ? reinterpret_cast<float*>(ps + (size_t)all.M * most) : nullptr;
+  int* pj = most > 1 ? reinterpret_cast<int*>(pv + (size_t)all.M * parts * all.top) : nullptr;
+  for (int64_t r = 0; r < all.M; r += kRows) {
+    a.M = std::min(kRows, all.M - r);
+    const unsigned g = (unsigned)(a.M * parts);
+    switch (a.dt) {
+      case W4_DT_F32: tok_kernel<W4_DT_F32><<<g, kT, 0, st>>>(a, parts, seg, ps, pv, pj); break;
+      case W4_DT_F16: tok_kernel<W4_DT_F16><<<g, kT, 0, st>>>(a, parts, seg, ps, pv, pj); break;
+      default: tok_kernel<W4_DT_BF16><<<g, kT, 0, st>>>(a, parts, seg, ps, pv, pj); break;
     }
-    return hipSuccess;
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.z = static_cast<const char*>(a.z) + (size_t)(kRows * a.ld) * elem_bytes(a.dt);
+    a.targets += kRows;
+    a.lp += kRows;
+    a.ent += kRows;
+    a.stats += 2 * kRows;
+    if (a.top > 0) {
+      a.top_lp += kRows * a.top;
+      a.top_ids += kRows * a.top;
+    }
   }
-  int parts = parts_of(a.M, a.V, caps, kMaxParts);
-  const int seg = seg_of(a.V, parts);
-  Part* ps = static_cast<Part*>(ws);
-  float* pv = reinterpret_cast<float*>(ps + (size_t)a.M * parts);
-  parts = (int)((a.V + seg - 1) / seg);  // rounding the columns up may leave fewer
-  int* pj = reinterpret_cast<int*>(pv + (size_t)a.M * parts * a.top);
-  const unsigned g = (unsigned)(a.M * parts);
-  switch (a.dt) {
-    case W4_DT_F32: tok_kernel<W4_DT_F32><<<g, kT, 0, st>>>(a, parts, seg, ps, pv, pj); break;
-    case W4_DT_F16: tok_kernel<W4_DT_F16><<<g, kT, 0, st>>>(a, parts, seg, ps, pv, pj); break;
-    default: tok_kernel<W4_DT_BF16><<<g, kT, 0, st>>>(a, parts, seg, ps, pv, pj); break;
-  }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || parts == 1) return e;
-  const size_t lds = (size_t)parts * a.top * 8;  // at most 64 x 64 pairs: 32 KB
-  switch (a.dt) {
-    case W4_DT_F32: tok_join_kernel<W4_DT_F32><<<(unsigned)a.M, kT, lds, st>>>(a, parts, ps, pv, pj); break;
-    case W4_DT_F16: tok_join_kernel<W4_DT_F16><<<(unsigned)a.M, kT, lds, st>>>(a, parts, ps, pv, pj); break;
-    default: tok_join_kernel<W4_DT_BF16><<<(unsigned)a.M, kT, lds, st>>>(a, parts, ps, pv, pj); break;
+  if (parts == 1) return hipSuccess;
+  const size_t lds = (size_t)parts * all.top * 8;  // at most 64 x 64 pairs: 32 KB
+  const unsigned g = (unsigned)all.M;
+  switch (all.dt) {
+    case W4_DT_F32: tok_join_kernel<W4_DT_F32><<<g, kT, lds, st>>>(all, parts, ps, pv, pj); break;
+    case W4_DT_F16: tok_join_kernel<W4_DT_F16><<<g, kT, lds, st>>>(all, parts, ps, pv, pj); break;
+    default: tok_join_kernel<W4_DT_BF16><<<g, kT, lds, st>>>(all, parts, ps, pv, pj); break;
   }
   return hipGetLastError();
 }
 
 hipError_t launch_tok_grad(const TokGradArgs& all, const DeviceCaps& caps, hipStream_t st) {
   TokGradArgs a = all;
-  if (a.M > kRows) {
-    for (int64_t r = 0; r < all.M; r += kRows) {
-      a.M = std::min(kRows, all.M - r);
-      const hipError_t e = launch_tok_grad(a, caps, st);
-      if (e != hipSuccess) return e;
-      a.z = static_cast<const char*>(a.z) + (size_t)(kRows * a.ld) * elem_bytes(a.dt);
-      a.dz = static_cast<char*>(a.dz) + (size_t)(kRows * a.ldd) * elem_bytes(a.dt);
-      a.targets += kRows;
-      a.stats += 2 * kRows;
-      a.ent += kRows;
-      if (a.g != nullptr) a.g += kRows;
-      if (a.h != nullptr) a.h += kRows;
-      if (a.top > 0) {
-        a.top_ids += kRows * a.top;
-        if (a.a != nullptr) a.a += kRows * a.top;
-      }
+  const int seg = seg_of(all.V, parts_of(all.M, all.V, caps, 1 << 20));
+  const int parts = (int)((all.V + seg - 1) / seg);
+  for (int64_t r = 0; r < all.M; r += kRows) {
+    a.M = std::min(kRows, all.M - r);
+    const unsigned g = (unsigned)(a.M * parts);
+    switch (a.dt) {
+      case W4_DT_F32: tok_grad_kernel<W4_DT_F32><<<g, kT, 0, st>>>(a, parts, seg); break;
+      case W4_DT_F16: tok_grad_kernel<W4_DT_F16><<<g, kT, 0, st>>>(a, parts, seg); break;
+      default: tok_grad_kernel<W4_DT_BF16><<<g, kT, 0, st>>>(a, parts, seg); break;
     }
-    return hipSuccess;
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.z = static_cast<const char*>(a.z) + (size_t)(kRows * a.ld) * elem_bytes(a.dt);
+    a.dz = static_cast<char*>(a.dz) + (size_t)(kRows * a.ldd) * elem_bytes(a.dt);
+    a.targets += kRows;
+    a.stats += 2 * kRows;
+    a.ent += kRows;
+    if (a.g != nullptr) a.g += kRows;
+    if (a.h != nullptr) a.h += kRows;
+    if (a.a != nullptr) {
+      a.a += kRows * a.top;
+      a.top_ids += kRows * a.top;
+    }
   }
-  int parts = parts_of(a.M, a.V, caps, 1 << 20);
-  const int seg = seg_of(a.V, parts);
-  parts = (int)((a.V + seg - 1) / seg);
-  const unsigned g = (unsigned)(a.M * parts);
-  switch (a.dt) {
-    case W4_DT_F32: tok_grad_kernel<W4_DT_F32><<<g, kT, 0, st>>>(a, parts, seg); break;
-    case W4_DT_F16: tok_grad_kernel<W4_DT_F16><<<g, kT, 0, st>>>(a, parts, seg); break;
-    default: tok_grad_kernel<W4_DT_BF16><<<g, kT, 0, st>>>(a, parts, seg); break;
-  }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace w4
