@@ -81,6 +81,27 @@ def space(nbytes: int, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
+class _Once(torch.autograd.Function):
+    """The identity of a gradient, as a function of what it was computed from: differentiating it
+    raises.  (A backward that is marked as once differentiable raises only where the gradient it
+    was given requires grad itself; its dependence on the saved tensors would go unnoticed.)"""
+
+    @staticmethod
+    def forward(ctx, grad, what, *of):
+        ctx.what = what
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.what}: trying to differentiate twice (its gradient has no derivative here)")
+
+
+def once(grad: torch.Tensor, what: str, *of) -> torch.Tensor:
+    """The result `grad` of a backward, computed from the tensors `of` (None among them), marked so
+    that a second derivative through it raises."""
+    return _Once.apply(grad, what, *of) if torch.is_grad_enabled() else grad
+
+
 def float_rows(x: torch.Tensor, what: str) -> torch.Tensor:
     """x as the library takes float rows: 2-D, columns next to one another, any row stride."""
     if x.dim() != 2:

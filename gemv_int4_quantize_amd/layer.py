@@ -27,7 +27,7 @@ from __future__ import annotations
 import torch
 
 from . import int8, ops
-from .int8 import Int8Rows
+from .int8 import Int8Rows, once
 from .ops import QuantizedWeight
 
 _OUT_DTYPES = (None, torch.float32, torch.bfloat16, torch.float16)
@@ -138,23 +138,23 @@ class _W8A8Matmul(torch.autograd.Function):
     @staticmethod
     def backward(ctx, gy: torch.Tensor):
         w: Int8Rows = ctx.w
-        g2 = gy.reshape(-1, w.rows)
         dx = None
         if ctx.needs_input_grad[0]:
+            g2 = gy.detach().reshape(-1, w.rows)
             if g2.dtype == torch.float32 and ctx.x_dtype == torch.float16:
                 g16, back = _half_rows(g2)
                 dx = int8.mm_int8_t(g16, w).mul_(back).to(ctx.x_dtype)
             else:
                 g16 = g2 if g2.dtype in _HALF else g2.to(torch.bfloat16)
                 dx = int8.mm_int8_t(g16, w, out_dtype=ctx.x_dtype)
-            dx = dx.view(*ctx.lead, w.cols)
-        db = g2.float().sum(0).to(ctx.bias_dtype) if ctx.needs_input_grad[2] else None
+            dx = once(dx.view(*ctx.lead, w.cols), "w8a8_linear", gy)
+        db = gy.reshape(-1, w.rows).float().sum(0).to(ctx.bias_dtype) if ctx.needs_input_grad[2] else None
         return dx, None, db, None
 
 
 def w8a8_linear(x: torch.Tensor, w: Int8Rows, bias: torch.Tensor | None = None,
                 out_dtype: torch.dtype | None = None) -> torch.Tensor:
-    """Differentiable ``x @ w^T (+ bias)`` in 8-bit integers over an int8 weight (one scale per
+    """Differentiable (once) ``x @ w^T (+ bias)`` in 8-bit integers over an int8 weight (one scale per
     output channel), x (float32, float16 or bfloat16) quantized per token: fp32 result, or
     ``out_dtype`` (bfloat16 / float16) rounded once."""
     if out_dtype not in _OUT_DTYPES:

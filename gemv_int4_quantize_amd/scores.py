@@ -15,7 +15,7 @@ from typing import NamedTuple
 import torch
 
 from ._lib import check, lib
-from .int8 import _row_stride, check_device, float_rows, on_device, space
+from .int8 import _row_stride, check_device, float_rows, on_device, once, space
 from .ops import _WDT, _stream
 
 
@@ -126,7 +126,7 @@ class _TokenLogprobs(torch.autograd.Function):
         top = ids.shape[1]
         _grad(z, t, stats, ent, ids, top, _plain_grad(g), _plain_grad(h), _plain_grad(a) if top else None,
               ctx.temperature, ctx.ignore, dz)
-        return dz, None, None, None, None
+        return once(dz, "token_logprobs", z, g, h, a), None, None, None, None
 
 
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, temperature: float = 1.0,
@@ -142,7 +142,7 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, te
 
     A logit of -inf is a masked token (probability 0).  A row that is masked throughout has log
     probabilities -inf, entropy 0 and no gradient; a row with a NaN or +inf scores NaN.  The three
-    float results are differentiable with respect to the logits."""
+    float results are differentiable with respect to the logits, once: a second derivative raises."""
     z = float_rows(logits, "logits")
     t = _targets(targets, z.shape[0])
     if torch.is_grad_enabled() and z.requires_grad:

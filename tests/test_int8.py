@@ -538,3 +538,35 @@ def test_layer_gradient_range():
     x0 = torch.empty(0, k, device=DEV, dtype=torch.float16, requires_grad=True)
     w4.w8a8_linear(x0, w).backward(torch.empty(0, n, device=DEV))
     assert x0.grad.shape == (0, k)
+
+
+def test_second_derivatives_raise(monkeypatch):
+    """The layer's gradient is no function that autograd knows: a second derivative through it raises.
+    (The launches are replaced by torch on the CPU: what is left is the autograd.)"""
+    from gemv_int4_quantize_amd import int8
+
+    def value(w):
+        return w.codes[:, :w.cols].float() * w.scales[:, None]
+
+    monkeypatch.setattr(int8, "mm_int8", lambda x, w, bias=None, out_dtype=None: x.float() @ value(w).t())
+    monkeypatch.setattr(int8, "mm_int8_t", lambda g, w, out_dtype=torch.float32: (g.float() @ value(w)).to(out_dtype))
+    w = w4.Int8Rows(torch.ones(8, 64, dtype=torch.int8), torch.ones(8), 8, 64)
+    bias = torch.zeros(8, requires_grad=True)
+    for b in (None, bias):
+        x = torch.randn(3, 64, requires_grad=True)
+        y = w4.w8a8_linear(x, w, b)
+        loss = y.square().sum() + (x**3).sum()
+        (g,) = torch.autograd.grad(loss, x, create_graph=True)
+        with pytest.raises(RuntimeError, match="twice|once_differentiable"):
+            g.square().sum().backward()
+        # of a constant dY the result is constant in x: no term is missing
+        x = torch.randn(3, 64, requires_grad=True)
+        (g,) = torch.autograd.grad(w4.w8a8_linear(x, w, b).sum() + (x**3).sum(), x, create_graph=True)
+        assert torch.allclose(torch.autograd.grad(g.sum(), x)[0], 6 * x)
+    for dtype in (torch.float16, torch.bfloat16):  # the first derivative, with its graph
+        x = torch.randn(3, 64).to(dtype).requires_grad_()
+        (g,) = torch.autograd.grad(w4.w8a8_linear(x, w).square().sum(), x, create_graph=True)
+        assert g.dtype == dtype and g.requires_grad
+    x = torch.randn(3, 64, requires_grad=True)
+    w4.w8a8_linear(x, w, bias).sum().backward()
+    assert (x.grad == 8).all() and (bias.grad == 3).all()

@@ -396,3 +396,38 @@ def test_more_rows_than_a_launch_holds():
     q = torch.sigmoid(d)  # the other's probability
     ref = torch.stack([torch.where(t == 0, q, -q), torch.where(t == 1, q, -q)], 1)
     assert (z.grad.double() - ref).abs().max() < 1e-5
+
+
+def _plain_launches(monkeypatch):
+    """The launches of the scores replaced by torch on the CPU: what is left is the autograd."""
+    from gemv_int4_quantize_amd import scores
+
+    def forward(z, t, top, temperature, ignore):
+        lp = torch.log_softmax(z / temperature, 1)
+        v, ids = lp.topk(top, 1)
+        return lp.gather(1, t[:, None])[:, 0], -(lp.exp() * lp).sum(1), v, ids, torch.zeros(z.shape[0], 2)
+
+    def grad(z, t, stats, ent, ids, top, g, h, a, temperature, ignore, out):
+        out.copy_(torch.zeros_like(z) if g is None else
+                  g[:, None] * (torch.nn.functional.one_hot(t, z.shape[1]) - torch.softmax(z / temperature, 1)) / temperature)
+
+    monkeypatch.setattr(scores, "_forward", forward)
+    monkeypatch.setattr(scores, "_grad", grad)
+
+
+def test_second_derivatives_raise(monkeypatch):
+    """The gradient is no function that autograd knows: a second derivative through it raises, and is
+    not silently that of the loss's other terms alone."""
+    _plain_launches(monkeypatch)
+    t = torch.tensor([1, 2])
+    for weight in (torch.ones(2), torch.ones(2, requires_grad=True)):
+        z = torch.randn(2, 5, requires_grad=True)
+        loss = (w4.token_logprobs(z, t).logprobs * weight).sum() + (z**3).sum()
+        (g,) = torch.autograd.grad(loss, z, create_graph=True)
+        with pytest.raises(RuntimeError, match="twice|once_differentiable"):
+            g.square().sum().backward()
+    # the first derivative is as it was, also with the graph kept
+    z = torch.randn(2, 5, requires_grad=True)
+    w4.token_logprobs(z, t).logprobs.sum().backward(retain_graph=True)
+    one = torch.nn.functional.one_hot(t, 5)
+    assert torch.allclose(z.grad, one - torch.softmax(z.detach(), 1))
