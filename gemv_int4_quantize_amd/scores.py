@@ -13,6 +13,7 @@ import functools
 from typing import NamedTuple
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from ._lib import check, lib
 from .int8 import _row_stride, check_device, float_rows, on_device, once, space
@@ -142,7 +143,10 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, te
 
     A logit of -inf is a masked token (probability 0).  A row that is masked throughout has log
     probabilities -inf, entropy 0 and no gradient; a row with a NaN or +inf scores NaN.  The three
-    float results are differentiable with respect to the logits, once: a second derivative raises."""
+    float results are differentiable with respect to the logits, once and in reverse
+    mode: a second derivative and a tangent raise."""
+    if unpack_dual(logits).tangent is not None:
+        raise RuntimeError("token_logprobs has no derivative in forward mode")
     z = float_rows(logits, "logits")
     t = _targets(targets, z.shape[0])
     if torch.is_grad_enabled() and z.requires_grad:

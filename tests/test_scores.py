@@ -431,3 +431,19 @@ def test_second_derivatives_raise(monkeypatch):
     w4.token_logprobs(z, t).logprobs.sum().backward(retain_graph=True)
     one = torch.nn.functional.one_hot(t, 5)
     assert torch.allclose(z.grad, one - torch.softmax(z.detach(), 1))
+
+
+def test_forward_mode_raises(monkeypatch):
+    """No tangent is computed: a dual tensor raises, and its tangent is not silently dropped."""
+    import torch.autograd.forward_ad as fwd
+
+    _plain_launches(monkeypatch)
+    t = torch.tensor([1, 2])
+    with fwd.dual_level():
+        for grad in (False, True):
+            z = fwd.make_dual(torch.randn(2, 5, requires_grad=grad), torch.randn(2, 5))
+            with pytest.raises(RuntimeError, match="forward"):
+                w4.token_logprobs(z, t)
+            with pytest.raises(RuntimeError, match="forward"), torch.no_grad():
+                w4.token_logprobs(z.t().contiguous().t(), t)
+        assert w4.token_logprobs(torch.randn(2, 5), t).logprobs.shape == (2,)
