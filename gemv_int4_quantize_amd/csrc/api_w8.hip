@@ -70,6 +70,16 @@ LinearWs linear_ws(int64_t M, int64_t N, int64_t K) {
   return w;
 }
 
+// Whether the input gradient reads a copy of dY's rows at an aligned pitch (apart from a dY that is
+// not 16-byte aligned): 16-byte loads of every row, at 32-bit offsets in a tile of 256 rows.
+// ld < 0: the row stride is not known.
+constexpr int64_t kGradLd = (int64_t)1 << 22;
+bool grad_copies(int64_t M, int64_t N, int64_t ld) {
+  if (ld < 0) return true;
+  if (M <= 1) ld = N;
+  return ld % 8 != 0 || N % 8 != 0 || ld >= kGradLd;
+}
+
 }  // namespace
 
 extern "C" {
@@ -180,7 +190,7 @@ int w8a16_mm_t_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ld, size
   if (!bytes) return fail(W4_ERR_INVALID, "bytes is NULL");
   *bytes = 0;
   if (M == 0) return ok();
-  if (ld < 0 || ld % 8 != 0 || N % 8 != 0) *bytes = up256((size_t)M * pitch_of(N) * 2);
+  if (grad_copies(M, N, ld)) *bytes = up256((size_t)M * pitch_of(N) * 2);
   *bytes += w4::w8_grad_workspace_bytes(M, N, K, device_caps());
   return ok();
 }
@@ -195,8 +205,7 @@ int w8a16_mm_t(const void* dY, int dtype, int64_t ld, int64_t M, const int8_t* W
   w4::Epi ep;
   s = make_epi(K, M, nullptr, out_dtype, segs, nsegs, &ep);
   if (s != W4_OK) return s;
-  // the kernel addresses a 256-row dY tile with 32-bit offsets
-  if (N >= ((int64_t)1 << 22)) return fail(W4_ERR_UNSUPPORTED, "N = %lld must be below 2^22", (long long)N);
+  if (N >= kGradLd) return fail(W4_ERR_UNSUPPORTED, "N = %lld must be below 2^22", (long long)N);
   if (M == 0) return ok();
   s = check_weight(W, w_scales);
   if (s == W4_OK) s = check_ws(ws);
@@ -206,11 +215,12 @@ int w8a16_mm_t(const void* dY, int dtype, int64_t ld, int64_t M, const int8_t* W
   size_t wsb = ws != nullptr ? ws_bytes : 0;
   char* w = static_cast<char*>(ws);
   w4::W8GradArgs a = {static_cast<const uint16_t*>(dY), dtype == W4_DT_F16, ld, N, W, w_scales, ep, M, N, K, pitch_of(K)};
-  if (ld % 8 != 0 || N % 8 != 0 || ld >= ((int64_t)1 << 22) || !aligned(dY, 16)) {
+  if (grad_copies(M, N, ld) || !aligned(dY, 16)) {
     const int64_t npad = pitch_of(N);
     const size_t need = up256((size_t)M * npad * 2);
     if (wsb < need)
-      return fail(W4_ERR_RESOURCE, "a dY that is not 16-byte aligned needs a workspace of %zu bytes (got %zu)", need, wsb);
+      return fail(W4_ERR_RESOURCE, "a dY of row stride %lld and %lld columns%s needs a workspace of %zu bytes (got %zu)",
+                  (long long)ld, (long long)N, aligned(dY, 16) ? "" : ", not 16-byte aligned,", need, wsb);
     s = launched(w4::launch_pad_rows(static_cast<const uint16_t*>(dY), M, N, ld, reinterpret_cast<uint16_t*>(w), npad, st),
                  "pad_rows");
     if (s != W4_OK) return s;

@@ -64,9 +64,10 @@ int w8a8_linear(const void* X, int x_dtype, int64_t ldx, int64_t M, const int8_t
  * dY [M][N] BF16 or F16 (row stride ld), w rounded to dY's dtype (F16: to its eleven bits at any
  * size of the scales, down to channels whose scale is 2^-21 of the largest), fp32 accumulation.
  * The segments cover K columns.  N < 2^22, K < 2^17.  The workspace that
- * w8a16_mm_t_workspace_bytes reports is required when ld or N is not a multiple of 8 or dY
- * is not 16-byte aligned (it holds an aligned copy of dY), else optional (a split
- * contraction, summed in a fixed order). */
+ * w8a16_mm_t_workspace_bytes reports is required when N or (for M > 1) ld is not a multiple
+ * of 8, when ld is 2^22 or more, or when dY is not 16-byte aligned (it holds an aligned copy
+ * of dY; for the last, ask with ld < 0), else optional (a split contraction, summed in a
+ * fixed order). */
 int w8a16_mm_t(const void* dY, int dtype, int64_t ld, int64_t M, const int8_t* W, const float* w_scales, int64_t N,
                int64_t K, int out_dtype, const w4_out_seg* segs, int nsegs, void* ws, size_t ws_bytes, void* stream);
 

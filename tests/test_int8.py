@@ -570,3 +570,30 @@ def test_second_derivatives_raise(monkeypatch):
     x = torch.randn(3, 64, requires_grad=True)
     w4.w8a8_linear(x, w, bias).sum().backward()
     assert (x.grad == 8).all() and (bias.grad == 3).all()
+
+
+def test_gradient_workspace_of_long_strides():
+    """The reported workspace is what the call asks for, at every row stride."""
+    L = w4.lib()
+    for M, N, ld in ((4, 64, 1 << 22), (4, 64, (1 << 22) - 8), (4, 64, (1 << 40)), (4, 64, 68), (4, 60, 60), (4, 64, -1),
+                     (1, 64, 1 << 22), (1, 64, 67), (1, 60, 64), (2, 64, (1 << 22) - 4)):
+        size = ctypes.c_size_t(0)
+        assert L.w8a16_mm_t_workspace_bytes(M, N, 128, ld, ctypes.byref(size)) == 0
+        copied = N % 8 != 0 or (ld % 8 != 0 or ld >= 1 << 22 if M > 1 else False) or ld < 0
+        assert (size.value >= M * 64 * 2) == copied, (M, N, ld)
+        if copied and ld > 0:
+            status = L.w8a16_mm_t(_p(), 2, ld, M, _p(), _p(), N, 128, 0, _seg(128), 1, _p(), M * 64 * 2 - 1, None)
+            assert status == _lib.W4_ERR_RESOURCE, (M, N, ld)
+            assert "workspace" in L.w4_last_error().decode()
+
+
+@pytest.mark.gpu
+def test_gradient_long_strides():
+    """The last tokens of long sequences: rows 2^22 elements apart."""
+    w, _, _ = _weight(51, 4096, 96)
+    dy = torch.empty(8, 1024, 4096, dtype=torch.bfloat16, device=DEV)
+    last = dy[:, -1, :]
+    last.copy_(torch.randn(8, 4096, device=DEV))
+    assert last.stride(0) == 1 << 22
+    assert torch.equal(w4.mm_int8_t(last, w), w4.mm_int8_t(last.contiguous(), w))
+    assert torch.equal(w4.mm_int8_t(last[:1], w), w4.mm_int8_t(last[:1].contiguous(), w))
