@@ -179,8 +179,8 @@ int w8a8_linear(const void* X, int x_dtype, int64_t ldx, int64_t M, const int8_t
 }
 
 const char* w8a8_kernel(int64_t M, int64_t N, int64_t K, int x_dtype) {
-  if (check_sizes(M, N, K) != W4_OK || M == 0) return nullptr;
-  (void)x_dtype;
+  if (check_sizes(M, N, K) != W4_OK || M == 0 || (x_dtype >= 0 && !is_dtype(x_dtype))) return nullptr;
+  if (x_dtype >= 0 && w4::w8_fused(M, K)) return "w8_decode_fused";
   return w4::w8_mm_name(M, N, K, device_caps());
 }
 

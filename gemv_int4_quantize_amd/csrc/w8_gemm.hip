@@ -413,7 +413,7 @@ size_t w8_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceCaps& 
 
 const char* w8_mm_name(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps) {
   static thread_local char buf[48];
-  if (w8_decode_supported(M)) return w8_fused(M, K) ? "w8_decode_fused" : "w8_decode";
+  if (w8_decode_supported(M)) return "w8_decode";
   const W8Plan p = pick(M, N, K, caps, true);
   const Tile& c = kTiles[p.tile];
   int at = snprintf(buf, sizeof(buf), "%s", c.name);

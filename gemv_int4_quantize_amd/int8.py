@@ -281,6 +281,6 @@ def mm_int8_t(dy: torch.Tensor, w: Int8Rows, out: torch.Tensor | None = None,
 
 
 def int8_kernel_for(M: int, N: int, K: int) -> str | None:
-    """Name of the kernel that multiplies M tokens by a weight of this shape (host-side query)."""
+    """Name of the kernel that multiplies M float tokens by a weight of this shape (host-side query)."""
     r = lib().w8a8_kernel(M, N, K, _lib.DT_BF16)
     return r.decode() if r is not None else None

@@ -597,3 +597,14 @@ def test_gradient_long_strides():
     assert last.stride(0) == 1 << 22
     assert torch.equal(w4.mm_int8_t(last, w), w4.mm_int8_t(last.contiguous(), w))
     assert torch.equal(w4.mm_int8_t(last[:1], w), w4.mm_int8_t(last[:1].contiguous(), w))
+
+
+def test_kernel_names():
+    """The name is that of the kernel launched: int8 rows never take the form that quantizes."""
+    k = w4.lib().w8a8_kernel
+    assert k(2, 4096, 4096, -1) == b"w8_decode" and k(2, 4096, 4096, _lib.DT_BF16) == b"w8_decode_fused"
+    assert k(4, 4096, 70000, _lib.DT_BF16) == b"w8_decode"  # codes that LDS does not hold: quantized before
+    assert k(64, 4096, 4096, -1) == k(64, 4096, 4096, _lib.DT_F32) is not None
+    for bad in ((2, 4096, 4096, 9), (0, 64, 64, -1), (4, 0, 64, -1), (4, 64, 1 << 17, -1)):
+        assert k(*bad) is None
+    assert w4.int8_kernel_for(1, 2048, 2048) == "w8_decode_fused"
