@@ -36,6 +36,28 @@ __device__ __forceinline__ i32x4 load16(rsrc_t r, int off, int soff) {
   return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, AUX));
 }
 
+// Units of a lane's 32 columns (from column 32 q4 of each) that count.  The last unit of a pitch that
+// is not a multiple of 128 holds 64 columns: past them the weight's bytes are the next channel's,
+// and the tokens are taken as 0.
+constexpr int code_cut(int pitch, int q4) {
+  const int units = (pitch + 127) >> 7;
+  return (pitch & 64) != 0 && q4 >= 2 ? units - 1 : units;
+}
+// Where a lane reads a token's codes for unit u: inside the token's row for every u, the last unit
+// that counts standing in for those past it, and the first columns where none does (a pitch of 64).
+constexpr int code_column(int cut, int q4) { return cut > 0 ? q4 * 32 : 0; }
+constexpr int code_unit(int u, int cut) { return u < cut ? u : cut > 0 ? cut - 1 : 0; }
+constexpr bool codes_in_row() {
+  for (int pitch = 64; pitch <= 1024; pitch += 64)
+    for (int q4 = 0; q4 < 4; ++q4)
+      for (int u = 0; u < pitch / 128 + 9; ++u) {
+        const int cut = code_cut(pitch, q4), at = code_column(cut, q4) + code_unit(u, cut) * 128;
+        if (at < 0 || at + 32 > pitch) return false;
+      }
+  return true;
+}
+static_assert(codes_in_row(), "LDS reads of the token codes");
+
 constexpr int kMaxM = 4;               // tokens
 constexpr int kFusedLds = 64 * 1024;   // bytes of codes that a workgroup may hold
 
@@ -139,19 +161,16 @@ __global__ __launch_bounds__(NW * 64) void w8_decode_kernel(const int8_t* __rest
   }
 
   i32x4 acc = {0, 0, 0, 0};
-  const char* xl = smem + min(r16, M - 1) * (pitch + 16) + q4 * 32;
-  // the last unit of a pitch that is not a multiple of 128 holds 64 columns: past them the
-  // weight's bytes are the next channel's, and the tokens are taken as 0
-  const int cut = (pitch & 64) != 0 && q4 >= 2 ? units - 1 : units;
+  const int cut = code_cut(pitch, q4);
+  const char* xl = smem + min(r16, M - 1) * (pitch + 16) + code_column(cut, q4);
   for (int u = u0; u < u1; u += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if constexpr (XDT >= 0) {
-          // past the wave's run the weight is 0; the address stays inside the codes
-          const int at = min(u + d, cut - 1);
-          x[d][h] = *reinterpret_cast<const i32x4*>(xl + at * 128 + h * 16);
+          // past the wave's run the weight is 0
+          x[d][h] = *reinterpret_cast<const i32x4*>(xl + code_unit(u + d, cut) * 128 + h * 16);
         }
         const i32x4 t = u + d < cut ? x[d][h] : i32x4{0, 0, 0, 0};
         acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[d][h], t, acc, 0, 0, 0);

@@ -608,3 +608,13 @@ def test_kernel_names():
     for bad in ((2, 4096, 4096, 9), (0, 64, 64, -1), (4, 0, 64, -1), (4, 64, 1 << 17, -1)):
         assert k(*bad) is None
     assert w4.int8_kernel_for(1, 2048, 2048) == "w8_decode_fused"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("k", [1, 31, 33, 63, 64, 65, 129, 192, 193, 320])
+def test_decode_short_rows(k, dtype):
+    """Few columns: codes of half a unit, and the last unit of a pitch that is not a multiple of 128."""
+    for m in (1, 2, 3, 4):
+        for n in (1, 16, 37, 9000):
+            test_product(m, n, k, dtype)
