@@ -618,3 +618,93 @@ def test_decode_short_rows(k, dtype):
     for m in (1, 2, 3, 4):
         for n in (1, 16, 37, 9000):
             test_product(m, n, k, dtype)
+
+
+EXACT = [(33, 4104, 2080), (1, 200, 70), (16, 2027, 130), (300, 1000, 520), (600, 515, 23000), (64, 8200, 257)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", EXACT)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_gradient_rows_alone(m, n, k, dtype):
+    """Every contraction row by itself: dY of one 1 a row gives that row of codes, exactly, wherever
+    it lies in a stage or a slice of the contraction."""
+    w, codes, _ = _weight(n, n, k)
+    w.scales[:] = 1.0
+    want = torch.from_numpy(codes).to(DEV).float()
+    for at in range(0, n, m):
+        rows = torch.arange(m, device=DEV) + min(at, max(0, n - m))
+        rows %= n
+        dy = torch.zeros(m, n, dtype=dtype, device=DEV)
+        dy[torch.arange(m, device=DEV), rows] = 1.0
+        assert torch.equal(w4.mm_int8_t(dy, w), want[rows]), at
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", EXACT)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_gradient_whole_numbers(m, n, k, dtype):
+    """Small whole numbers: every partial sum is exact in fp32, in any order."""
+    w, codes, _ = _weight(n + 1, n, k)
+    w.scales[:] = 1.0
+    dy = torch.from_numpy(np.random.default_rng(m).integers(-3, 4, (m, n)).astype(np.float32))
+    assert 3 * 127 * n < 1 << 24
+    ref = dy.double().to(DEV) @ torch.from_numpy(codes).double().to(DEV)
+    assert torch.equal(w4.mm_int8_t(dy.to(dtype).to(DEV), w).double(), ref)
+
+
+@pytest.mark.gpu
+def test_gradient_far_offsets():
+    """A weight of more than 2^31 bytes: rows of its codes alone, from either side of 2^31."""
+    n, k = 70003, 32768
+    codes = torch.randint(-127, 128, (n, k), dtype=torch.int8, device=DEV)
+    w = w4.Int8Rows(codes, torch.ones(n, device=DEV), n, k)
+    rows = torch.cat([torch.arange(4), torch.arange(65530, 65542), torch.arange(n - 24, n)]).to(DEV)
+    for dtype in (torch.bfloat16, torch.float16):
+        dy = torch.zeros(len(rows), n, dtype=dtype, device=DEV)
+        dy[torch.arange(len(rows), device=DEV), rows] = 2.0
+        assert torch.equal(w4.mm_int8_t(dy, w, out_dtype=dtype), 2 * codes[rows].to(dtype))
+
+
+@pytest.mark.gpu
+def test_gradient_segments():
+    """Several outputs side by side, rows of wider buffers, from the C entry."""
+    w, _, _ = _weight(61, 200, 96)
+    dy, _ = _rows(3, 40, 200, torch.bfloat16)
+    dy = dy.contiguous()
+    whole = w4.mm_int8_t(dy, w)
+    bufs = [torch.full((40, c + 3), 5.0, device=DEV) for c in (32, 7, 57)]
+    segs = (_lib.W4OutSeg * 3)(*[(b.data_ptr() + 4, b.shape[1] - 3, b.shape[1]) for b in bufs])
+    st = torch.cuda.current_stream().cuda_stream
+    size = ctypes.c_size_t(0)
+    assert w4.lib().w8a16_mm_t_workspace_bytes(40, 200, 96, 200, ctypes.byref(size)) == 0
+    ws = torch.empty(max(16, size.value), dtype=torch.uint8, device=DEV)
+    assert w4.lib().w8a16_mm_t(dy.data_ptr(), _lib.DT_BF16, 200, 40, w.codes.data_ptr(), w.scales.data_ptr(), 200, 96,
+                               _lib.DT_F32, segs, 3, ws.data_ptr(), size.value, st) == 0
+    assert torch.equal(torch.cat([b[:, 1:-2] for b in bufs], 1), whole)
+    for b in bufs:
+        assert (b[:, 0] == 5).all() and (b[:, -2:] == 5).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("m,n,k", [(32, 4096, 512), (131, 1003, 515)])
+def test_gradient_stream_and_graph(m, n, k, dtype):
+    w, _, _ = _weight(71, n, k)
+    dy = _rows(1, m, n, dtype)[0].contiguous()
+    want = w4.mm_int8_t(dy, w)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        got = w4.mm_int8_t(dy, w)
+    st.synchronize()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dx = w4.mm_int8_t(dy, w)
+    for i in range(3):
+        dy.copy_(_rows(200 + i, m, n, dtype)[0])
+        want = w4.mm_int8_t(dy, w)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dx, want)

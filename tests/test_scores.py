@@ -447,3 +447,48 @@ def test_forward_mode_raises(monkeypatch):
             with pytest.raises(RuntimeError, match="forward"), torch.no_grad():
                 w4.token_logprobs(z.t().contiguous().t(), t)
         assert w4.token_logprobs(torch.randn(2, 5), t).logprobs.shape == (2,)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,v", [(500, 17003), (250, 33001), (9, 70001), (1, 17003), (1100, 5003)])
+def test_every_column_counts_once(m, v, dtype):
+    """Rows of two logits, all else masked: one at a column of its own, which goes over the whole row
+    (over the edges of every 64 columns where that is too much), one at the first or the last.  Each
+    has probability 1/2: a logit lost or counted twice at a part's or a run's edge would show as
+    log p = 0 or -log 3, and a column without its gradient as a value other than +-1/2."""
+    cols = torch.arange(1, v - 1, device=DEV)
+    if m < 100:
+        cols = cols[(cols % 64 < 2) | (cols % 64 > 62)]
+        cols = cols[:: max(1, len(cols) // (m * 60)) | 1]
+    half = torch.full((m,), -math.log(2.0), device=DEV)
+    rows = torch.arange(m, device=DEV)
+    for at in range(0, len(cols), m):
+        j = cols[at:at + m]
+        j = torch.cat([j, cols[:m - len(j)]])
+        other = torch.where(rows % 2 == 0, 0, v - 1)
+        z = torch.full((m, v), -math.inf, dtype=dtype, device=DEV)
+        z[rows, j] = 4.0
+        z[rows, other] = 4.0
+        r = w4.token_logprobs(z, j, top=2)
+        # one logarithm of 2 (2^-24 of it and of its half ulp)
+        assert (r.logprobs - half).abs().max() <= 2.0**-22 and (r.entropy + half).abs().max() <= 2.0**-22, at
+        assert torch.equal(r.top_ids, torch.stack([torch.minimum(j, other), torch.maximum(j, other)], 1)), at
+        dz = w4.token_logprobs_grad(z, j, r.stats, r.entropy, r.top_ids, torch.ones(m, device=DEV))
+        want = torch.zeros_like(dz)
+        want[rows, j], want[rows, other] = 0.5, -0.5
+        assert ((dz - want).abs() <= 2.0**-20).all(), at
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [3, 200, 1100])
+def test_equal_logits_sum_to_their_number(m):
+    """A row of equal logits at a number of columns that fp32 counts exactly: log p = -log V."""
+    for v in (4096, 65536, 131072, 17003, 40001):
+        if m * v > 1 << 27:
+            continue
+        z = torch.full((m, v), -3.0, device=DEV)
+        r = w4.token_logprobs(z, torch.full((m,), v - 1, device=DEV))
+        # terms of 1 and sums of whole numbers are exact: one logarithm and its rounding are left
+        assert (r.logprobs.double() + math.log(v)).abs().max() <= 2.0**-20, v
+        assert (r.entropy.double() - math.log(v)).abs().max() <= 2.0**-20, v
