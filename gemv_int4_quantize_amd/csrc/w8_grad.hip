@@ -8,8 +8,8 @@
 // leaves over would double the work.  The error is that of a weight stored in that type (8 bits of
 // bf16, 11 of fp16).  fp16's short range is not w's: a power of two takes the largest scale of the
 // contraction to [2^7, 2^8) (codes to at most 2^15) and the sums are taken back by it, both
-// exactly.  Scales 2^21 times smaller than the largest one begin to lose bits.  (Measured: 1% at
-// M = 2048, (4096, 11008), 184 -> 186 us; 1 us of the scales' latency at M = 32, 17.4 -> 18.3.)
+// exactly.  Scales 2^21 times smaller than the largest one begin to lose bits.  (Measured: M = 2048,
+// (4096, 11008) 182 -> 185 us; M = 32 17.2 -> 17.7; M = 131, (2027, 1030), the kernel 8.0 -> 8.7.)
 //
 // What bounds it: at M = 2048, (N, K) = (4096, 8192) 118 us, 1165 TFLOP/s, where a bf16 product
 // whose weight needs no widening (the library's) takes 111.  The matrix cores are busy 57% of
@@ -148,30 +148,44 @@ __device__ __forceinline__ void grad_tile(char* smem, const uint16_t* __restrict
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
 
+  // fp16: the largest finite scale.  A thread's first eight are asked for ahead of the stages (loads
+  // return in order), the others behind them.
+  const int n_end = min(N, (k0 + KT) * BK);
+  uint32_t peak = 0;
+  auto take = [&](uint32_t u) { peak = umax(peak, (u & 0x7FFFFFFFu) < 0x7F800000u ? u & 0x7FFFFFFFu : 0u); };
+  auto scales8 = [&](int n) {
+    if (n + 8 <= n_end) return load_raw8<W4_DT_F32>(sw + n);
+    return n < n_end ? load_raw8_part<W4_DT_F32>(sw + n, n_end - n, 0u) : Raw8<W4_DT_F32>{};
+  };
+  Raw8<W4_DT_F32> first;
+  if constexpr (F16) {
+    first = scales8(k0 * BK + tid * 8);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 #pragma unroll
   for (int k = 0; k < NB - 1; ++k) dma(k, k, 0, UL);
   if constexpr (F16) {
     __shared__ uint32_t peaks[WN];
-    uint32_t m = 0;
-    const int n_end = min(N, (k0 + KT) * BK);
-    auto take = [&](uint32_t u) { m = umax(m, (u & 0x7FFFFFFFu) < 0x7F800000u ? u & 0x7FFFFFFFu : 0u); };
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) take(first.q[j >> 2][j & 3]);
 #pragma unroll 4
-    for (int n = k0 * BK + tid * 8; n < n_end; n += T * 8) {
-      if (n + 8 <= n_end) {
-        const Raw8<W4_DT_F32> s8 = load_raw8<W4_DT_F32>(sw + n);
+    for (int n = k0 * BK + (tid + T) * 8; n < n_end; n += T * 8) {
+      const Raw8<W4_DT_F32> s8 = scales8(n);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) take(s8.q[j >> 2][j & 3]);
-      } else {
-        for (int j = n; j < n_end; ++j) take(__float_as_uint(sw[j]));
-      }
+      for (int j = 0; j < 8; ++j) take(s8.q[j >> 2][j & 3]);
     }
-    m = wave_umax(m);
-    if (lane == 0) peaks[wave] = m;
-    __syncthreads();
+    peak = wave_umax(peak);
+    if (lane == 0) peaks[wave] = peak;
+    // this wave's LDS write done, then a barrier with no fence, which would wait for the stages
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < WN; ++i) m = umax(m, peaks[i]);
-    const int e = min(134 - (int)(__builtin_amdgcn_readfirstlane(m) >> 23), 126);
-    if (m != 0) {
+    for (int i = 0; i < WN; ++i) peak = umax(peak, peaks[i]);
+    const int e = min(134 - (int)(__builtin_amdgcn_readfirstlane(peak) >> 23), 126);
+    if (peak != 0) {
       up = __uint_as_float((uint32_t)(127 + e) << 23);
       down = __uint_as_float((uint32_t)(127 - e) << 23);
     }
