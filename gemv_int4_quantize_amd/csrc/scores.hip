@@ -18,10 +18,12 @@
 // logits at the threshold (many equal ones, or fewer unmasked than alternatives) collect
 // those above it, and of those equal to it the lowest ids in order, from the pairs' chunks.
 //
-// Both directions are bound by memory.  Measured at M = 2048, V = 128256 bf16: forward without
-// alternatives 98 us, with five 104 (5.1 TB/s), gradient 205 us (5.1 TB/s of reads and
-// writes; stores that bypass the caches, 319 -> 302 us for the pair).  Four fp32 rows with
-// twenty alternatives: 10 us and 5 for the join, both mostly latency.
+// Measured at M = 2048, V = 128256 bf16: forward without alternatives 95-100 us (5.3-5.5 TB/s),
+// with five 104 (5.0 TB/s), gradient 205 us (5.1 TB/s of reads and writes; stores that bypass the
+// caches, 319 -> 302 us for the pair).  The forward pass is bound by the vector units and by memory
+// together: counters have the former busy 77% of the cycles (74% with alternatives) while a plain
+// read reaches 6.75 TB/s; the gradient by memory (vector units 31%).  Four fp32 rows with twenty
+// alternatives: 10 us and 5 for the join, both mostly latency.
 #include <algorithm>
 
 #include "api_common.h"

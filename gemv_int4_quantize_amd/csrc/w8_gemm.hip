@@ -370,7 +370,9 @@ constexpr Tile kTiles[] = {
 // the write and read of its int32 planes (8 TB/s: they fit the caches).  The 256 x 256 tiles take
 // all of the columns, or those that make whole rounds, or none, and the lower tiles the others in
 // a shorter last round (M = 3000, (8192, 2048) 62.9 -> 58.8 us, M = 2048, (11008, 4096)
-// 100.5 -> 97.9).
+// 100.5 -> 97.9; on weights from memory, six of them in turn, 77.7 -> 71.1 and 121.6 -> 123.5, and
+// at M = 4096 208 -> 203.5).  The figures are those of calls on warm operands outside a graph; in
+// a captured graph a split costs a launch's 2.5 us and not the host's 4.5.
 W8Plan pick(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps, bool allow_split) {
   const int64_t cus = caps.cus > 0 ? caps.cus : 256, kt = ((K + 63) / 64 * 64 + BK - 1) / BK;
   W8Plan best;
