@@ -33,7 +33,7 @@ EXPORTS = (
 # every entry point declared in include/w8a8.h
 EXPORTS_W8 = (
     "w8_pitch", "w8_quantize_rows", "w8a8_workspace_bytes", "w8a16_mm_t_workspace_bytes", "w8a8_mm", "w8a8_linear",
-    "w8a16_mm_t", "w8a8_kernel", "tok_workspace_bytes", "tok_logprobs", "tok_logprobs_grad",
+    "w8a16_mm_t", "w8a32_mm_t_workspace_bytes", "w8a32_mm_t", "w8a8_kernel", "tok_workspace_bytes", "tok_logprobs", "tok_logprobs_grad",
 )
 
 
@@ -114,6 +114,8 @@ def lib() -> ctypes.CDLL:
     L.w8a8_mm.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, i32, pseg, i32, vp, sz, vp]
     L.w8a8_linear.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, vp, i32, pseg, i32, vp, sz, vp]
     L.w8a16_mm_t.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, i32, pseg, i32, vp, sz, vp]
+    L.w8a32_mm_t_workspace_bytes.argtypes = [i64, i64, i64, psz]
+    L.w8a32_mm_t.argtypes = [vp, i64, i64, vp, vp, i64, i64, i32, pseg, i32, vp, sz, vp]
     L.w8a8_kernel.argtypes = [i64, i64, i64, i32]
     L.w8a8_kernel.restype = ctypes.c_char_p
     L.tok_workspace_bytes.argtypes = [i64, i64, i32, psz]

@@ -80,6 +80,9 @@ bool grad_copies(int64_t M, int64_t N, int64_t ld) {
   return ld % 8 != 0 || N % 8 != 0 || ld >= kGradLd;
 }
 
+// Workspace of w8a32_mm_t ahead of the product's own: fp16 rows, and their powers of two.
+size_t half_bytes(int64_t M, int64_t N) { return up256((size_t)M * pitch_of(N) * 2) + up256((size_t)M * 4); }
+
 }  // namespace
 
 extern "C" {
@@ -214,7 +217,7 @@ int w8a16_mm_t(const void* dY, int dtype, int64_t ld, int64_t M, const int8_t* W
   if (M == 1) ld = N;
   size_t wsb = ws != nullptr ? ws_bytes : 0;
   char* w = static_cast<char*>(ws);
-  w4::W8GradArgs a = {static_cast<const uint16_t*>(dY), dtype == W4_DT_F16, ld, N, W, w_scales, ep, M, N, K, pitch_of(K)};
+  w4::W8GradArgs a = {static_cast<const uint16_t*>(dY), dtype == W4_DT_F16, ld, N, W, w_scales, ep, M, N, K, pitch_of(K), nullptr};
   if (grad_copies(M, N, ld) || !aligned(dY, 16)) {
     const int64_t npad = pitch_of(N);
     const size_t need = up256((size_t)M * npad * 2);
@@ -230,6 +233,44 @@ int w8a16_mm_t(const void* dY, int dtype, int64_t ld, int64_t M, const int8_t* W
     wsb -= need;
   }
   return launched(w4::launch_w8_grad(a, device_caps(), wsb > 0 ? w : nullptr, wsb, st), "w8a16_mm_t");
+}
+
+int w8a32_mm_t_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  const int s = check_sizes(M, N, K);
+  if (s != W4_OK) return s;
+  if (!bytes) return fail(W4_ERR_INVALID, "bytes is NULL");
+  *bytes = M == 0 ? 0 : half_bytes(M, N) + w4::w8_grad_workspace_bytes(M, N, K, device_caps());
+  return ok();
+}
+
+int w8a32_mm_t(const float* dY, int64_t ld, int64_t M, const int8_t* W, const float* w_scales, int64_t N, int64_t K,
+               int out_dtype, const w4_out_seg* segs, int nsegs, void* ws, size_t ws_bytes, void* stream) {
+  int s = check_sizes(M, N, K);
+  if (s != W4_OK) return s;
+  s = check_rows(dY, W4_DT_F32, M, N, ld, "dY");
+  if (s != W4_OK) return s;
+  w4::Epi ep;
+  s = make_epi(K, M, nullptr, out_dtype, segs, nsegs, &ep);
+  if (s != W4_OK) return s;
+  if (N >= kGradLd) return fail(W4_ERR_UNSUPPORTED, "N = %lld must be below 2^22", (long long)N);
+  if (M == 0) return ok();
+  s = check_weight(W, w_scales);
+  if (s == W4_OK) s = check_ws(ws);
+  if (s != W4_OK) return s;
+  const size_t need = half_bytes(M, N);
+  if (ws == nullptr || ws_bytes < need)
+    return fail(W4_ERR_RESOURCE, "w8a32_mm_t needs a workspace of %zu bytes (got %zu)", need,
+                ws != nullptr ? ws_bytes : (size_t)0);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const int64_t npad = pitch_of(N);
+  char* w = static_cast<char*>(ws);
+  uint16_t* half = reinterpret_cast<uint16_t*>(w);
+  int* back = reinterpret_cast<int*>(w + up256((size_t)M * npad * 2));
+  s = launched(w4::launch_half_rows(dY, M, N, ld, half, npad, back, st), "half_rows");
+  if (s != W4_OK) return s;
+  const w4::W8GradArgs a = {half, true, npad, npad, W, w_scales, ep, M, N, K, pitch_of(K), back};
+  const size_t left = ws_bytes - need;
+  return launched(w4::launch_w8_grad(a, device_caps(), left > 0 ? w + need : nullptr, left, st), "w8a32_mm_t");
 }
 
 int tok_workspace_bytes(int64_t M, int64_t V, int top, size_t* bytes) {

@@ -145,9 +145,14 @@ struct W8GradArgs {
   const float* w_scales;
   Epi ep;
   int64_t M, N, K, pitch;
+  const int* back;  // F16: powers of two that the rows' sums are multiplied by (or nullptr)
 };
 size_t w8_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps);
 hipError_t launch_w8_grad(const W8GradArgs& a, const DeviceCaps& caps, void* ws, size_t ws_bytes, hipStream_t st);
+
+// X [rows][cols] fp32, row stride ld -> out [rows][pitch] fp16 of X times 2^-back[row] (w8_quantize.hip).
+hipError_t launch_half_rows(const float* X, int64_t rows, int64_t cols, int64_t ld, uint16_t* out, int64_t pitch,
+                            int* back, hipStream_t st);
 
 // dY [M][N] 16-bit, row stride ld -> out [M][npad], zeros past column N.
 hipError_t launch_pad_rows(const uint16_t* dY, int64_t M, int64_t N, int64_t ld, uint16_t* out, int64_t npad,

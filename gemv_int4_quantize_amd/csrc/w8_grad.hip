@@ -9,7 +9,9 @@
 // bf16, 11 of fp16).  fp16's short range is not w's: a power of two takes the largest scale of the
 // contraction to [2^7, 2^8) (codes to at most 2^15) and the sums are taken back by it, both
 // exactly.  Scales 2^21 times smaller than the largest one begin to lose bits.  (Measured: M = 2048,
-// (4096, 11008) 182 -> 185 us; M = 32 17.2 -> 17.7; M = 131, (2027, 1030), the kernel 8.0 -> 8.7.)
+// (4096, 11008) 187.8 -> 188.4 us, M = 32 17.5 -> 18.2, M = 512, (8192, 2048) 32.4 -> 33.3; that the
+// rows' own powers of an fp32 dY were looked for in every launch spilled registers, 188 -> 194, so
+// theirs are kernels of their own.)
 //
 // What bounds it: at M = 2048, (N, K) = (4096, 8192) 118 us, 1165 TFLOP/s, where a bf16 product
 // whose weight needs no widening (the library's) takes 111.  The matrix cores are busy 57% of
@@ -53,10 +55,12 @@ constexpr int BK = 64;  // contraction rows of a stage
 // in the middle of a stage says that the next one has landed, and that the one before has been
 // read, whose slot is then filled; all codes of the next stage are read there, before those
 // loads are issued (the compiler waits for every load in flight ahead of a transposing read).
-template <int WN, int FM, bool F16>
+// BACK: row m's sums are multiplied by 2^back[m] as well (F16).
+template <int WN, int FM, bool F16, bool BACK>
 __device__ __forceinline__ void grad_tile(char* smem, const uint16_t* __restrict__ dY, const int8_t* __restrict__ W,
                                           const float* __restrict__ sw, const Epi& ep, int M, int N, int L, int K, int ld,
-                                          int pitch, int m0, int c0, int slice, int per, float* __restrict__ part) {
+                                          int pitch, int m0, int c0, int slice, int per, float* __restrict__ part,
+                                          const int* __restrict__ back) {
   constexpr int T = WN * 64, BM = FM * 32, BN = WN * 32, NB = 3;
   constexpr int UA = BM * 8 / T, CB = BN / 16, UB = BK * CB / T;  // chunks a thread loads in a stage
   static_assert(BM * 8 % T == 0 && BK * CB % T == 0, "tile split");
@@ -130,8 +134,9 @@ __device__ __forceinline__ void grad_tile(char* smem, const uint16_t* __restrict
 #pragma unroll
     for (int h = 0; h < 2; ++h) s[h] = *reinterpret_cast<const f32x4*>(base + OS + (16 * p + 8 * hi + 4 * h) * 4);
   };
-  // fp16: the powers of two that take the largest finite scale of this slice to [2^7, 2^8), and back
-  float up = 1.0f, down = 1.0f;
+  // fp16: the power of two that takes the largest finite scale of this slice to [2^7, 2^8)
+  int power = 0;
+  float up = 1.0f;
   auto widen = [&](const i32x2& v, const f32x4 (&s)[2], u32x4& o) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -184,11 +189,8 @@ __device__ __forceinline__ void grad_tile(char* smem, const uint16_t* __restrict
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int i = 0; i < WN; ++i) peak = umax(peak, peaks[i]);
-    const int e = min(134 - (int)(__builtin_amdgcn_readfirstlane(peak) >> 23), 126);
-    if (peak != 0) {
-      up = __uint_as_float((uint32_t)(127 + e) << 23);
-      down = __uint_as_float((uint32_t)(127 - e) << 23);
-    }
+    if (peak != 0) power = min(134 - (int)(__builtin_amdgcn_readfirstlane(peak) >> 23), 126);
+    up = __uint_as_float((uint32_t)(127 + power) << 23);
   }
   sync(std::integral_constant<int, NB - 2>());
   read_x(smem, 0, x[0]);
@@ -231,13 +233,28 @@ __device__ __forceinline__ void grad_tile(char* smem, const uint16_t* __restrict
   }
   // no direct LDS load may land after the workgroup's LDS is handed on
   __builtin_amdgcn_s_waitcnt(0x0070);
-  if constexpr (F16)
+  const int cbase = c0 + wave * 32, mbase = m0 + hi * 4, c = cbase + lr;
+  if constexpr (BACK) {
+    // by the weight's power and the row's own in one step: the product of the two may be no fp32
+    const rsrc_t rb = make_rsrc(back, (uint32_t)M * 4u);  // M < 2^30
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      __builtin_amdgcn_sched_barrier(0);  // sixteen rows' at a time: all at once would spill
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const u32x4 b = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                      rb, (int)((uint32_t)(mbase + i * 32 + g * 8) * 4u), 0, 0));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][g * 4 + q] = __builtin_ldexpf(acc[i][g * 4 + q], (int)b[q] - power);
+      }
+    }
+  } else if constexpr (F16) {
+    const float down = __uint_as_float((uint32_t)(127 - power) << 23);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][r] *= down;
-
-  const int cbase = c0 + wave * 32, mbase = m0 + hi * 4, c = cbase + lr;
+  }
   if (part == nullptr && epi_wide(ep, K) != 0) {
     const EpiQuad q = epi_quad(ep, cbase + (lr & ~3), K);
 #pragma unroll
@@ -274,10 +291,11 @@ struct Grid {
   int per;        // stages of a slice
 };
 
-template <int WN, int FB, int FM, bool F16>
+template <int WN, int FB, int FM, bool F16, bool BACK>
 __global__ __launch_bounds__(WN * 64) void w8_grad_kernel(const uint16_t* __restrict__ dY, const int8_t* __restrict__ W,
                                                           const float* __restrict__ sw, const Epi ep, int M, int N, int L,
-                                                          int K, int ld, int pitch, const Grid g, float* __restrict__ part) {
+                                                          int K, int ld, int pitch, const Grid g, float* __restrict__ part,
+                                                          const int* __restrict__ back) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int n_high = FB > 0 ? g.full * g.high : 0, n_all = n_high + (g.tn - g.full) * g.low;
   const int slice = blockIdx.x / (unsigned)n_all;
@@ -294,10 +312,11 @@ __global__ __launch_bounds__(WN * 64) void w8_grad_kernel(const uint16_t* __rest
   const int tr = grp * 8 + in_grp % rows_grp, tc = in_grp / rows_grp + (high ? 0 : g.full);
   if constexpr (FB > 0)
     if (high) {
-      grad_tile<WN, FB, F16>(smem, dY, W, sw, ep, M, N, L, K, ld, pitch, tr * FB * 32, tc * WN * 32, slice, g.per, part);
+      grad_tile<WN, FB, F16, BACK>(smem, dY, W, sw, ep, M, N, L, K, ld, pitch, tr * FB * 32, tc * WN * 32, slice, g.per, part,
+                              back);
       return;
     }
-  grad_tile<WN, FM, F16>(smem, dY, W, sw, ep, M, N, L, K, ld, pitch, tr * FM * 32, tc * WN * 32, slice, g.per, part);
+  grad_tile<WN, FM, F16, BACK>(smem, dY, W, sw, ep, M, N, L, K, ld, pitch, tr * FM * 32, tc * WN * 32, slice, g.per, part, back);
 }
 
 // Tiles of WN * 32 columns: FB * 32 rows (0: none) and FM * 32 rows, and what one stage of them
@@ -359,7 +378,9 @@ size_t plan_bytes(int64_t M, int64_t K, const GradPlan& p) { return p.splits > 1
 
 template <int WN, int FB, int FM>
 hipError_t run(const W8GradArgs& a, const GradPlan& p, float* part, hipStream_t st) {
-  auto k = a.f16 ? w8_grad_kernel<WN, FB, FM, true> : w8_grad_kernel<WN, FB, FM, false>;
+  auto k = !a.f16 ? w8_grad_kernel<WN, FB, FM, false, false>
+           : a.back == nullptr ? w8_grad_kernel<WN, FB, FM, true, false>
+                               : w8_grad_kernel<WN, FB, FM, true, true>;
   constexpr int rows = (FB > FM ? FB : FM) * 32;
   const int lds = 3 * ((p.full > 0 ? rows : FM * 32) * 128 + BK * WN * 32 + BK * 4);
   if (lds > 64 * 1024) {
@@ -376,7 +397,7 @@ hipError_t run(const W8GradArgs& a, const GradPlan& p, float* part, hipStream_t 
   const int splits = (kt + g.per - 1) / g.per;  // every slice gets at least one stage
   const int64_t wgs = ((int64_t)g.full * g.high + (int64_t)(g.tn - g.full) * g.low) * splits;
   k<<<(unsigned)wgs, WN * 64, lds, st>>>(a.dY, a.W, a.w_scales, a.ep, (int)a.M, (int)a.N, (int)a.L, (int)a.K, (int)a.ld,
-                                         (int)a.pitch, g, splits > 1 ? part : nullptr);
+                                         (int)a.pitch, g, splits > 1 ? part : nullptr, a.back);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   return launch_splitk_reduce(part, splits, a.M, 0, a.K, a.ep, st);

@@ -87,6 +87,50 @@ __global__ __launch_bounds__(1024) void quantize_long_rows_kernel(const void* __
     *reinterpret_cast<u32x2*>(codes + row * pitch + col) = bad ? u32x2{0u, 0u} : code8<DT>(load(col), rs.inv);
 }
 
+// fp32 rows to fp16 at a power of two each (w8a32_mm_t): 2^e takes a row's largest finite magnitude to
+// [2^14, 2^15), so that none overflows and only what is 2^-39 of it or less becomes 0; back = -e.
+// Columns cols .. pitch - 1 are 0.  One workgroup a row: a row is read twice, the second time from
+// cache.  Bound by memory: 14 us of a call at [2048][4096], 51 at [1024][32000] (a cast 7 and 32).
+__global__ __launch_bounds__(512) void half_rows_kernel(const float* __restrict__ X, int64_t cols, int64_t ld,
+                                                        int64_t pitch, uint16_t* __restrict__ out,
+                                                        int* __restrict__ back) {
+  constexpr int T = 512;
+  const int64_t row = blockIdx.x;
+  const float* x = X + row * ld;
+  auto load = [&](int64_t col) {
+    if (col + 8 <= cols) return load_raw8<W4_DT_F32>(x + col);
+    return col < cols ? load_raw8_part<W4_DT_F32>(x + col, (int)(cols - col), 0u) : Raw8<W4_DT_F32>{};
+  };
+  uint32_t m = 0;
+#pragma unroll 4
+  for (int64_t col = threadIdx.x * 8; col < cols; col += T * 8) {
+    const Raw8<W4_DT_F32> r = load(col);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t u = r.q[j >> 2][j & 3] & 0x7FFFFFFFu;
+      m = umax(m, u < 0x7F800000u ? u : 0u);
+    }
+  }
+  m = wave_umax(m);
+  __shared__ uint32_t part[T / 64];
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < T / 64; ++i) m = umax(m, part[i]);
+  const int e = m == 0 ? 0 : min(141 - (int)(m >> 23), 126);
+  const float f = __uint_as_float((uint32_t)(127 + e) << 23);
+  if (threadIdx.x == 0) back[row] = -e;
+#pragma unroll 4
+  for (int64_t col = threadIdx.x * 8; col < pitch; col += T * 8) {
+    float v[8];
+    widen8<W4_DT_F32>(load(col), v);
+    u32x4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = pack_f16x2(v[2 * j] * f, v[2 * j + 1] * f);
+    *reinterpret_cast<u32x4*>(out + row * pitch + col) = o;
+  }
+}
+
 template <int DT, int TPR, int C>
 hipError_t launch(const void* X, int64_t rows, int cols, int64_t ld, int pitch, int8_t* codes, float* scales,
                   hipStream_t st) {
@@ -108,6 +152,19 @@ hipError_t launch_dt(const void* X, int64_t rows, int cols, int64_t ld, int pitc
 }
 
 }  // namespace
+
+hipError_t launch_half_rows(const float* X, int64_t rows, int64_t cols, int64_t ld, uint16_t* out, int64_t pitch,
+                            int* back, hipStream_t st) {
+  // a launch holds fewer than 2^32 threads
+  constexpr int64_t kRows = (int64_t)1 << 22;
+  for (int64_t r = 0; r < rows; r += kRows) {
+    half_rows_kernel<<<(unsigned)std::min(kRows, rows - r), 512, 0, st>>>(X + r * ld, cols, ld, pitch, out + r * pitch,
+                                                                          back + r);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 hipError_t launch_quantize_rows(const void* X, int dt, int64_t rows, int64_t cols, int64_t ld, int8_t* codes,
                                 float* scales, hipStream_t st) {

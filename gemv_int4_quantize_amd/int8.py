@@ -280,6 +280,32 @@ def mm_int8_t(dy: torch.Tensor, w: Int8Rows, out: torch.Tensor | None = None,
     return out
 
 
+@functools.lru_cache(maxsize=4096)
+def _gradient32_bytes(M: int, N: int, K: int) -> int:
+    size = ctypes.c_size_t(0)
+    check(lib().w8a32_mm_t_workspace_bytes(M, N, K, ctypes.byref(size)))
+    return size.value
+
+
+def gradient_of_fp32(dy: torch.Tensor, w: Int8Rows, out_dtype: torch.dtype) -> torch.Tensor:
+    """mm_int8_t of an fp32 dY [M][N] with fp16 operands: each of its rows enters at a power of two of
+    its own, so that no size of dY is lost."""
+    dy = float_rows(dy, "dY")
+    M, N, K = dy.shape[0], w.rows, w.cols
+    if dy.dtype is not torch.float32 or dy.shape[1] != N:
+        raise ValueError(f"dY must be a float32 tensor of width {N}")
+    _check_rows(w, "weight")
+    out, segs = _new_output(M, K, out_dtype, dy.device)
+    with on_device(check_device(dy, w.codes, w.scales)):
+        size = _gradient32_bytes(M, N, K)
+        ws = space(size, dy.device)
+        status = lib().w8a32_mm_t(dy.data_ptr(), _row_stride(dy), M, w.codes.data_ptr(), w.scales.data_ptr(), N, K,
+                                  _ODT[out_dtype], segs, 1, ws.data_ptr() if ws is not None else None, size,
+                                  _stream(dy.device))
+    check(status)
+    return out
+
+
 def int8_kernel_for(M: int, N: int, K: int) -> str | None:
     """Name of the kernel that multiplies M float tokens by a weight of this shape (host-side query)."""
     r = lib().w8a8_kernel(M, N, K, _lib.DT_BF16)

@@ -109,16 +109,6 @@ class W4A16Linear(torch.nn.Module):
         return w4a16_linear(x, self.qw, self.bias, self.out_dtype)
 
 
-def _half_rows(g: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
-    """fp32 rows as fp16 ones at a power of two each (the row's largest magnitude to [2^14, 2^15),
-    so none overflows and what underflows is below 2^-39 of it), and the factors back [rows][1]."""
-    lo, hi = torch.aminmax(g, dim=1, keepdim=True)
-    power = (15 - torch.frexp(torch.maximum(hi, -lo)).exponent).clamp_(-126, 126)
-    one = torch.ones_like(lo)
-    out = torch.empty(g.shape, dtype=torch.float16, device=g.device)
-    return torch.mul(g, torch.ldexp(one, power), out=out), torch.ldexp(one, -power)
-
-
 class _W8A8Matmul(torch.autograd.Function):
     """Forward: tokens quantized to int8, integer product.  Backward: dX = dY @ (codes * scale)
     with 16-bit gradients, the rounding of the tokens passed straight through.  A bf16 or fp16
@@ -142,11 +132,9 @@ class _W8A8Matmul(torch.autograd.Function):
         if ctx.needs_input_grad[0]:
             g2 = gy.detach().reshape(-1, w.rows)
             if g2.dtype == torch.float32 and ctx.x_dtype == torch.float16:
-                g16, back = _half_rows(g2)
-                dx = int8.mm_int8_t(g16, w).mul_(back).to(ctx.x_dtype)
+                dx = int8.gradient_of_fp32(g2, w, ctx.x_dtype)
             else:
-                g16 = g2 if g2.dtype in _HALF else g2.to(torch.bfloat16)
-                dx = int8.mm_int8_t(g16, w, out_dtype=ctx.x_dtype)
+                dx = int8.mm_int8_t(g2 if g2.dtype in _HALF else g2.to(torch.bfloat16), w, out_dtype=ctx.x_dtype)
             dx = once(dx.view(*ctx.lead, w.cols), "w8a8_linear", gy)
         db = gy.reshape(-1, w.rows).float().sum(0).to(ctx.bias_dtype) if ctx.needs_input_grad[2] else None
         return dx, None, db, None

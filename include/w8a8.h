@@ -71,6 +71,14 @@ int w8a8_linear(const void* X, int x_dtype, int64_t ldx, int64_t M, const int8_t
 int w8a16_mm_t(const void* dY, int dtype, int64_t ld, int64_t M, const int8_t* W, const float* w_scales, int64_t N,
                int64_t K, int out_dtype, const w4_out_seg* segs, int nsegs, void* ws, size_t ws_bytes, void* stream);
 
+/* The same of an fp32 dY (row stride ld): w8a16_mm_t of F16 rows, each at a power of two that takes
+ * its largest finite magnitude to [2^14, 2^15), the sums taken back by it exactly.  Eleven bits
+ * of every dY down to 2^-29 of its row's largest; what is 2^-39 of it or less becomes 0.  The
+ * workspace that w8a32_mm_t_workspace_bytes reports is required. */
+int w8a32_mm_t_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
+int w8a32_mm_t(const float* dY, int64_t ld, int64_t M, const int8_t* W, const float* w_scales, int64_t N, int64_t K,
+               int out_dtype, const w4_out_seg* segs, int nsegs, void* ws, size_t ws_bytes, void* stream);
+
 /* Name of the kernel w8a8_mm (x_dtype < 0) / w8a8_linear launches for these sizes, given
  * the workspace w8a8_workspace_bytes reports; NULL when they are invalid.  Host only. */
 const char* w8a8_kernel(int64_t M, int64_t N, int64_t K, int x_dtype);

@@ -550,6 +550,7 @@ def test_second_derivatives_raise(monkeypatch):
 
     monkeypatch.setattr(int8, "mm_int8", lambda x, w, bias=None, out_dtype=None: x.float() @ value(w).t())
     monkeypatch.setattr(int8, "mm_int8_t", lambda g, w, out_dtype=torch.float32: (g.float() @ value(w)).to(out_dtype))
+    monkeypatch.setattr(int8, "gradient_of_fp32", lambda g, w, out_dtype: (g @ value(w)).to(out_dtype))
     w = w4.Int8Rows(torch.ones(8, 64, dtype=torch.int8), torch.ones(8), 8, 64)
     bias = torch.zeros(8, requires_grad=True)
     for b in (None, bias):
@@ -708,3 +709,79 @@ def test_gradient_stream_and_graph(m, n, k, dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(dx, want)
+
+
+def test_fp32_gradient_refusals():
+    def mt(dY=_p(), ld=64, M=4, N=64, K=128, segs=_seg(128), ws=_p(), wsb=1 << 20):
+        return w4.lib().w8a32_mm_t(dY, ld, M, _p(), _p(), N, K, 0, segs, 1, ws, wsb, None)
+
+    assert mt(dY=None) == _lib.W4_ERR_INVALID
+    assert mt(dY=_p(0x10002)) == _lib.W4_ERR_ALIGN
+    assert mt(ld=63) == _lib.W4_ERR_INVALID
+    assert mt(segs=_seg(64)) == _lib.W4_ERR_INVALID
+    assert mt(N=1 << 22, ld=1 << 22) == _lib.W4_ERR_UNSUPPORTED
+    assert mt(ws=_p(0x10008)) == _lib.W4_ERR_ALIGN
+    assert mt(M=0, dY=None, ws=None, wsb=0) == _lib.W4_OK
+    size = ctypes.c_size_t(0)
+    assert w4.lib().w8a32_mm_t_workspace_bytes(4, 63, 128, ctypes.byref(size)) == 0 and size.value >= 4 * 64 * 2 + 4 * 4
+    assert mt(wsb=4 * 64 * 2 + 255) == _lib.W4_ERR_RESOURCE and mt(ws=None) == _lib.W4_ERR_RESOURCE
+
+
+def _fp32_gradient(dy, w):
+    """The definition by way of the fp16 gradient: rows at their powers of two, results taken back.
+    (The powers on the host: the device's pow and ldexp of them are not exact.)"""
+    d = dy.cpu().numpy()
+    e = np.minimum(15 - np.frexp(np.abs(d).max(axis=1, keepdims=True))[1], 126)
+    half = torch.from_numpy(np.ldexp(d, e).astype(np.float16)).to(DEV)
+    y = np.ldexp(w4.mm_int8_t(half, w).double().cpu().numpy(), -e)
+    return torch.from_numpy(y).float().to(DEV)  # the result is fp32: so is its range
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k,pad", [(1, 1, 1, 0), (1, 64, 64, 0), (3, 100, 70, 3), (33, 4104, 2080, 0), (131, 2027, 515, 1),
+                                       (300, 1000, 520, 8), (16, 9001, 130, 0), (513, 72, 33000, 5), (5, 70001, 64, 0)])
+def test_fp32_gradient(m, n, k, pad):
+    from gemv_int4_quantize_amd.int8 import gradient_of_fp32
+
+    dy, _ = _rows(m + n, m, n, torch.float32, pad, scale=0.1)
+    if not pad:
+        dy = torch.from_numpy(np.ldexp(dy.cpu().numpy(), np.linspace(-60, 60, m).round().astype(int)[:, None])).to(DEV)
+    w, _, _ = _weight(k, n, k)
+    ref = _fp32_gradient(dy.contiguous(), w)
+    got = gradient_of_fp32(dy, w, torch.float32)
+    assert torch.equal(got, ref)
+    for dtype in (torch.float16, torch.bfloat16):
+        assert torch.equal(gradient_of_fp32(dy, w, dtype), ref.to(dtype))
+    far = w4.Int8Rows(w.codes, w.scales * 2.0**-90, n, k)  # neither power alone would do
+    up = dy * 2.0**60 if pad else dy.clamp(-1e15, 1e15) * 2.0**60
+    assert torch.equal(gradient_of_fp32(up, far, torch.float32), _fp32_gradient(up.contiguous(), far))
+
+
+@pytest.mark.gpu
+def test_fp32_gradient_special_rows_and_replays():
+    from gemv_int4_quantize_amd.int8 import gradient_of_fp32
+
+    w, _, _ = _weight(6, 200, 96)
+    w.codes[:, :96][w.codes[:, :96] == 0] = 1
+    dy = torch.randn(9, 200, device=DEV)
+    dy[1] = 0
+    dy[2, 5], dy[3, 7], dy[4, 0] = float("nan"), float("inf"), -float("inf")
+    dy[5], dy[6], dy[7] = 3e38, 2.0**-126, 2.0**-140
+    got = gradient_of_fp32(dy, w, torch.float32)
+    assert not got[1].any() and torch.isnan(got[2]).all() and torch.isinf(got[3:5]).all()
+    assert (got[3].sign() == w.codes[7, :96].sign()).all() and (got[4].sign() == -w.codes[0, :96].sign()).all()
+    assert torch.equal(got[5:7], _fp32_gradient(dy[5:7], w)) and got[7].abs().max() < 2.0**-126
+    assert gradient_of_fp32(dy[:0], w, torch.float32).shape == (0, 96)
+    graph = torch.cuda.CUDAGraph()
+    x = torch.randn(40, 200, device=DEV)
+    gradient_of_fp32(x, w, torch.float16)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        y = gradient_of_fp32(x, w, torch.float16)
+    for i in range(3):
+        x.normal_()
+        x *= 10.0 ** (8 * i - 8)
+        want = gradient_of_fp32(x, w, torch.float16)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
