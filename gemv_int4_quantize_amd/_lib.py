@@ -36,6 +36,12 @@ EXPORTS_W8 = (
     "w8a16_mm_t", "w8a32_mm_t_workspace_bytes", "w8a32_mm_t", "w8a8_kernel", "tok_workspace_bytes", "tok_logprobs", "tok_logprobs_grad",
 )
 
+# every entry point declared in include/mxfp4.h
+EXPORTS_MX = (
+    "mx4_pitch", "mx4_quantize_rows", "mx4_dequantize_rows", "mx4_workspace_bytes", "mx4_mm", "mx4_linear", "mx4_kernel",
+    "mx4_mm_t_workspace_bytes", "mx4_mm_t", "mx4_moe_workspace_bytes", "mx4_moe",
+)
+
 
 class W4Desc(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int64), ("mode", ctypes.c_int32), ("group", ctypes.c_int32)]
@@ -123,6 +129,22 @@ def lib() -> ctypes.CDLL:
     L.tok_logprobs_grad.argtypes = [vp, i32, i64, i64, i64, vp, i64, dbl, i32, vp, vp, vp, vp, vp, vp, vp, i64, vp]
     for name in EXPORTS_W8:
         if name not in ("w8_pitch", "w8a8_kernel"):
+            getattr(L, name).restype = ctypes.c_int
+    L.mx4_pitch.argtypes = [i64]
+    L.mx4_pitch.restype = i64
+    L.mx4_quantize_rows.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+    L.mx4_dequantize_rows.argtypes = [vp, vp, i64, i64, vp, i32, i64, vp]
+    L.mx4_workspace_bytes.argtypes = [i64, i64, i64, i32, psz]
+    L.mx4_mm.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, i32, pseg, i32, vp, sz, vp]
+    L.mx4_linear.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, vp, i32, pseg, i32, vp, sz, vp]
+    L.mx4_kernel.argtypes = [i64, i64, i64, i32]
+    L.mx4_kernel.restype = ctypes.c_char_p
+    L.mx4_mm_t_workspace_bytes.argtypes = [i64, i64, i64, i32, i64, psz]
+    L.mx4_mm_t.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, i32, pseg, i32, vp, sz, vp]
+    L.mx4_moe_workspace_bytes.argtypes = [i64, i64, i32, i64, i64, i32, psz]
+    L.mx4_moe.argtypes = [vp, i32, i64, i64, vp, i32, i64, i64, i32, i32, vp, vp, vp, vp, i64, i64, vp, i64, vp, sz, vp]
+    for name in EXPORTS_MX:
+        if name not in ("mx4_pitch", "mx4_kernel"):
             getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L

@@ -158,6 +158,80 @@ hipError_t launch_half_rows(const float* X, int64_t rows, int64_t cols, int64_t 
 hipError_t launch_pad_rows(const uint16_t* dY, int64_t M, int64_t N, int64_t ld, uint16_t* out, int64_t npad,
                            hipStream_t st);
 
+// ---- microscaled 4-bit operators (include/mxfp4.h)
+
+constexpr int64_t mx_pitch(int64_t cols) { return (cols + 127) / 128 * 128; }
+
+// X [rows][cols] (dtype dt, row stride ld) -> codes [rows][P / 2], scales [rows][P / 32], and back.
+hipError_t launch_mx_quantize(const void* X, int dt, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                              uint8_t* scales, hipStream_t st);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out, int dt,
+                                int64_t ldo, hipStream_t st);
+
+// X [rows][cols] -> out [rows][mx_parts(dt)][pitch] bf16, parts whose sum is X, zeros past the columns.
+constexpr int mx_parts(int dt) { return dt == W4_DT_F32 ? 3 : dt == W4_DT_F16 ? 2 : 1; }
+hipError_t launch_mx_parts(const void* X, int dt, int64_t rows, int64_t cols, int64_t ld, int64_t pitch, uint16_t* out,
+                           hipStream_t st);
+
+// Product of microscaled rows after validation.  X != nullptr: float activations (dtype x_dt, row
+// stride ldx) that the decode kernel quantizes itself; else A / a_scales.  P: padded columns.
+struct MxArgs {
+  const uint8_t* A;
+  const uint8_t* a_scales;
+  const void* X;
+  int x_dt;
+  int64_t ldx;
+  const uint8_t* W;
+  const uint8_t* w_scales;
+  Epi ep;
+  int64_t M, N, K, P;
+};
+size_t mx_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps);
+const char* mx_mm_name(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps);
+hipError_t launch_mx_mm(const MxArgs& a, const DeviceCaps& caps, void* ws, size_t ws_bytes, hipStream_t st);
+// Few tokens (mx_decode.hip); mx_fused: float tokens are quantized inside that launch.
+bool mx_fused(int64_t M, int64_t K);
+bool mx_decode_supported(int64_t M);
+hipError_t launch_mx_decode(const MxArgs& a, const DeviceCaps& caps, hipStream_t st);
+
+// Input gradient (mx_grad.hip): dY [M][parts][ld] bf16 parts (ld a multiple of 8, L <= ld columns of
+// each to read), 16-byte aligned.
+struct MxGradArgs {
+  const uint16_t* dY;
+  int parts;
+  int64_t ld, L;
+  const uint8_t* W;
+  const uint8_t* w_scales;
+  Epi ep;
+  int64_t M, N, K, P;
+};
+size_t mx_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int parts, const DeviceCaps& caps);
+hipError_t launch_mx_grad(const MxGradArgs& a, const DeviceCaps& caps, void* ws, size_t ws_bytes, hipStream_t st);
+
+// A layer of experts (mx_moe.hip) for T <= kMoeTokens tokens: x [T][mx_parts(dt)][ldx] bf16 parts
+// (rows 16-byte aligned), Hx columns of each (a multiple of 64) to read.
+constexpr int kMoeTokens = 64, kMoeTop = 16, kMoeExperts = 512;
+constexpr int moe_parts(int dt) { return dt == W4_DT_F32 ? 3 : 2; }  // of what lies between the products
+struct MoeArgs {
+  const uint16_t* x;
+  int64_t ldx, Hx;
+  const void* logits;
+  int ldt;
+  int64_t ldl;
+  const uint8_t* W1;
+  const uint8_t* w1_scales;
+  const uint8_t* W2;
+  const uint8_t* w2_scales;
+  int64_t T, E, H, F;
+  int top;
+  int renorm;
+  int dt;  // of x and the output
+  void* out;
+  int64_t ldo;
+};
+size_t moe_workspace_bytes(const MoeArgs& a, const DeviceCaps& caps);
+hipError_t launch_moe(const MoeArgs& a, const DeviceCaps& caps, void* ws, hipStream_t st);
+
 // ---- token scores (include/w8a8.h)
 
 struct TokArgs {
