@@ -5,9 +5,10 @@
 // in two launches: the choice of experts and g_j a_j, then the sum over experts (and, where the
 // rows of y alone would leave compute units idle, a third that adds its parts).
 //
-// What bounds it: the weights of the experts that some token reaches, each read once.  They go from
-// memory straight to registers, are widened to bf16 (exactly: two significant bits) and multiplied on
-// the matrix cores with up to sixteen tokens as the columns.  The activations enter as bf16 parts
+// What bounds it: the weights of the experts that some token reaches, each read once.  A wave has its own
+// ring of units in LDS, filled by direct loads (in registers their lanes, each at a row of its own,
+// cost the vector caches a tag for every 16 bytes); they are widened to bf16 (exactly: two significant
+// bits) and multiplied on the matrix cores with up to sixteen tokens as the columns.  The activations enter as bf16 parts
 // whose sum they are (one of bf16, two of fp16, three of fp32), and so does g_j a_j (two parts,
 // 16 bits; three for fp32): the matrix cores have time for it, and what lies between the two
 // products is not rounded to bf16's eight bits.
@@ -21,20 +22,29 @@ namespace w4 {
 
 namespace {
 
-constexpr int kNonTemporal = 2;  // cache-policy operand of a buffer load
 constexpr int kTokens = kMoeTokens, kMaxTop = kMoeTop, kMaxExperts = kMoeExperts;
 constexpr int kNone = 0x7FFF0000;  // a buffer offset that is out of range: 0 without a request
-constexpr uint32_t kOverflows = 253;  // stored exponents from which on a value may pass bf16's range
 constexpr int NW = 8;              // waves of a workgroup
 
 // The experts that the tokens reach, in the order of their numbers, as the second launch takes them
-// from the workspace: expert, bit set of its tokens, and its first row of a_j (rows in token order).
+// from the workspace: expert, its tokens' number and first row of g_j a_j, and the rows' tokens.
 struct Reached {
   uint64_t bad;  // tokens whose logits hold a NaN or +infinity
   int count;
   int expert[kMaxExperts];
-  int first[kMaxExperts];
-  uint64_t tokens[kMaxExperts];
+  int cols[kMaxExperts], first[kMaxExperts];
+  uint8_t token[kTokens * kMaxTop];
+};
+
+// What a workgroup of the first launch holds of the choice, and what it needs while it makes it.
+struct Routing : Reached {
+  float gate[kTokens * kMaxTop];  // g_j of each row
+};
+struct Choice {
+  uint64_t tokens[kMaxExperts];  // of each expert
+  float weight[kTokens][kMaxTop];
+  short chosen[kTokens][kMaxTop];
+  short slot[kMaxExperts];  // of each expert that is reached
 };
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -43,19 +53,11 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-template <int DT>
-__device__ __forceinline__ float logit(const void* z, int64_t i) {
-  return elem_to_f32<DT>(static_cast<const typename Elem<DT>::type*>(z)[i]);
+__device__ __forceinline__ float logit(const void* z, int dt, int64_t i) {
+  if (dt == W4_DT_F32) return static_cast<const float*>(z)[i];
+  const uint32_t b = static_cast<const uint16_t*>(z)[i];
+  return dt == W4_DT_F16 ? f16_bits_to_f32(b) : bf16_bits_to_f32(b);
 }
-
-struct Routing {
-  uint64_t tokens[kMaxExperts];  // of each expert
-  uint64_t bad;
-  int count;
-  int expert[kMaxExperts], first[kMaxExperts];  // those reached
-  short chosen[kTokens][kMaxTop];
-  float weight[kTokens][kMaxTop];
-};
 
 // Values as unsigned integers of the same order.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -63,270 +65,390 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Every workgroup makes the choice for all tokens, a wave a token: 64 lanes hold E / 64 logits each and
-// take the largest out `top` times.
-template <int DT>
-__device__ __forceinline__ void route(Routing& s, const void* __restrict__ logits, int64_t ldl, int T, int E, int top,
-                                      bool renorm) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  constexpr int C = kMaxExperts / 64;
-  for (int e = tid; e < E; e += NW * 64) s.tokens[e] = 0;
-  if (tid == 0) s.bad = 0;
-  __syncthreads();
+// A wave's choice for token t: lane l holds experts l C .. l C + C - 1, and the largest is taken out `top`
+// times, from the lowest lane and its lowest expert that hold it.
+template <int C>
+__device__ __forceinline__ void choose(Routing& s, Choice& c0, const void* __restrict__ logits, int ldt, int64_t ldl, int t, int E, int top,
+                                       bool renorm) {
+  const int lane = threadIdx.x & 63;
   const uint32_t masked = order_key(-__builtin_inff());
-  for (int t = wave; t < T; t += NW) {
-    uint32_t key[C];
-    float v[C];
-    bool odd = false;
+  uint32_t key[C];
+  float v[C];
+  bool odd = false;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int e = c * 64 + lane;
-      v[c] = e < E ? logit<DT>(logits, t * ldl + e) : -__builtin_inff();
-      odd |= !(v[c] < __builtin_inff());
-      // -0 and +0 are equal
-      key[c] = e < E ? order_key(v[c] + 0.0f) : 0u;
-    }
-    if (__ballot(odd) != 0) {
-      if (lane == 0) atomicOr(reinterpret_cast<unsigned long long*>(&s.bad), 1ull << t);
-      if (lane < top) s.chosen[t][lane] = -1;
-      continue;
-    }
-    float mx = 0.0f, total = 0.0f;
-    for (int j = 0; j < top; ++j) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int c = 0; c < C; ++c) best = umax(best, key[c]);
-      best = wave_umax(best);
-      int expert = -1;
-      float w = 0.0f;
-      if (best > masked) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const uint64_t at = __ballot(key[c] == best);
-          if (expert < 0 && at != 0) {
-            const int l = __builtin_ctzll(at);
-            expert = c * 64 + l;
-            if (lane == l) key[c] = 0;
-          }
-        }
-        const float z = __uint_as_float(best & 0x80000000u ? best & 0x7FFFFFFFu : ~best);
-        if (j == 0) mx = z;
-        w = expf(z - mx);
-        total += w;
-      }
-      if (lane == 0) {
-        s.chosen[t][j] = (short)expert;
-        s.weight[t][j] = w;
-        if (expert >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&s.tokens[expert]), 1ull << t);
-      }
-    }
-    __builtin_amdgcn_wave_barrier();  // lane 0's writes, then the other lanes' reads
-    if (!renorm) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int c = 0; c < C; ++c) sum += expf(v[c] - mx);
-      total = wave_sum(sum);
-    }
-    if (lane < top) s.weight[t][lane] = s.weight[t][lane] / total;
+  for (int c = 0; c < C; ++c) {
+    const int e = lane * C + c;
+    v[c] = e < E ? logit(logits, ldt, t * ldl + e) : -__builtin_inff();
   }
-  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    odd |= !(v[c] < __builtin_inff());
+    key[c] = lane * C + c < E ? order_key(v[c] + 0.0f) : 0u;  // -0 and +0 are equal
+  }
+  if (__ballot(odd) != 0) {
+    if (lane == 0) atomicOr(reinterpret_cast<unsigned long long*>(&s.bad), 1ull << t);
+    if (lane < top) c0.chosen[t][lane] = -1;
+    return;
+  }
+  float mx = 0.0f, total = 0.0f, weight = 0.0f;
+  int chosen = -1;
+  for (int j = 0; j < top; ++j) {
+    uint32_t own = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) own = umax(own, key[c]);
+    const uint32_t best = __builtin_amdgcn_readfirstlane(wave_umax(own));
+    if (best <= masked) break;
+    const int l = __builtin_ctzll(__ballot(own == best));
+    int at = 0;
+#pragma unroll
+    for (int c = C - 1; c >= 0; --c) at = key[c] == best ? c : at;
+    if (lane == l) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) key[c] = c == at ? 0u : key[c];
+    }
+    const int expert = l * C + __builtin_amdgcn_readlane(at, l);
+    const float z = __uint_as_float(best & 0x80000000u ? best & 0x7FFFFFFFu : ~best);
+    if (j == 0) mx = z;
+    const float w = expf(z - mx);
+    total += w;
+    if (lane == j) {  // lane j keeps choice j
+      chosen = expert;
+      weight = w;
+    }
+  }
+  if (!renorm) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) sum += expf(v[c] - mx);
+    total = wave_sum(sum);
+  }
+  if (lane < top) {
+    c0.chosen[t][lane] = (short)chosen;
+    c0.weight[t][lane] = weight / total;
+    if (chosen >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&c0.tokens[chosen]), 1ull << t);
+  }
+}
+
+// This wave's LDS reads and writes done, then a barrier with no fence (a fence would wait for the
+// weights in flight).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Every workgroup makes the choice for all tokens, a wave a token.
+__device__ __forceinline__ void route(Routing& s, Choice& c, const void* __restrict__ logits, int ldt, int64_t ldl, int T, int E,
+                                      int top, bool renorm) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int e = tid; e < E; e += NW * 64) c.tokens[e] = 0;
+  if (tid == 0) s.bad = 0;
+  lds_barrier();
+  for (int t = wave; t < T; t += NW) {
+    if (E <= 64) choose<1>(s, c, logits, ldt, ldl, t, E, top, renorm);
+    else if (E <= 128) choose<2>(s, c, logits, ldt, ldl, t, E, top, renorm);
+    else choose<kMaxExperts / 64>(s, c, logits, ldt, ldl, t, E, top, renorm);
+  }
+  lds_barrier();
   if (wave == 0) {
     int count = 0, rows = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
-      const int e = e0 + lane;
-      const uint64_t m = e < E ? s.tokens[e] : 0;
-      const uint64_t live = __ballot(m != 0);
-      int n = __popcll(m), before = n;
+      const int e = e0 + lane, n = e < E ? __popcll(c.tokens[e]) : 0;
+      const uint64_t live = __ballot(n != 0);
+      int upto = n;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
-        const int up = __shfl_up(before, d, 64);
-        if (lane >= d) before += up;
+        const int up = __shfl_up(upto, d, 64);
+        if (lane >= d) upto += up;
       }
-      if (m != 0) {
+      if (n != 0) {
         const int at = count + __popcll(live & ((1ull << lane) - 1));
         s.expert[at] = e;
-        s.first[at] = rows + before - n;
+        s.cols[at] = n;
+        s.first[at] = rows + upto - n;
+        c.slot[e] = (short)at;
       }
       count += __popcll(live);
-      rows += __shfl(before, 63, 64);
+      rows += __shfl(upto, 63, 64);
     }
     if (lane == 0) s.count = count;
   }
-  __syncthreads();
+  lds_barrier();
+  for (int i = tid; i < T * top; i += NW * 64) {
+    const int t = i / top, j = i - t * top, e = c.chosen[t][j];
+    if (e < 0) continue;
+    const int row = s.first[c.slot[e]] + __popcll(c.tokens[e] & ((1ull << t) - 1));
+    s.token[row] = (uint8_t)t;
+    s.gate[row] = c.weight[t][j];
+  }
+  lds_barrier();
 }
 
-// The i-th set bit of m.
-__device__ __forceinline__ int nth_bit(uint64_t m, int i) {
-  for (int k = 0; k < i; ++k) m &= m - 1;
-  return __builtin_ctzll(m);
-}
-
-template <int AUX>
-__device__ __forceinline__ u32x4 load16(rsrc_t r, int off, int soff) {
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, AUX));
-}
 __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// A wave's RT tiles of 16 weight rows over a unit of 256 columns: lane l takes two blocks of 32 columns
-// (from 64 (l / 16)) of row l % 16, so that its loads touch whole 128-byte lines, and the same
-// columns of the token that column l % 16 stands for.
-template <int RT>
-struct Unit {
-  u32x4 w[RT][2];
-  uint32_t e[RT];
+// A unit: 256 columns of RT tiles of 16 weight rows, 128 bytes and 8 exponents a row.  In LDS, a row's
+// 16-byte chunks (a block of 32 columns each) are at chunk ^ (row / 2 % 8), on the source address of
+// the direct loads, so that reads of 16 rows hit distinct banks; behind them the exponents, 8 bytes
+// a row in groups of 64 words.
+constexpr int RT = 2, kSlots = 3;
+
+// Where a lane's direct loads begin in a group of rows: 16 rows of codes by two loads of 8 rows, and the
+// exponents of 32 rows.
+struct Lanes {
+  int codes[2], exponents;
+  __device__ __forceinline__ Lanes(int P, int lane) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = 8 * j + (lane >> 3);
+      codes[j] = r * (P >> 1) + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+    }
+    exponents = (lane >> 1) * (P >> 5) + (lane & 1) * 4;
+  }
 };
 
-// Tiles [r0, r0 + n) from weight rows [first, first + rows) (rows past them: 0).
-template <int RT>
-__device__ __forceinline__ void load_tiles(Unit<RT>& t, int r0, int n, const uint8_t* W, const uint8_t* we, size_t first,
-                                           uint32_t rows, int P, int u, int lane) {
-  const int row = P >> 1, erow = P >> 5, r16 = lane & 15, q4 = lane >> 4;
-  const rsrc_t rw = mx_rsrc(W + first * row, rows * (uint32_t)row);
-  const rsrc_t re = mx_rsrc(we + first * erow, rows * (uint32_t)erow);
+// Direct loads of 16 rows (those from `rows` on: 0, without a request), unit u, to LDS.
+__device__ __forceinline__ void dma_codes(char* at, const uint8_t* W, uint32_t rows, int P, int u, const Lanes& l) {
+  const rsrc_t rw = mx_rsrc(W, rows * (uint32_t)(P >> 1));
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    if (r < r0 || r >= r0 + n) continue;
-    const int at = (r - r0) * 16 + r16;
+  for (int j = 0; j < 2; ++j)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(at + j * 1024), 16, (int)l.codes[j], (int)(u * 128), 0, 0);
+}
+__device__ __forceinline__ void dma_exponents(char* at, const uint8_t* we, uint32_t rows, int P, int u, const Lanes& l) {
+  const rsrc_t re = mx_rsrc(we, rows * (uint32_t)(P >> 5));
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(re, (lds_void*)at, 4, (int)l.exponents, (int)(u * 8), 0, 0);
+}
+
+// A unit's columns of sixteen tokens (column l % 16 is this lane's), NP parts `step` bytes after one
+// another: lane l takes blocks l / 16 and 4 + l / 16 of eight, where they lie inside the row of
+// `width` columns.
+template <int NP>
+struct Columns {
+  u32x4 x[NP][2][4];
+};
+template <int NP>
+__device__ __forceinline__ void load_columns(Columns<NP>& c, rsrc_t rx, int row, int u, int width, int step, int lane) {
+  const int col = u * 256 + (lane >> 4) * 32;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) t.w[r][h] = load16<kNonTemporal>(rw, at * row + q4 * 32 + h * 16, u * 128);
-    t.e[r] = __builtin_amdgcn_raw_buffer_load_b16(re, at * erow + q4 * 2, u * 8, 0);
+  for (int h = 0; h < 2; ++h) {
+    const int at = row != kNone && col + h * 128 < width ? row + (col + h * 128) * 2 : kNone;
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c.x[k][h][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at + i * 16, k * step, 0));
   }
 }
 
-// acc[r][b] += tile r times the sixteen columns of block b, whose parts (`step` bytes after one another)
-// begin at xo[b].  in: the lane's 64 columns lie in the row (else they are the next row's).
-template <int RT, int NP, int NB>
-__device__ __forceinline__ void multiply(const Unit<RT>& t, bool in, rsrc_t rx, const int (&xo)[NB], uint32_t blocks, int step,
-                                         f32x4 (&acc)[RT][NB]) {
+// acc[r] += tile r of the unit at `base` (its exponents at `ex`, tile r's GR bytes after one another)
+// times the columns.  whole: the unit's second half lies in the row, too.
+template <int NP, int GR>
+__device__ __forceinline__ void multiply(const char* base, const char* ex, const Columns<NP>& c, bool whole, int lane,
+                                         f32x4 (&acc)[RT]) {
+  const int r16 = lane & 15, q4 = lane >> 4;
+  const char* at = base + r16 * 128 + ((q4 ^ (r16 >> 1)) << 4);
+  u32x4 w[2][RT];
+  u32x2 e[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    w[0][r] = *reinterpret_cast<const u32x4*>(at + r * 2048);
+    w[1][r] = *reinterpret_cast<const u32x4*>(base + r * 2048 + r16 * 128 + (((4 + q4) ^ (r16 >> 1)) << 4));
+    e[r] = *reinterpret_cast<const u32x2*>(ex + r * GR + r16 * 8);
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    if (h == 1 && !whole) break;
     float p[RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) p[r] = in ? mx_power((t.e[r] >> (8 * h)) & 255u) : 1.0f;
+    for (int r = 0; r < RT; ++r) p[r] = mx_power((e[r][h] >> (8 * q4)) & 255u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       u32x4 a[RT];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) a[r] = mx_bf16x8(in ? t.w[r][h][i] : 0u, p[r]);
+      for (int r = 0; r < RT; ++r) a[r] = mx_bf16x8(w[h][r][i], p[r]);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if (NB > 1 && (blocks >> b & 1) == 0) continue;
+      for (int k = 0; k < NP; ++k)
 #pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          const u32x4 x = load16<0>(rx, xo[b] + h * 64 + i * 16, k * step);
-#pragma unroll
-          for (int r = 0; r < RT; ++r) acc[r][b] = mfma16(a[r], x, acc[r][b]);
-        }
-      }
+        for (int r = 0; r < RT; ++r) acc[r] = mfma16(a[r], c.x[k][h][i], acc[r]);
     }
   }
 }
 
-// The waves' sums of block b in LDS.
-template <int RT, int NB>
-__device__ __forceinline__ void put_sums(float (*sums)[RT * 16][17], const f32x4 (&acc)[RT][NB], int b, int wave, int lane) {
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sums[wave][r * 16 + (lane >> 4) * 4 + i][lane & 15] = acc[r][b][i];
+// All loads but the last n done.
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(n < 64, "the wait's counter");
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((n & 15) | 0xF70 | ((n >> 4) << 14));
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
-// First launch: the choice, then items of R x 16 gate rows and the same up rows of one expert, whose
-// contraction the workgroup's waves share.  x [T][NP][ldx] bf16 parts, Hx (a multiple of 64) columns
-// of each to read; a [rows][HP][Fp] bf16 parts of g_j a_j, a row for each expert and token of it.
-template <int DT, int LDT, int R, int NB>
+// First launch: the choice, then items of 16 gate rows and the same up rows of one expert, for sixteen of
+// its tokens at a time, whose contraction the workgroup's waves share.  While a wave multiplies a
+// unit, the columns of the next and the weights of the next two, of this item or those that follow,
+// are on their way, also while an item's sums are put together.
+// x [T][NP][ldx] bf16 parts, Hx (a multiple of 32) columns of each to read; a [rows][HP][Fp] bf16
+// parts of g_j a_j, a row for each expert and token of it.
+template <int DT>
 __global__ __launch_bounds__(NW * 64) void moe_up_kernel(const uint16_t* __restrict__ x, int ldx, int Hx,
-                                                         const void* __restrict__ logits, int64_t ldl,
+                                                         const void* __restrict__ logits, int ldt, int64_t ldl,
                                                          const uint8_t* __restrict__ W, const uint8_t* __restrict__ we, int T,
                                                          int E, int top, int renorm, int P, int F, int Fp,
                                                          uint16_t* __restrict__ a, Reached* __restrict__ reached) {
-  constexpr int NP = mx_parts(DT), HP = moe_parts(DT), RT = 2 * R;
+  constexpr int NP = mx_parts(DT), HP = moe_parts(DT), SLOT = RT * 2048 + 512;
+  constexpr int nD = 6, nX = NP * 8;  // loads of a unit's weights and columns
+  extern __shared__ __attribute__((aligned(16))) char ring[];  // [NW][kSlots][SLOT]
   __shared__ Routing s;
-  __shared__ float sums[NW][RT * 16][17];
+  __shared__ __attribute__((aligned(16))) float sums[2][NW][RT * 16][17];  // of items in turn
+  static_assert(sizeof(Choice) <= sizeof(sums), "the choice is made where the sums will be");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  route<LDT>(s, logits, ldl, T, E, top, renorm != 0);
+  route(s, *reinterpret_cast<Choice*>(&sums[0][0][0][0]), logits, ldt, ldl, T, E, top, renorm != 0);
+  const int count = __builtin_amdgcn_readfirstlane(s.count);
   if (blockIdx.x == 0) {  // for the second launch
-    for (int i = tid; i < s.count; i += NW * 64) {
+    for (int i = tid; i < count; i += NW * 64) {
       reached->expert[i] = s.expert[i];
+      reached->cols[i] = s.cols[i];
       reached->first[i] = s.first[i];
-      reached->tokens[i] = s.tokens[s.expert[i]];
     }
+    for (int i = tid; i < T * top; i += NW * 64) reached->token[i] = s.token[i];
     if (tid == 0) {
-      reached->count = s.count;
+      reached->count = count;
       reached->bad = s.bad;
     }
   }
-  const int tiles = Fp / (16 * R), items = s.count * tiles;
+  const int tiles = Fp / 16, items = count * tiles;
+  if ((int)blockIdx.x >= items) return;
   const int units = (P + 255) >> 8, per = (units + NW - 1) / NW;
   const int u0 = min(wave * per, units), u1 = min(u0 + per, units);
-  const int r16 = lane & 15, q4 = lane >> 4;
   const rsrc_t rx = mx_rsrc(x, (uint32_t)T * (uint32_t)(NP * ldx) * 2u);
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int slot = item / tiles, f0 = (item - slot * tiles) * 16 * R;
+  char* own = ring + wave * (kSlots * SLOT);
+
+  // An item, the tokens of its expert from b0, the unit (one step also where the wave has none), and
+  // the item's gate rows (`rows` that are to be read).
+  struct Place {
+    int item, b0, u, f0, cols, first;
+    uint32_t rows;
+    const uint8_t *w, *e;
+  };
+  const size_t codes_up = (size_t)F * (P >> 1), exponents_up = (size_t)F * (P >> 5);
+  auto enter = [&](Place& p) {
+    const int slot = p.item / tiles;
+    p.f0 = (p.item - slot * tiles) * 16;
     const int e = __builtin_amdgcn_readfirstlane(s.expert[slot]);
-    const uint64_t tokens = s.tokens[e];
-    const int cols = __popcll(tokens);
-    const uint32_t rows = (uint32_t)max(0, min(16 * R, F - f0));
-    int tok[NB];
-    uint32_t blocks = 0;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      tok[b] = b * 16 + r16 < cols ? nth_bit(tokens, b * 16 + r16) * (NP * ldx * 2) : kNone;
-      blocks |= (b * 16 < cols ? 1u : 0u) << b;
+    p.cols = __builtin_amdgcn_readfirstlane(s.cols[slot]);
+    p.first = __builtin_amdgcn_readfirstlane(s.first[slot]);
+    p.rows = u0 < u1 ? (uint32_t)max(0, min(16, F - p.f0)) : 0u;
+    const size_t g = (size_t)e * 2 * F + p.f0;
+    p.w = W + g * (P >> 1);
+    p.e = we + g * (P >> 5);
+  };
+  auto advance = [&](Place& p) {
+    if (p.u + 1 < u1) {
+      ++p.u;
+      return;
     }
-    blocks = __builtin_amdgcn_readfirstlane(blocks);
-    f32x4 acc[RT][NB];
+    p.u = u0;
+    p.b0 += 16;
+    if (p.b0 < p.cols) return;
+    p.b0 = 0;
+    p.item += gridDim.x;
+    if (p.item < items) enter(p);
+    else p.rows = 0u, p.cols = 0;
+  };
+  const Lanes lanes(P, lane);
+  auto load = [&](const Place& p, int slot) {
+    char* at = own + slot * SLOT;
+    dma_codes(at, p.w, p.rows, P, p.u, lanes);
+    dma_codes(at + 2048, p.w + codes_up, p.rows, P, p.u, lanes);
+    dma_exponents(at + RT * 2048, p.e, p.rows, P, p.u, lanes);
+    dma_exponents(at + RT * 2048 + 256, p.e + exponents_up, p.rows, P, p.u, lanes);
+  };
+  auto columns = [&](Columns<NP>& c, const Place& p) {
+    const int col = p.b0 + (lane & 15);
+    const bool has = p.u < u1 && col < p.cols;
+    load_columns<NP>(c, rx, has ? (int)s.token[p.first + col] * (NP * ldx * 2) : kNone, p.u, Hx, ldx * 2, lane);
+  };
+  f32x4 acc[RT];
+  auto begin = [&]() {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  // Sums of the waves, activation, weight, and the parts (as of mx_parts_kernel: the rest cut to eight
+  // bits, the last one rounded), by waves in turn.  One barrier an item: the next item's sums have a
+  // place of their own, and when they are written every wave has passed this one's.
+  int turn = 0;
+  auto finish = [&](const Place& p) {
+    float(*sum)[RT * 16][17] = sums[turn & 1];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) acc[r][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int u = u0; u < u1; ++u) {
-      Unit<RT> t;
-      load_tiles<RT>(t, 0, R, W, we, (size_t)e * 2 * F + f0, rows, P, u, lane);
-      load_tiles<RT>(t, R, R, W, we, ((size_t)e * 2 + 1) * F + f0, rows, P, u, lane);
-      const int col = u * 256 + q4 * 64;
-      int xo[NB];
+      for (int i = 0; i < 4; ++i) sum[wave][r * 16 + (lane >> 4) * 4 + i][lane & 15] = acc[r][i];
+    lds_barrier();
+    const int f = lane & 15, c = ((wave + turn) & (NW - 1)) * 4 + (lane >> 4), col = p.b0 + c;
+    ++turn;
+    if (c < 16 && col < p.cols) {
+      float g = 0.0f, up = 0.0f;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) xo[b] = col < Hx && tok[b] != kNone ? tok[b] + col * 2 : kNone;
-      multiply<RT, NP, NB>(t, col < P, rx, xo, blocks, ldx * 2, acc);
-    }
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      if (NB > 1 && (blocks >> b & 1) == 0) break;
-      put_sums<RT, NB>(sums, acc, b, wave, lane);
-      __syncthreads();
-      for (int i = tid; i < 16 * R * 16; i += NW * 64) {
-        const int f = i % (16 * R), c = i / (16 * R), col = b * 16 + c;
-        if (col >= cols) break;  // columns ascend with i
-        float g = 0.0f, up = 0.0f;
-#pragma unroll
-        for (int v = 0; v < NW; ++v) {
-          g += sums[v][f][c];
-          up += sums[v][16 * R + f][c];
-        }
-        const int t = nth_bit(tokens, col);
-        float w = 0.0f;
-        for (int j = 0; j < top; ++j) w = s.chosen[t][j] == e ? s.weight[t][j] : w;
-        float v = g / (1.0f + expf(-g)) * up * w;
-        uint16_t* o = a + (size_t)(s.first[slot] + col) * (HP * Fp) + f0 + f;
-        // parts as of mx_parts_kernel: the rest cut to eight bits
-        const bool odd = (__float_as_uint(v) & 0x7FFFFFFFu) >= 0x7F800000u;
-#pragma unroll
-        for (int k = 0; k < HP; ++k) {
-          uint32_t bits = __float_as_uint(v) >> 16;
-          if (k == HP - 1 && !odd) bits = pack_bf16x2(v, 0.0f) & 0xFFFFu;  // the last one rounded
-          if (odd) bits = k > 0 ? 0u : (__float_as_uint(v) & 0x7FFFFFu) != 0 ? 0x7FC0u : bits;
-          o[(size_t)k * Fp] = (uint16_t)bits;
-          v -= __uint_as_float(bits << 16);
-          if (odd) v = 0.0f;
-        }
+      for (int v = 0; v < NW; ++v) {
+        g += sum[v][f][c];
+        up += sum[v][16 + f][c];
       }
-      __syncthreads();
+      float v = g / (1.0f + expf(-g)) * up * s.gate[p.first + col];
+      uint16_t* o = a + (size_t)(p.first + col) * (HP * Fp) + p.f0 + f;
+      const bool odd = (__float_as_uint(v) & 0x7FFFFFFFu) >= 0x7F800000u;
+#pragma unroll
+      for (int k = 0; k < HP; ++k) {
+        uint32_t bits = __float_as_uint(v) >> 16;
+        if (k == HP - 1 && !odd) bits = pack_bf16x2(v, 0.0f) & 0xFFFFu;
+        if (odd) bits = k > 0 ? 0u : (__float_as_uint(v) & 0x7FFFFFu) != 0 ? 0x7FC0u : bits;
+        o[(size_t)k * Fp] = (uint16_t)bits;
+        v -= __uint_as_float(bits << 16);
+        if (odd) v = 0.0f;
+      }
     }
+  };
+  Place now, next, after;  // of the products, the columns, the weights
+  now.item = blockIdx.x;
+  now.b0 = 0;
+  now.u = u0;
+  enter(now);
+  load(now, 0);
+  next = now;
+  advance(next);
+  Columns<NP> c0, c1;
+  columns(c0, now);
+  load(next, 1);
+  after = next;
+  advance(after);
+  begin();
+  int slot = 0;
+  auto step = [&](const Columns<NP>& c, Columns<NP>& coming) {
+    const int spare = slot == 0 ? kSlots - 1 : slot - 1;
+    columns(coming, next);
+    load(after, spare);
+    wait_loads<2 * nD + nX>();
+    const char* at = own + slot * SLOT;
+    if (now.u < u1) multiply<NP, 256>(at, at + RT * 2048, c, now.u * 256 + 128 < P, lane, acc);
+    __builtin_amdgcn_sched_barrier(0);
+    slot = slot == kSlots - 1 ? 0 : slot + 1;
+    if (now.u + 1 >= u1) {
+      finish(now);
+      begin();
+    }
+    now = next;
+    next = after;
+    advance(after);
+    return now.item < items;
+  };
+  while (step(c0, c1) && step(c1, c0)) {
   }
+  wait_loads<0>();  // no direct LDS load may land after the workgroup's LDS is handed on
 }
 
 template <int DT>
@@ -336,95 +458,145 @@ __device__ __forceinline__ void store(void* out, int64_t i, float v) {
   else static_cast<uint16_t*>(out)[i] = f32_to_f16_bits(v);
 }
 
-// Second launch: RT x 16 rows of y for a workgroup, whose waves share the units of all reached experts,
-// with those of the other S - 1 workgroups of these rows.  The columns are the tokens, those that an
-// expert does not have being 0, so that the sum over experts stays in registers.
-template <int DT, int RT, int NB>
+// Second launch: 32 rows of y for a workgroup, whose waves share the units of all reached experts with
+// those of the other S - 1 workgroups of these rows.  The columns are sixteen of an expert's tokens; at
+// the end of its units a wave adds them to its own sums of all tokens in LDS, [T][32].  (Columns for
+// all tokens, 0 for those without the expert, would need no LDS but read and multiply zeros, and a
+// NaN among the weights would reach every token.)
+constexpr int kRowPitch = RT * 16 + 4;
+
+template <int DT, int SLOTS>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(const uint16_t* __restrict__ a, const Reached* __restrict__ reached,
                                                            const uint8_t* __restrict__ W, const uint8_t* __restrict__ we, int T,
-                                                           int rows_a, int H, int Fp, int S, void* __restrict__ out, int64_t ldo,
-                                                           float* __restrict__ part) {
-  constexpr int HP = moe_parts(DT);
+                                                           int E, int top, int H, int Fp, int S, void* __restrict__ out,
+                                                           int64_t ldo, float* __restrict__ part) {
+  constexpr int HP = moe_parts(DT), SLOT = RT * 2048 + 256;
+  constexpr int nD = 5, nX = HP * 8;  // loads of a unit's weights and columns
+  extern __shared__ __attribute__((aligned(16))) char smem[];  // rings [NW][SLOTS][SLOT], sums [NW][T][kRowPitch]
   __shared__ Reached s;
-  __shared__ float sums[NW][RT * 16][17];
+  float* sums = reinterpret_cast<float*>(smem + NW * SLOTS * SLOT);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int most = min(E, T * top);
+  for (int i = tid; i < most; i += NW * 64) {  // past the count: not used
+    s.expert[i] = reached->expert[i];
+    s.cols[i] = reached->cols[i];
+    s.first[i] = reached->first[i];
+  }
+  for (int i = tid; i < T * top; i += NW * 64) s.token[i] = reached->token[i];
   const int count = __builtin_amdgcn_readfirstlane(reached->count);
   const uint64_t bad = reached->bad;
-  for (int i = tid; i < count; i += NW * 64) {
-    s.expert[i] = reached->expert[i];
-    s.first[i] = reached->first[i];
-    s.tokens[i] = reached->tokens[i];
-  }
-  __syncthreads();
+  for (int i = tid; i < NW * T * kRowPitch; i += NW * 64) sums[i] = 0.0f;
+  lds_barrier();
   const int group = blockIdx.x / (unsigned)S, slice = blockIdx.x - group * S;
   const int h0 = group * 16 * RT;
   const uint32_t rows = (uint32_t)min(16 * RT, H - h0);
-  const int r16 = lane & 15, q4 = lane >> 4;
   const int of_expert = (Fp + 255) >> 8, units = count * of_expert;
   const int per = (units + S * NW - 1) / (S * NW);
   const int u0 = min((slice * NW + wave) * per, units), u1 = min(u0 + per, units);
-  const rsrc_t rx = mx_rsrc(a, (uint32_t)rows_a * (uint32_t)(HP * Fp) * 2u);
-  f32x4 acc[RT][NB];
+  const rsrc_t rx = mx_rsrc(a, (uint32_t)(T * top) * (uint32_t)(HP * Fp) * 2u);
+  float* mine = sums + wave * T * kRowPitch;
+  char* own = smem + wave * (SLOTS * SLOT);
+  if (u0 < u1) {
+    // An expert, its units [from, to) of this wave and the next of them, its tokens from b0.
+    struct Place {
+      int slot, b0, u, from, to, cols, first;
+      uint32_t rows;
+      const uint8_t *w, *e;
+    };
+    const int last_slot = (u1 - 1) / of_expert;
+    auto enter = [&](Place& p) {
+      const int e = __builtin_amdgcn_readfirstlane(s.expert[p.slot]);
+      p.cols = __builtin_amdgcn_readfirstlane(s.cols[p.slot]);
+      p.first = __builtin_amdgcn_readfirstlane(s.first[p.slot]);
+      p.from = max(u0 - p.slot * of_expert, 0);
+      p.to = min(of_expert, u1 - p.slot * of_expert);
+      p.u = p.from;
+      p.b0 = 0;
+      p.rows = rows;
+      const size_t first = (size_t)e * H + h0;
+      p.w = W + first * (Fp >> 1);
+      p.e = we + first * (Fp >> 5);
+    };
+    auto advance = [&](Place& p) {
+      if (++p.u < p.to) return;
+      p.u = p.from;
+      p.b0 += 16;
+      if (p.b0 < p.cols) return;
+      if (++p.slot <= last_slot) enter(p);
+      else p.rows = 0u, p.cols = 0;
+    };
+    const Lanes lanes(Fp, lane);
+    auto load = [&](const Place& p, int slot) {
+      char* at = own + slot * SLOT;
+      dma_codes(at, p.w, p.rows, Fp, p.u, lanes);
+      dma_codes(at + 2048, p.w + 16 * (Fp >> 1), p.rows > 16 ? p.rows - 16 : 0u, Fp, p.u, lanes);
+      dma_exponents(at + RT * 2048, p.e, p.rows, Fp, p.u, lanes);
+    };
+    auto columns = [&](Columns<HP>& c, const Place& p) {
+      const int col = p.b0 + (lane & 15);
+      load_columns<HP>(c, rx, col < p.cols ? (p.first + col) * (HP * Fp * 2) : kNone, p.u, Fp, Fp * 2, lane);
+    };
+    f32x4 acc[RT];
+    auto begin = [&]() {
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int b = 0; b < NB; ++b) acc[r][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int i = u0; i < u1; ++i) {
-    const int slot = i / of_expert, u = i - slot * of_expert;
-    const int e = __builtin_amdgcn_readfirstlane(s.expert[slot]);
-    Unit<RT> t;
-    load_tiles<RT>(t, 0, RT, W, we, (size_t)e * H + h0, rows, Fp, u, lane);
-    const uint64_t tokens = s.tokens[slot];
-    const int col = u * 256 + q4 * 64;
-    int xo[NB];
-    bool has[NB];
-    uint32_t blocks = 0;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int tk = b * 16 + r16;
-      has[b] = (tokens >> tk & 1) != 0;
-      const int at = s.first[slot] + __popcll(tokens & ((1ull << tk) - 1));
-      xo[b] = has[b] && col < Fp ? (at * (HP * Fp) + col) * 2 : kNone;
-      blocks |= ((tokens >> (b * 16) & 0xFFFF) != 0 ? 1u : 0u) << b;
+      for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    Place now, next, after;  // of the products, the columns, the weights
+    now.slot = u0 / of_expert;
+    enter(now);
+    load(now, 0);
+    next = now;
+    advance(next);
+    Columns<HP> c0, c1;
+    columns(c0, now);
+    after = next;
+    if constexpr (SLOTS == 3) {
+      load(next, 1);
+      advance(after);
     }
-    blocks = __builtin_amdgcn_readfirstlane(blocks);
-    // a weight that is NaN or past bf16's range must not reach the tokens without the expert, whose
-    // columns are 0: theirs are put back, a tile at a time
-    bool odd = false;
+    begin();
+    int slot = 0;
+    auto step = [&](const Columns<HP>& c, Columns<HP>& coming) {
+      const int spare = slot == 0 ? SLOTS - 1 : slot - 1;
+      columns(coming, next);
+      load(SLOTS == 3 ? after : next, spare);
+      wait_loads<(SLOTS - 1) * nD + nX>();
+      const char* at = own + slot * SLOT;
+      multiply<HP, 128>(at, at + RT * 2048, c, now.u * 256 + 128 < Fp, lane, acc);
+      __builtin_amdgcn_sched_barrier(0);
+      slot = slot == SLOTS - 1 ? 0 : slot + 1;
+      if (now.u + 1 >= now.to) {
+        const int col = now.b0 + (lane & 15);
+        if (col < now.cols) {
+          float* to = mine + s.token[now.first + col] * kRowPitch + (lane >> 4) * 4;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) odd |= (t.e[r] & 255u) >= kOverflows || (t.e[r] >> 8) >= kOverflows;
-    if (__ballot(odd) == 0) {
-      multiply<RT, HP, NB>(t, col < Fp, rx, xo, blocks, Fp * 2, acc);
-    } else {
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const Unit<1> one = {{{t.w[r][0], t.w[r][1]}}, {t.e[r]}};
-        f32x4 sum[1][NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) sum[0][b] = acc[r][b];
-        multiply<1, HP, NB>(one, col < Fp, rx, xo, blocks, Fp * 2, sum);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[r][b] = has[b] ? sum[0][b] : acc[r][b];
+          for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(to + r * 16) += acc[r];
+        }
+        begin();
       }
+      now = next;
+      if constexpr (SLOTS == 3) {
+        next = after;
+        advance(after);
+      } else {
+        advance(next);
+      }
+      return now.slot <= last_slot;
+    };
+    while (step(c0, c1) && step(c1, c0)) {
     }
+    wait_loads<0>();  // no direct LDS load may land after the workgroup's LDS is handed on
   }
+  lds_barrier();
+  for (int i = tid; i < T * RT * 16; i += NW * 64) {
+    const int t = i / (RT * 16), h = i - t * (RT * 16);
+    if (h >= (int)rows) continue;
+    float v = 0.0f;
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    if (b * 16 >= T) break;
-    put_sums<RT, NB>(sums, acc, b, wave, lane);
-    __syncthreads();
-    for (int i = tid; i < RT * 16 * 16; i += NW * 64) {
-      const int h = i % (RT * 16), c = i / (RT * 16), t = b * 16 + c;
-      if (t >= T) break;
-      if (h >= (int)rows) continue;
-      float v = 0.0f;
-#pragma unroll
-      for (int k = 0; k < NW; ++k) v += sums[k][h][c];
-      if (part != nullptr) part[((size_t)slice * T + t) * H + h0 + h] = v;
-      else store<DT>(out, t * ldo + h0 + h, (bad >> t & 1) != 0 ? __builtin_nanf("") : v);
-    }
-    __syncthreads();
+    for (int k = 0; k < NW; ++k) v += sums[(k * T + t) * kRowPitch + h];
+    if (part != nullptr) part[((size_t)slice * T + t) * H + h0 + h] = v;
+    else store<DT>(out, t * ldo + h0 + h, (bad >> t & 1) != 0 ? __builtin_nanf("") : v);
   }
 }
 
@@ -441,13 +613,11 @@ __global__ __launch_bounds__(256) void moe_join_kernel(const float* __restrict__
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Rows of the second launch's workgroups, and workgroups for the same rows: about two a CU.
-constexpr int kDownTiles = 4;
+// Workgroups of the second launch for the same rows: as many as a round of them, one a CU, holds.
 int down_slices(const MoeArgs& a, const DeviceCaps& caps) {
-  const int64_t groups = (a.H + kDownTiles * 16 - 1) / (kDownTiles * 16);
+  const int64_t groups = (a.H + RT * 16 - 1) / (RT * 16);
   const int64_t units = std::min<int64_t>(a.E, a.T * a.top) * ((mx_pitch(a.F) + 255) / 256);
-  int64_t s = (2 * (int64_t)caps.cus + groups - 1) / groups;
-  s = std::min(s, (units + NW - 1) / NW);
+  const int64_t s = std::min<int64_t>(caps.cus / groups, (units + NW - 1) / NW);
   return (int)std::max<int64_t>(1, std::min<int64_t>(s, 16));
 }
 
@@ -464,45 +634,48 @@ Space space_of(const MoeArgs& a, const DeviceCaps& caps) {
   return s;
 }
 
-template <int DT, int LDT, int R, int NB>
+template <typename K>
+hipError_t allow_lds(K k, int bytes) {
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int DT>
 hipError_t up(const MoeArgs& a, const DeviceCaps& caps, char* ws, const Space& sp, hipStream_t st) {
   const int64_t Fp = mx_pitch(a.F);
-  const int64_t items = std::min<int64_t>(a.E, a.T * a.top) * (Fp / (16 * R));
-  const int64_t wgs = std::max<int64_t>(1, std::min<int64_t>(items, 2 * (int64_t)caps.cus));
-  moe_up_kernel<DT, LDT, R, NB><<<(unsigned)wgs, NW * 64, 0, st>>>(
-      a.x, (int)a.ldx, (int)a.Hx, a.logits, a.ldl, a.W1, a.w1_scales, (int)a.T, (int)a.E, a.top, a.renorm, (int)mx_pitch(a.H),
-      (int)a.F, (int)Fp, reinterpret_cast<uint16_t*>(ws + sp.rows), reinterpret_cast<Reached*>(ws));
+  const int64_t items = std::min<int64_t>(a.E, a.T * a.top) * (Fp / 16);
+  const int64_t wgs = std::max<int64_t>(1, std::min<int64_t>(items, caps.cus));
+  constexpr int lds = NW * kSlots * (RT * 2048 + 512);
+  const hipError_t e = allow_lds(moe_up_kernel<DT>, lds);
+  if (e != hipSuccess) return e;
+  moe_up_kernel<DT><<<(unsigned)wgs, NW * 64, lds, st>>>(
+      a.x, (int)a.ldx, (int)a.Hx, a.logits, a.ldt, a.ldl, a.W1, a.w1_scales, (int)a.T, (int)a.E, a.top, a.renorm,
+      (int)mx_pitch(a.H), (int)a.F, (int)Fp, reinterpret_cast<uint16_t*>(ws + sp.rows), reinterpret_cast<Reached*>(ws));
   return hipGetLastError();
 }
 
-template <int DT, int LDT>
-hipError_t run_up(const MoeArgs& a, const DeviceCaps& caps, char* ws, const Space& sp, hipStream_t st) {
-  const int64_t items = std::min<int64_t>(a.E, a.T * a.top) * (mx_pitch(a.F) / 32);
-  const bool few = items < 2 * (int64_t)caps.cus;
-  if (a.T <= 16) return few ? up<DT, LDT, 1, 1>(a, caps, ws, sp, st) : up<DT, LDT, 2, 1>(a, caps, ws, sp, st);
-  return up<DT, LDT, 2, 4>(a, caps, ws, sp, st);
+template <int DT, int SLOTS>
+hipError_t down(const MoeArgs& a, char* ws, const Space& sp, int S, hipStream_t st) {
+  const int lds = NW * (SLOTS * (RT * 2048 + 256) + (int)a.T * kRowPitch * 4);
+  const hipError_t e = allow_lds(moe_down_kernel<DT, SLOTS>, lds);
+  if (e != hipSuccess) return e;
+  const int groups = (int)((a.H + RT * 16 - 1) / (RT * 16));
+  moe_down_kernel<DT, SLOTS><<<(unsigned)(groups * S), NW * 64, lds, st>>>(
+      reinterpret_cast<const uint16_t*>(ws + sp.rows), reinterpret_cast<const Reached*>(ws), a.W2, a.w2_scales, (int)a.T,
+      (int)a.E, a.top, (int)a.H, (int)mx_pitch(a.F), S, a.out, a.ldo, S > 1 ? reinterpret_cast<float*>(ws + sp.part) : nullptr);
+  return hipGetLastError();
 }
 
 template <int DT>
 hipError_t run(const MoeArgs& a, const DeviceCaps& caps, char* ws, hipStream_t st) {
   const Space sp = space_of(a, caps);
-  hipError_t e;
-  if (a.ldt == W4_DT_F32) e = run_up<DT, W4_DT_F32>(a, caps, ws, sp, st);
-  else if (a.ldt == W4_DT_F16) e = run_up<DT, W4_DT_F16>(a, caps, ws, sp, st);
-  else e = run_up<DT, W4_DT_BF16>(a, caps, ws, sp, st);
+  hipError_t e = up<DT>(a, caps, ws, sp, st);
   if (e != hipSuccess) return e;
   const int S = down_slices(a, caps);
-  const Reached* reached = reinterpret_cast<const Reached*>(ws);
-  const uint16_t* rows = reinterpret_cast<const uint16_t*>(ws + sp.rows);
-  float* part = S > 1 ? reinterpret_cast<float*>(ws + sp.part) : nullptr;
-  const int groups = (int)((a.H + kDownTiles * 16 - 1) / (kDownTiles * 16));
-  auto k = a.T <= 16 ? moe_down_kernel<DT, kDownTiles, 1> : moe_down_kernel<DT, kDownTiles, 4>;
-  k<<<(unsigned)(groups * S), NW * 64, 0, st>>>(rows, reached, a.W2, a.w2_scales, (int)a.T, (int)(a.T * a.top), (int)a.H,
-                                                (int)mx_pitch(a.F), S, a.out, a.ldo, part);
-  e = hipGetLastError();
+  // the sums of more tokens leave LDS for rings of two units
+  e = a.T <= 40 ? down<DT, 3>(a, ws, sp, S, st) : down<DT, 2>(a, ws, sp, S, st);
   if (e != hipSuccess || S == 1) return e;
-  moe_join_kernel<DT><<<dim3((unsigned)((a.H + 255) / 256), (unsigned)a.T), 256, 0, st>>>(part, reached, (int)a.T, (int)a.H, S,
-                                                                                        a.out, a.ldo);
+  moe_join_kernel<DT><<<dim3((unsigned)((a.H + 255) / 256), (unsigned)a.T), 256, 0, st>>>(
+      reinterpret_cast<const float*>(ws + sp.part), reinterpret_cast<const Reached*>(ws), (int)a.T, (int)a.H, S, a.out, a.ldo);
   return hipGetLastError();
 }
 
