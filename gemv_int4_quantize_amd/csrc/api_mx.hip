@@ -21,7 +21,7 @@ using w4::ok;
 constexpr int64_t kMaxCols = (int64_t)1 << 22;       // 32-bit offsets in a tile of 256 rows
 constexpr int64_t kMaxRows = ((int64_t)1 << 30) - 1;  // a launch holds fewer than 2^32 threads
 constexpr int64_t kMaxGradN = (int64_t)1 << 20;      // the same of three parts of 16 bits
-constexpr int64_t kMaxExpertWidth = (int64_t)1 << 18;
+constexpr int64_t kMaxExpertWidth = (int64_t)1 << 17;
 constexpr int64_t kDirectLd = (int64_t)1 << 22;
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -89,7 +89,7 @@ int check_moe(int64_t T, int64_t E, int top, int64_t H, int64_t F, int dtype) {
     return fail(W4_ERR_UNSUPPORTED, "E = %lld and top = %d must be at most %d and %d", (long long)E, top, w4::kMoeExperts,
                 w4::kMoeTop);
   if (H >= kMaxExpertWidth || F >= kMaxExpertWidth || T > kMaxRows)
-    return fail(W4_ERR_UNSUPPORTED, "H and F must be below 2^18, T below 2^30");
+    return fail(W4_ERR_UNSUPPORTED, "H and F must be below 2^17, T below 2^30");
   return W4_OK;
 }
 

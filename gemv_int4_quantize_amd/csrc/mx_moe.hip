@@ -22,18 +22,18 @@ namespace w4 {
 
 namespace {
 
+constexpr int kNonTemporal = 2;  // cache-policy operand of a load
 constexpr int kTokens = kMoeTokens, kMaxTop = kMoeTop, kMaxExperts = kMoeExperts;
 constexpr int kNone = 0x7FFF0000;  // a buffer offset that is out of range: 0 without a request
-constexpr int NW = 8;              // waves of a workgroup
+constexpr int NW = 4;              // waves of a workgroup; a CU holds two workgroups
 
 // The experts that the tokens reach, in the order of their numbers, as the second launch takes them
 // from the workspace: expert, its tokens' number and first row of g_j a_j, and the rows' tokens.
 struct Reached {
   uint64_t bad;  // tokens whose logits hold a NaN or +infinity
   int count;
-  int expert[kMaxExperts];
-  int cols[kMaxExperts], first[kMaxExperts];
-  uint8_t token[kTokens * kMaxTop];
+  uint16_t expert[kMaxExperts], first[kMaxExperts];
+  uint8_t cols[kMaxExperts], token[kTokens * kMaxTop];
 };
 
 // What a workgroup of the first launch holds of the choice, and what it needs while it makes it.
@@ -47,10 +47,24 @@ struct Choice {
   short slot[kMaxExperts];  // of each expert that is reached
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s, 64);
-  return v;
+// Maximum, minimum and sum over a row of sixteen lanes, in every lane of it.
+template <typename F>
+__device__ __forceinline__ uint32_t row_reduce(uint32_t v, F f) {
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));  // row mirror
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));  // half-row mirror
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));   // lane ^ 2
+  return f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));  // lane ^ 1
+}
+__device__ __forceinline__ uint32_t row_umax(uint32_t v) {
+  return row_reduce(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ uint32_t row_umin(uint32_t v) {
+  return row_reduce(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+__device__ __forceinline__ float row_sum(float v) {
+  return __uint_as_float(row_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
 }
 
 __device__ __forceinline__ float logit(const void* z, int dt, int64_t i) {
@@ -65,66 +79,61 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// A wave's choice for token t: lane l holds experts l C .. l C + C - 1, and the largest is taken out `top`
-// times, from the lowest lane and its lowest expert that hold it.
+// The choice for four tokens at a time, a row of sixteen lanes each (from token t0; none past T): lane l
+// of a row holds experts l C .. l C + C - 1, and the largest is taken out `top` times, the one of the
+// lowest number among equals; lane j keeps choice j.
 template <int C>
-__device__ __forceinline__ void choose(Routing& s, Choice& c0, const void* __restrict__ logits, int ldt, int64_t ldl, int t, int E, int top,
-                                       bool renorm) {
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ void choose(Routing& s, Choice& c0, const void* __restrict__ logits, int ldt, int64_t ldl, int t0,
+                                       int T, int E, int top, bool renorm) {
+  const int l16 = threadIdx.x & 15, t = t0 + ((threadIdx.x & 63) >> 4), first = l16 * C;
   const uint32_t masked = order_key(-__builtin_inff());
   uint32_t key[C];
   float v[C];
-  bool odd = false;
+#pragma unroll
+  for (int c = 0; c < C; ++c) v[c] = t < T && first + c < E ? logit(logits, ldt, t * ldl + first + c) : -__builtin_inff();
+  uint32_t odd = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int e = lane * C + c;
-    v[c] = e < E ? logit(logits, ldt, t * ldl + e) : -__builtin_inff();
+    odd |= !(v[c] < __builtin_inff()) ? 1u : 0u;
+    key[c] = order_key(v[c] + 0.0f);  // -0 and +0 are equal
   }
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    odd |= !(v[c] < __builtin_inff());
-    key[c] = lane * C + c < E ? order_key(v[c] + 0.0f) : 0u;  // -0 and +0 are equal
-  }
-  if (__ballot(odd) != 0) {
-    if (lane == 0) atomicOr(reinterpret_cast<unsigned long long*>(&s.bad), 1ull << t);
-    if (lane < top) c0.chosen[t][lane] = -1;
-    return;
-  }
-  float mx = 0.0f, total = 0.0f, weight = 0.0f;
+  odd = row_umax(odd);
+  float mx = 0.0f, z = -__builtin_inff();
   int chosen = -1;
   for (int j = 0; j < top; ++j) {
-    uint32_t own = 0;
+    uint32_t own = key[0];
 #pragma unroll
-    for (int c = 0; c < C; ++c) own = umax(own, key[c]);
-    const uint32_t best = __builtin_amdgcn_readfirstlane(wave_umax(own));
-    if (best <= masked) break;
-    const int l = __builtin_ctzll(__ballot(own == best));
-    int at = 0;
+    for (int c = 1; c < C; ++c) own = umax(own, key[c]);
+    const uint32_t best = row_umax(own);
+    uint32_t at = 0xFFFFu;
 #pragma unroll
-    for (int c = C - 1; c >= 0; --c) at = key[c] == best ? c : at;
-    if (lane == l) {
+    for (int c = C - 1; c >= 0; --c) at = key[c] == best ? (uint32_t)(first + c) : at;
+    at = row_umin(at);
 #pragma unroll
-      for (int c = 0; c < C; ++c) key[c] = c == at ? 0u : key[c];
-    }
-    const int expert = l * C + __builtin_amdgcn_readlane(at, l);
-    const float z = __uint_as_float(best & 0x80000000u ? best & 0x7FFFFFFFu : ~best);
-    if (j == 0) mx = z;
-    const float w = expf(z - mx);
-    total += w;
-    if (lane == j) {  // lane j keeps choice j
-      chosen = expert;
-      weight = w;
+    for (int c = 0; c < C; ++c) key[c] = at == (uint32_t)(first + c) ? 0u : key[c];
+    const float value = __uint_as_float(best & 0x80000000u ? best & 0x7FFFFFFFu : ~best);
+    if (j == 0 && best > masked) mx = value;
+    if (l16 == j && best > masked) {
+      chosen = (int)at;
+      z = value;
     }
   }
+  const float weight = expf(z - mx);  // 0 where there is none
+  float sum = weight;
   if (!renorm) {
-    float sum = 0.0f;
+    sum = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) sum += expf(v[c] - mx);
-    total = wave_sum(sum);
   }
-  if (lane < top) {
-    c0.chosen[t][lane] = (short)chosen;
-    c0.weight[t][lane] = weight / total;
+  const float total = row_sum(sum);
+  if (t >= T) return;
+  if (odd != 0) {
+    if (l16 == 0) atomicOr(reinterpret_cast<unsigned long long*>(&s.bad), 1ull << t);
+    chosen = -1;
+  }
+  if (l16 < top) {
+    c0.chosen[t][l16] = (short)chosen;
+    c0.weight[t][l16] = weight / total;
     if (chosen >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&c0.tokens[chosen]), 1ull << t);
   }
 }
@@ -138,7 +147,7 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// Every workgroup makes the choice for all tokens, a wave a token.
+// Every workgroup makes the choice for all tokens.
 __device__ __forceinline__ void route(Routing& s, Choice& c, const void* __restrict__ logits, int ldt, int64_t ldl, int T, int E,
                                       int top, bool renorm) {
   const int tid = threadIdx.x, lane = tid & 63;
@@ -146,10 +155,10 @@ __device__ __forceinline__ void route(Routing& s, Choice& c, const void* __restr
   for (int e = tid; e < E; e += NW * 64) c.tokens[e] = 0;
   if (tid == 0) s.bad = 0;
   lds_barrier();
-  for (int t = wave; t < T; t += NW) {
-    if (E <= 64) choose<1>(s, c, logits, ldt, ldl, t, E, top, renorm);
-    else if (E <= 128) choose<2>(s, c, logits, ldt, ldl, t, E, top, renorm);
-    else choose<kMaxExperts / 64>(s, c, logits, ldt, ldl, t, E, top, renorm);
+  for (int t = wave * 4; t < T; t += NW * 4) {
+    if (E <= 64) choose<4>(s, c, logits, ldt, ldl, t, T, E, top, renorm);
+    else if (E <= 128) choose<8>(s, c, logits, ldt, ldl, t, T, E, top, renorm);
+    else choose<kMaxExperts / 16>(s, c, logits, ldt, ldl, t, T, E, top, renorm);
   }
   lds_barrier();
   if (wave == 0) {
@@ -196,83 +205,123 @@ __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f3
 // a row in groups of 64 words.
 constexpr int RT = 2, kSlots = 3;
 
-// Where a lane's direct loads begin in a group of rows: 16 rows of codes by two loads of 8 rows, and the
-// exponents of 32 rows.
+constexpr int kSlot = RT * 2048 + 256;
+constexpr int column_bytes(int parts, int cols) { return cols == 4 ? parts * 2048 : 0; }  // in LDS, of a wave
+
+// Where a lane's direct loads begin: in 16 rows of codes by two loads of 8 rows, and in the exponents of
+// twice 16 rows, the second sixteen `apart` rows behind the first.
 struct Lanes {
   int codes[2], exponents;
-  __device__ __forceinline__ Lanes(int P, int lane) {
+  __device__ __forceinline__ Lanes(int P, int lane, int apart) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int r = 8 * j + (lane >> 3);
       codes[j] = r * (P >> 1) + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
     }
-    exponents = (lane >> 1) * (P >> 5) + (lane & 1) * 4;
+    exponents = ((lane >> 5) * apart + ((lane & 31) >> 1)) * (P >> 5) + (lane & 1) * 4;
   }
 };
 
 // Direct loads of 16 rows (those from `rows` on: 0, without a request), unit u, to LDS.
 __device__ __forceinline__ void dma_codes(char* at, const uint8_t* W, uint32_t rows, int P, int u, const Lanes& l) {
-  const rsrc_t rw = mx_rsrc(W, rows * (uint32_t)(P >> 1));
+  const rsrc_t rw = mx_rsrc(W, __builtin_amdgcn_readfirstlane(rows * (uint32_t)(P >> 1)));  // else a loop over lanes
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(at + j * 1024), 16, (int)l.codes[j], (int)(u * 128), 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(at + j * 1024), 16, (int)l.codes[j], (int)(u * 128), 0,
+                                             kNonTemporal);
 }
+// The exponents of both sixteens, of `rows` rows in all from the first.
 __device__ __forceinline__ void dma_exponents(char* at, const uint8_t* we, uint32_t rows, int P, int u, const Lanes& l) {
-  const rsrc_t re = mx_rsrc(we, rows * (uint32_t)(P >> 5));
+  const rsrc_t re = mx_rsrc(we, __builtin_amdgcn_readfirstlane(rows * (uint32_t)(P >> 5)));
   __builtin_amdgcn_raw_ptr_buffer_load_lds(re, (lds_void*)at, 4, (int)l.exponents, (int)(u * 8), 0, 0);
 }
 
-// A unit's columns of sixteen tokens (column l % 16 is this lane's), NP parts `step` bytes after one
-// another: lane l takes blocks l / 16 and 4 + l / 16 of eight, where they lie inside the row of
-// `width` columns.
-template <int NP>
+// A unit's columns for up to COLS tokens, NP bf16 parts `step` bytes after one another, on their way in
+// registers; lane l multiplies blocks l / 16 and 4 + l / 16 of eight for column l % 16.
+// COLS = 16: as they are multiplied.  COLS = 4 (eight loads would fetch mostly nothing, and the caches'
+// return path is what the weights need as well: 108 us with them, 96 without, 4 tokens on 2 of 8 experts
+// of 4096 x 11008): rows of four tokens by two loads a part, through LDS (put, [NP][4][512 bytes], the
+// 16-byte chunks of token t at chunk ^ t, so that reads hit distinct banks).
+template <int NP, int COLS>
 struct Columns {
-  u32x4 x[NP][2][4];
-};
-template <int NP>
-__device__ __forceinline__ void load_columns(Columns<NP>& c, rsrc_t rx, int row, int u, int width, int step, int lane) {
-  const int col = u * 256 + (lane >> 4) * 32;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int at = row != kNone && col + h * 128 < width ? row + (col + h * 128) * 2 : kNone;
-#pragma unroll
-    for (int k = 0; k < NP; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        c.x[k][h][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at + i * 16, k * step, 0));
-  }
-}
+  u32x4 x[NP][COLS == 4 ? 2 : 8];
 
-// acc[r] += tile r of the unit at `base` (its exponents at `ex`, tile r's GR bytes after one another)
-// times the columns.  whole: the unit's second half lies in the row, too.
-template <int NP, int GR>
-__device__ __forceinline__ void multiply(const char* base, const char* ex, const Columns<NP>& c, bool whole, int lane,
+  // row(c): byte offset of token c's columns, kNone for no token; `width` columns lie in a row
+  template <typename F>
+  __device__ __forceinline__ void fetch(rsrc_t rx, F row, int u, int width, int step, int lane) {
+    if constexpr (COLS == 4) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int t = 2 * j + (lane >> 5), chunk = (lane & 31) ^ t, col = u * 256 + chunk * 8, r = row(t);
+        const int at = r != kNone && col < width ? r + col * 2 : kNone;
+#pragma unroll
+        for (int k = 0; k < NP; ++k) x[k][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at, k * step, 0));
+      }
+    } else {
+      const int col = u * 256 + (lane >> 4) * 32, r = row(lane & 15);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = r != kNone && col + h * 128 < width ? r + (col + h * 128) * 2 : kNone;
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[k][h * 4 + i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at + i * 16, k * step, 0));
+      }
+    }
+  }
+  __device__ __forceinline__ void put(char* xs, int lane) const {
+    if constexpr (COLS == 4) {
+#pragma unroll
+      for (int k = 0; k < NP; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) *reinterpret_cast<u32x4*>(xs + k * 2048 + j * 1024 + lane * 16) = x[k][j];
+    }
+  }
+  __device__ __forceinline__ u32x4 operand(const char* xs, int k, int h, int i, int lane) const {
+    if constexpr (COLS == 4) {
+      const int t = lane & 3;  // columns past the fourth: not used
+      return *reinterpret_cast<const u32x4*>(xs + k * 2048 + t * 512 + ((((4 * h + (lane >> 4)) * 4 + i) ^ t) << 4));
+    } else {
+      return x[k][h * 4 + i];
+    }
+  }
+};
+
+// acc[r] += tile r of the unit at `base` times the columns.  whole: the unit's second half lies in the
+// row, too.
+// The conversion takes its power from the exponent bits of an fp32 alone (checked over all exponents,
+// 0 and NaN's among them, with any sign and mantissa): byte q4 of a word is rotated there.
+template <int NP, int COLS>
+__device__ __forceinline__ void multiply(const char* base, const Columns<NP, COLS>& c, const char* xs, bool whole, int lane,
                                          f32x4 (&acc)[RT]) {
   const int r16 = lane & 15, q4 = lane >> 4;
-  const char* at = base + r16 * 128 + ((q4 ^ (r16 >> 1)) << 4);
   u32x4 w[2][RT];
   u32x2 e[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    w[0][r] = *reinterpret_cast<const u32x4*>(at + r * 2048);
-    w[1][r] = *reinterpret_cast<const u32x4*>(base + r * 2048 + r16 * 128 + (((4 + q4) ^ (r16 >> 1)) << 4));
-    e[r] = *reinterpret_cast<const u32x2*>(ex + r * GR + r16 * 8);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      w[h][r] = *reinterpret_cast<const u32x4*>(base + r * 2048 + r16 * 128 + (((4 * h + q4) ^ (r16 >> 1)) << 4));
+    e[r] = *reinterpret_cast<const u32x2*>(base + RT * 2048 + r * 128 + r16 * 8);
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (h == 1 && !whole) break;
     float p[RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) p[r] = mx_power((e[r][h] >> (8 * q4)) & 255u);
+    for (int r = 0; r < RT; ++r) p[r] = __uint_as_float(__builtin_amdgcn_alignbit(e[r][h], e[r][h], 8 * q4 + 9));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       u32x4 a[RT];
 #pragma unroll
       for (int r = 0; r < RT; ++r) a[r] = mx_bf16x8(w[h][r][i], p[r]);
 #pragma unroll
-      for (int k = 0; k < NP; ++k)
+      for (int k = 0; k < NP; ++k) {
+        const u32x4 x = c.operand(xs, k, h, i, lane);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) acc[r] = mfma16(a[r], c.x[k][h][i], acc[r]);
+        for (int r = 0; r < RT; ++r) acc[r] = mfma16(a[r], x, acc[r]);
+      }
     }
   }
 }
@@ -288,27 +337,27 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// First launch: the choice, then items of 16 gate rows and the same up rows of one expert, for sixteen of
-// its tokens at a time, whose contraction the workgroup's waves share.  While a wave multiplies a
+// First launch: the choice, then items of 16 gate rows and the same up rows of one expert, for COLS of its
+// tokens at a time, whose contraction the workgroup's waves share.  While a wave multiplies a
 // unit, the columns of the next and the weights of the next two, of this item or those that follow,
 // are on their way, also while an item's sums are put together.
 // x [T][NP][ldx] bf16 parts, Hx (a multiple of 32) columns of each to read; a [rows][HP][Fp] bf16
 // parts of g_j a_j, a row for each expert and token of it.
-template <int DT>
+template <int DT, int COLS>
 __global__ __launch_bounds__(NW * 64) void moe_up_kernel(const uint16_t* __restrict__ x, int ldx, int Hx,
                                                          const void* __restrict__ logits, int ldt, int64_t ldl,
                                                          const uint8_t* __restrict__ W, const uint8_t* __restrict__ we, int T,
                                                          int E, int top, int renorm, int P, int F, int Fp,
                                                          uint16_t* __restrict__ a, Reached* __restrict__ reached) {
-  constexpr int NP = mx_parts(DT), HP = moe_parts(DT), SLOT = RT * 2048 + 512;
-  constexpr int nD = 6, nX = NP * 8;  // loads of a unit's weights and columns
-  extern __shared__ __attribute__((aligned(16))) char ring[];  // [NW][kSlots][SLOT]
+  constexpr int NP = mx_parts(DT), HP = moe_parts(DT);
+  constexpr int nD = 5, nX = COLS == 4 ? NP * 2 : NP * 8;  // loads of a unit's weights and columns
+  extern __shared__ __attribute__((aligned(16))) char ring[];  // [NW][kSlots][kSlot], then columns [NW][column_bytes]
   __shared__ Routing s;
-  __shared__ __attribute__((aligned(16))) float sums[2][NW][RT * 16][17];  // of items in turn
-  static_assert(sizeof(Choice) <= sizeof(sums), "the choice is made where the sums will be");
+  __shared__ __attribute__((aligned(16))) float sums[2][NW][RT * 16][COLS + 1];  // of items in turn
+  static_assert(sizeof(Choice) <= NW * kSlots * kSlot, "the choice is made where the ring will be");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  route(s, *reinterpret_cast<Choice*>(&sums[0][0][0][0]), logits, ldt, ldl, T, E, top, renorm != 0);
+  route(s, *reinterpret_cast<Choice*>(ring), logits, ldt, ldl, T, E, top, renorm != 0);
   const int count = __builtin_amdgcn_readfirstlane(s.count);
   if (blockIdx.x == 0) {  // for the second launch
     for (int i = tid; i < count; i += NW * 64) {
@@ -322,57 +371,61 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(const uint16_t* __restr
       reached->bad = s.bad;
     }
   }
-  const int tiles = Fp / 16, items = count * tiles;
-  if ((int)blockIdx.x >= items) return;
-  const int units = (P + 255) >> 8, per = (units + NW - 1) / NW;
-  const int u0 = min(wave * per, units), u1 = min(u0 + per, units);
+  const int tiles = Fp / 16;
+  if ((int)blockIdx.x >= count * tiles) return;
+  const int units = (P + 255) >> 8;  // wave w takes units w, w + NW, ..
   const rsrc_t rx = mx_rsrc(x, (uint32_t)T * (uint32_t)(NP * ldx) * 2u);
-  char* own = ring + wave * (kSlots * SLOT);
+  char* own = ring + wave * (kSlots * kSlot);
+  char* xs = ring + NW * kSlots * kSlot + wave * column_bytes(NP, COLS);
 
-  // An item, the tokens of its expert from b0, the unit (one step also where the wave has none), and
-  // the item's gate rows (`rows` that are to be read).
+  // An item (a tile of the expert in a slot), the tokens of its expert from b0, the unit (one step also
+  // where the wave has none), and the item's gate rows (`rows` that are to be read).
   struct Place {
-    int item, b0, u, f0, cols, first;
+    int slot, tile, b0, u, cols, first;
     uint32_t rows;
     const uint8_t *w, *e;
   };
-  const size_t codes_up = (size_t)F * (P >> 1), exponents_up = (size_t)F * (P >> 5);
+  const size_t codes_up = (size_t)F * (P >> 1);
   auto enter = [&](Place& p) {
-    const int slot = p.item / tiles;
-    p.f0 = (p.item - slot * tiles) * 16;
-    const int e = __builtin_amdgcn_readfirstlane(s.expert[slot]);
-    p.cols = __builtin_amdgcn_readfirstlane(s.cols[slot]);
-    p.first = __builtin_amdgcn_readfirstlane(s.first[slot]);
-    p.rows = u0 < u1 ? (uint32_t)max(0, min(16, F - p.f0)) : 0u;
-    const size_t g = (size_t)e * 2 * F + p.f0;
+    const int e = __builtin_amdgcn_readfirstlane(s.expert[p.slot]), f0 = p.tile * 16;
+    p.cols = __builtin_amdgcn_readfirstlane(s.cols[p.slot]);
+    p.first = __builtin_amdgcn_readfirstlane(s.first[p.slot]);
+    p.rows = wave < units ? (uint32_t)max(0, min(16, F - f0)) : 0u;
+    const size_t g = (size_t)e * 2 * F + f0;
     p.w = W + g * (P >> 1);
     p.e = we + g * (P >> 5);
   };
+  const int more_slots = gridDim.x / (unsigned)tiles, more_tiles = gridDim.x - more_slots * tiles;
   auto advance = [&](Place& p) {
-    if (p.u + 1 < u1) {
-      ++p.u;
+    if (p.u + NW < units) {
+      p.u += NW;
       return;
     }
-    p.u = u0;
-    p.b0 += 16;
+    p.u = wave;
+    p.b0 += COLS;
     if (p.b0 < p.cols) return;
     p.b0 = 0;
-    p.item += gridDim.x;
-    if (p.item < items) enter(p);
+    p.slot += more_slots;
+    p.tile += more_tiles;
+    if (p.tile >= tiles) {
+      p.tile -= tiles;
+      ++p.slot;
+    }
+    if (p.slot < count) enter(p);
     else p.rows = 0u, p.cols = 0;
   };
-  const Lanes lanes(P, lane);
+  const Lanes lanes(P, lane, F);
   auto load = [&](const Place& p, int slot) {
-    char* at = own + slot * SLOT;
+    char* at = own + slot * kSlot;
     dma_codes(at, p.w, p.rows, P, p.u, lanes);
     dma_codes(at + 2048, p.w + codes_up, p.rows, P, p.u, lanes);
-    dma_exponents(at + RT * 2048, p.e, p.rows, P, p.u, lanes);
-    dma_exponents(at + RT * 2048 + 256, p.e + exponents_up, p.rows, P, p.u, lanes);
+    // (gate rows past the last get up rows' exponents: with codes 0, and their sums are not used)
+    dma_exponents(at + RT * 2048, p.e, p.rows > 0 ? F + p.rows : 0u, P, p.u, lanes);
   };
-  auto columns = [&](Columns<NP>& c, const Place& p) {
-    const int col = p.b0 + (lane & 15);
-    const bool has = p.u < u1 && col < p.cols;
-    load_columns<NP>(c, rx, has ? (int)s.token[p.first + col] * (NP * ldx * 2) : kNone, p.u, Hx, ldx * 2, lane);
+  auto columns = [&](Columns<NP, COLS>& c, const Place& p) {
+    c.fetch(rx, [&](int t) {
+      return p.u < units && p.b0 + t < p.cols ? (int)s.token[p.first + p.b0 + t] * (NP * ldx * 2) : kNone;
+    }, p.u, Hx, ldx * 2, lane);
   };
   f32x4 acc[RT];
   auto begin = [&]() {
@@ -384,23 +437,26 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(const uint16_t* __restr
   // place of their own, and when they are written every wave has passed this one's.
   int turn = 0;
   auto finish = [&](const Place& p) {
-    float(*sum)[RT * 16][17] = sums[turn & 1];
+    float(*sum)[RT * 16][COLS + 1] = sums[turn & 1];
+    if ((lane & 15) < COLS) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum[wave][r * 16 + (lane >> 4) * 4 + i][lane & 15] = acc[r][i];
+        for (int i = 0; i < 4; ++i) sum[wave][r * 16 + (lane >> 4) * 4 + i][lane & 15] = acc[r][i];
+    }
     lds_barrier();
     const int f = lane & 15, c = ((wave + turn) & (NW - 1)) * 4 + (lane >> 4), col = p.b0 + c;
     ++turn;
-    if (c < 16 && col < p.cols) {
+    static_assert(NW == 4, "sixteen tokens, four a wave");
+    if (c < COLS && col < p.cols) {
       float g = 0.0f, up = 0.0f;
 #pragma unroll
       for (int v = 0; v < NW; ++v) {
         g += sum[v][f][c];
         up += sum[v][16 + f][c];
       }
-      float v = g / (1.0f + expf(-g)) * up * s.gate[p.first + col];
-      uint16_t* o = a + (size_t)(p.first + col) * (HP * Fp) + p.f0 + f;
+      float v = p.tile * 16 + f < F ? g / (1.0f + expf(-g)) * up * s.gate[p.first + col] : 0.0f;
+      uint16_t* o = a + (size_t)(p.first + col) * (HP * Fp) + p.tile * 16 + f;
       const bool odd = (__float_as_uint(v) & 0x7FFFFFFFu) >= 0x7F800000u;
 #pragma unroll
       for (int k = 0; k < HP; ++k) {
@@ -414,37 +470,39 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(const uint16_t* __restr
     }
   };
   Place now, next, after;  // of the products, the columns, the weights
-  now.item = blockIdx.x;
+  now.slot = blockIdx.x / (unsigned)tiles;
+  now.tile = blockIdx.x - now.slot * tiles;
   now.b0 = 0;
-  now.u = u0;
+  now.u = wave;
   enter(now);
   load(now, 0);
   next = now;
   advance(next);
-  Columns<NP> c0, c1;
+  Columns<NP, COLS> c0, c1;
   columns(c0, now);
   load(next, 1);
   after = next;
   advance(after);
   begin();
+  c0.put(xs, lane);
   int slot = 0;
-  auto step = [&](const Columns<NP>& c, Columns<NP>& coming) {
+  auto step = [&](const Columns<NP, COLS>& c, Columns<NP, COLS>& coming) {
     const int spare = slot == 0 ? kSlots - 1 : slot - 1;
     columns(coming, next);
     load(after, spare);
     wait_loads<2 * nD + nX>();
-    const char* at = own + slot * SLOT;
-    if (now.u < u1) multiply<NP, 256>(at, at + RT * 2048, c, now.u * 256 + 128 < P, lane, acc);
+    if (now.u < units) multiply<NP, COLS>(own + slot * kSlot, c, xs, now.u * 256 + 128 < P, lane, acc);
     __builtin_amdgcn_sched_barrier(0);
     slot = slot == kSlots - 1 ? 0 : slot + 1;
-    if (now.u + 1 >= u1) {
+    if (now.u + NW >= units) {
       finish(now);
       begin();
     }
+    coming.put(xs, lane);
     now = next;
     next = after;
     advance(after);
-    return now.item < items;
+    return now.slot < count;
   };
   while (step(c0, c1) && step(c1, c0)) {
   }
@@ -459,22 +517,23 @@ __device__ __forceinline__ void store(void* out, int64_t i, float v) {
 }
 
 // Second launch: 32 rows of y for a workgroup, whose waves share the units of all reached experts with
-// those of the other S - 1 workgroups of these rows.  The columns are sixteen of an expert's tokens; at
+// those of the other S - 1 workgroups of these rows.  The columns are COLS of an expert's tokens; at
 // the end of its units a wave adds them to its own sums of all tokens in LDS, [T][32].  (Columns for
 // all tokens, 0 for those without the expert, would need no LDS but read and multiply zeros, and a
 // NaN among the weights would reach every token.)
 constexpr int kRowPitch = RT * 16 + 4;
 
-template <int DT, int SLOTS>
+template <int DT, int COLS, int SLOTS>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(const uint16_t* __restrict__ a, const Reached* __restrict__ reached,
                                                            const uint8_t* __restrict__ W, const uint8_t* __restrict__ we, int T,
                                                            int E, int top, int H, int Fp, int S, void* __restrict__ out,
                                                            int64_t ldo, float* __restrict__ part) {
-  constexpr int HP = moe_parts(DT), SLOT = RT * 2048 + 256;
-  constexpr int nD = 5, nX = HP * 8;  // loads of a unit's weights and columns
-  extern __shared__ __attribute__((aligned(16))) char smem[];  // rings [NW][SLOTS][SLOT], sums [NW][T][kRowPitch]
+  constexpr int HP = moe_parts(DT);
+  constexpr int nD = 5, nX = COLS == 4 ? HP * 2 : HP * 8;  // loads of a unit's weights and columns
+  // rings [NW][SLOTS][kSlot], columns [NW][column_bytes], sums [NW][T][kRowPitch]
+  extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ Reached s;
-  float* sums = reinterpret_cast<float*>(smem + NW * SLOTS * SLOT);
+  float* sums = reinterpret_cast<float*>(smem + NW * (SLOTS * kSlot + column_bytes(HP, COLS)));
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int most = min(E, T * top);
@@ -496,7 +555,8 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(const uint16_t* __res
   const int u0 = min((slice * NW + wave) * per, units), u1 = min(u0 + per, units);
   const rsrc_t rx = mx_rsrc(a, (uint32_t)(T * top) * (uint32_t)(HP * Fp) * 2u);
   float* mine = sums + wave * T * kRowPitch;
-  char* own = smem + wave * (SLOTS * SLOT);
+  char* own = smem + wave * (SLOTS * kSlot);
+  char* xs = smem + NW * SLOTS * kSlot + wave * column_bytes(HP, COLS);
   if (u0 < u1) {
     // An expert, its units [from, to) of this wave and the next of them, its tokens from b0.
     struct Place {
@@ -521,21 +581,20 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(const uint16_t* __res
     auto advance = [&](Place& p) {
       if (++p.u < p.to) return;
       p.u = p.from;
-      p.b0 += 16;
+      p.b0 += COLS;
       if (p.b0 < p.cols) return;
       if (++p.slot <= last_slot) enter(p);
       else p.rows = 0u, p.cols = 0;
     };
-    const Lanes lanes(Fp, lane);
+    const Lanes lanes(Fp, lane, 16);
     auto load = [&](const Place& p, int slot) {
-      char* at = own + slot * SLOT;
+      char* at = own + slot * kSlot;
       dma_codes(at, p.w, p.rows, Fp, p.u, lanes);
       dma_codes(at + 2048, p.w + 16 * (Fp >> 1), p.rows > 16 ? p.rows - 16 : 0u, Fp, p.u, lanes);
       dma_exponents(at + RT * 2048, p.e, p.rows, Fp, p.u, lanes);
     };
-    auto columns = [&](Columns<HP>& c, const Place& p) {
-      const int col = p.b0 + (lane & 15);
-      load_columns<HP>(c, rx, col < p.cols ? (p.first + col) * (HP * Fp * 2) : kNone, p.u, Fp, Fp * 2, lane);
+    auto columns = [&](Columns<HP, COLS>& c, const Place& p) {
+      c.fetch(rx, [&](int t) { return p.b0 + t < p.cols ? (p.first + p.b0 + t) * (HP * Fp * 2) : kNone; }, p.u, Fp, Fp * 2, lane);
     };
     f32x4 acc[RT];
     auto begin = [&]() {
@@ -548,7 +607,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(const uint16_t* __res
     load(now, 0);
     next = now;
     advance(next);
-    Columns<HP> c0, c1;
+    Columns<HP, COLS> c0, c1;
     columns(c0, now);
     after = next;
     if constexpr (SLOTS == 3) {
@@ -556,25 +615,26 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(const uint16_t* __res
       advance(after);
     }
     begin();
+    c0.put(xs, lane);
     int slot = 0;
-    auto step = [&](const Columns<HP>& c, Columns<HP>& coming) {
+    auto step = [&](const Columns<HP, COLS>& c, Columns<HP, COLS>& coming) {
       const int spare = slot == 0 ? SLOTS - 1 : slot - 1;
       columns(coming, next);
       load(SLOTS == 3 ? after : next, spare);
       wait_loads<(SLOTS - 1) * nD + nX>();
-      const char* at = own + slot * SLOT;
-      multiply<HP, 128>(at, at + RT * 2048, c, now.u * 256 + 128 < Fp, lane, acc);
+      multiply<HP, COLS>(own + slot * kSlot, c, xs, now.u * 256 + 128 < Fp, lane, acc);
       __builtin_amdgcn_sched_barrier(0);
       slot = slot == SLOTS - 1 ? 0 : slot + 1;
       if (now.u + 1 >= now.to) {
         const int col = now.b0 + (lane & 15);
-        if (col < now.cols) {
+        if ((lane & 15) < COLS && col < now.cols) {
           float* to = mine + s.token[now.first + col] * kRowPitch + (lane >> 4) * 4;
 #pragma unroll
           for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(to + r * 16) += acc[r];
         }
         begin();
       }
+      coming.put(xs, lane);
       now = next;
       if constexpr (SLOTS == 3) {
         next = after;
@@ -613,11 +673,11 @@ __global__ __launch_bounds__(256) void moe_join_kernel(const float* __restrict__
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Workgroups of the second launch for the same rows: as many as a round of them, one a CU, holds.
+// Workgroups of the second launch for the same rows: as many as a round of them, two a CU, holds.
 int down_slices(const MoeArgs& a, const DeviceCaps& caps) {
   const int64_t groups = (a.H + RT * 16 - 1) / (RT * 16);
   const int64_t units = std::min<int64_t>(a.E, a.T * a.top) * ((mx_pitch(a.F) + 255) / 256);
-  const int64_t s = std::min<int64_t>(caps.cus / groups, (units + NW - 1) / NW);
+  const int64_t s = std::min<int64_t>(2 * caps.cus / groups, (units + NW - 1) / NW);
   return (int)std::max<int64_t>(1, std::min<int64_t>(s, 16));
 }
 
@@ -639,40 +699,57 @@ hipError_t allow_lds(K k, int bytes) {
   return hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int DT>
+// Tokens of an expert that its weights are widened for at a time: four where experts have few (an
+// expert with more reads its weights again), else sixteen.
+bool few_each(const MoeArgs& a) { return a.T <= 4 || a.T * a.top <= 3 * a.E; }
+
+template <int DT, int COLS>
 hipError_t up(const MoeArgs& a, const DeviceCaps& caps, char* ws, const Space& sp, hipStream_t st) {
   const int64_t Fp = mx_pitch(a.F);
   const int64_t items = std::min<int64_t>(a.E, a.T * a.top) * (Fp / 16);
-  const int64_t wgs = std::max<int64_t>(1, std::min<int64_t>(items, caps.cus));
-  constexpr int lds = NW * kSlots * (RT * 2048 + 512);
-  const hipError_t e = allow_lds(moe_up_kernel<DT>, lds);
+  constexpr int lds = NW * (kSlots * kSlot + column_bytes(mx_parts(DT), COLS));
+  constexpr int fixed = sizeof(Routing) + 2 * NW * RT * 16 * (COLS + 1) * 4;
+  const int64_t per_cu = lds + fixed <= 80 * 1024 ? 2 : 1;
+  const int64_t wgs = std::max<int64_t>(1, std::min<int64_t>(items, per_cu * caps.cus));
+  const hipError_t e = allow_lds(moe_up_kernel<DT, COLS>, lds);
   if (e != hipSuccess) return e;
-  moe_up_kernel<DT><<<(unsigned)wgs, NW * 64, lds, st>>>(
+  moe_up_kernel<DT, COLS><<<(unsigned)wgs, NW * 64, lds, st>>>(
       a.x, (int)a.ldx, (int)a.Hx, a.logits, a.ldt, a.ldl, a.W1, a.w1_scales, (int)a.T, (int)a.E, a.top, a.renorm,
       (int)mx_pitch(a.H), (int)a.F, (int)Fp, reinterpret_cast<uint16_t*>(ws + sp.rows), reinterpret_cast<Reached*>(ws));
   return hipGetLastError();
 }
 
-template <int DT, int SLOTS>
+constexpr int down_lds(int dt, int cols, int slots, int64_t T) {
+  return NW * (slots * kSlot + column_bytes(moe_parts(dt), cols) + (int)T * kRowPitch * 4);
+}
+
+template <int DT, int COLS, int SLOTS>
 hipError_t down(const MoeArgs& a, char* ws, const Space& sp, int S, hipStream_t st) {
-  const int lds = NW * (SLOTS * (RT * 2048 + 256) + (int)a.T * kRowPitch * 4);
-  const hipError_t e = allow_lds(moe_down_kernel<DT, SLOTS>, lds);
+  const int lds = down_lds(DT, COLS, SLOTS, a.T);
+  const hipError_t e = allow_lds(moe_down_kernel<DT, COLS, SLOTS>, lds);
   if (e != hipSuccess) return e;
   const int groups = (int)((a.H + RT * 16 - 1) / (RT * 16));
-  moe_down_kernel<DT, SLOTS><<<(unsigned)(groups * S), NW * 64, lds, st>>>(
+  moe_down_kernel<DT, COLS, SLOTS><<<(unsigned)(groups * S), NW * 64, lds, st>>>(
       reinterpret_cast<const uint16_t*>(ws + sp.rows), reinterpret_cast<const Reached*>(ws), a.W2, a.w2_scales, (int)a.T,
       (int)a.E, a.top, (int)a.H, (int)mx_pitch(a.F), S, a.out, a.ldo, S > 1 ? reinterpret_cast<float*>(ws + sp.part) : nullptr);
   return hipGetLastError();
 }
 
+// Rings of three units where two workgroups of them share a CU, else of two (the sums of many tokens
+// take the place).
+template <int DT, int COLS>
+hipError_t both(const MoeArgs& a, const DeviceCaps& caps, char* ws, const Space& sp, int S, hipStream_t st) {
+  const hipError_t e = up<DT, COLS>(a, caps, ws, sp, st);
+  if (e != hipSuccess) return e;
+  return down_lds(DT, COLS, 3, a.T) + (int)sizeof(Reached) <= 80 * 1024 ? down<DT, COLS, 3>(a, ws, sp, S, st)
+                                                                         : down<DT, COLS, 2>(a, ws, sp, S, st);
+}
+
 template <int DT>
 hipError_t run(const MoeArgs& a, const DeviceCaps& caps, char* ws, hipStream_t st) {
   const Space sp = space_of(a, caps);
-  hipError_t e = up<DT>(a, caps, ws, sp, st);
-  if (e != hipSuccess) return e;
   const int S = down_slices(a, caps);
-  // the sums of more tokens leave LDS for rings of two units
-  e = a.T <= 40 ? down<DT, 3>(a, ws, sp, S, st) : down<DT, 2>(a, ws, sp, S, st);
+  const hipError_t e = few_each(a) ? both<DT, 4>(a, caps, ws, sp, S, st) : both<DT, 16>(a, caps, ws, sp, S, st);
   if (e != hipSuccess || S == 1) return e;
   moe_join_kernel<DT><<<dim3((unsigned)((a.H + 255) / 256), (unsigned)a.T), 256, 0, st>>>(
       reinterpret_cast<const float*>(ws + sp.part), reinterpret_cast<const Reached*>(ws), (int)a.T, (int)a.H, S, a.out, a.ldo);

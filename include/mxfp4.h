@@ -91,7 +91,7 @@ int mx4_mm_t(const void* dY, int dtype, int64_t ld, int64_t M, const uint8_t* W,
  * A logit of -infinity is an expert that is masked: it is never run, also where fewer than `top` are
  * left.  A token whose logits are all -infinity gets 0.  A token with a NaN or +infinity among its
  * logits gets NaN.
- * 1 <= top <= min(E, 16), E <= 512, H and F < 2^18.  T == 0 is a no-op; more than 64 tokens run 64 at a time,
+ * 1 <= top <= min(E, 16), E <= 512, H and F < 2^17.  T == 0 is a no-op; more than 64 tokens run 64 at a time,
  * each run reading its weights again.  The workspace that mx4_moe_workspace_bytes reports is
  * required; it belongs to the call until its launches have ended. */
 int mx4_moe_workspace_bytes(int64_t T, int64_t E, int top, int64_t H, int64_t F, int dtype, size_t* bytes);
