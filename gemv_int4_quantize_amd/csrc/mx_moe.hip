@@ -49,20 +49,20 @@ struct Choice {
 
 // Maximum, minimum and sum over a row of sixteen lanes, in every lane of it.
 template <typename F>
-__device__ __forceinline__ uint32_t row_reduce(uint32_t v, F f) {
-  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));  // row mirror
-  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));  // half-row mirror
-  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));   // lane ^ 2
-  return f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));  // lane ^ 1
+__device__ __forceinline__ uint32_t row_reduce(uint32_t v, int none, F f) {  // f(v, none) = v
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(none, (int)v, 0x140, 0xF, 0xF, false));  // row mirror
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(none, (int)v, 0x141, 0xF, 0xF, false));  // half-row mirror
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(none, (int)v, 0x4E, 0xF, 0xF, false));   // lane ^ 2
+  return f(v, (uint32_t)__builtin_amdgcn_update_dpp(none, (int)v, 0xB1, 0xF, 0xF, false));  // lane ^ 1
 }
 __device__ __forceinline__ uint32_t row_umax(uint32_t v) {
-  return row_reduce(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+  return row_reduce(v, 0, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
 __device__ __forceinline__ uint32_t row_umin(uint32_t v) {
-  return row_reduce(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+  return row_reduce(v, -1, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 }
 __device__ __forceinline__ float row_sum(float v) {
-  return __uint_as_float(row_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+  return __uint_as_float(row_reduce(__float_as_uint(v), 0, [](uint32_t a, uint32_t b) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
   }));
 }
@@ -79,14 +79,29 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// The largest of C keys.
+template <int C>
+__device__ __forceinline__ uint32_t largest(const uint32_t (&key)[C]) {
+  uint32_t m = key[0];
+#pragma unroll
+  for (int c = 1; c < C; ++c) m = umax(m, key[c]);
+  return m;
+}
+
 // The choice for four tokens at a time, a row of sixteen lanes each (from token t0; none past T): lane l
 // of a row holds experts l C .. l C + C - 1, and the largest is taken out `top` times, the one of the
 // lowest number among equals; lane j keeps choice j.
+// A round is short where a key says which expert it is: its last nine bits give way to the number, the
+// lower the larger.  16-bit logits lose nothing by it.  Of fp32 logits it may not tell the last choice
+// from the next one, and where these agree in the bits left the choice is made again with whole keys.
+// (Whole keys throughout: 19.6 us instead of 18.9 for a call of one token and 8 of 128 experts.)
 template <int C>
 __device__ __forceinline__ void choose(Routing& s, Choice& c0, const void* __restrict__ logits, int ldt, int64_t ldl, int t0,
                                        int T, int E, int top, bool renorm) {
+  constexpr uint32_t kNumber = kMaxExperts - 1;
+  static_assert((kMaxExperts & kNumber) == 0, "bits of a number");
   const int l16 = threadIdx.x & 15, t = t0 + ((threadIdx.x & 63) >> 4), first = l16 * C;
-  const uint32_t masked = order_key(-__builtin_inff());
+  const uint32_t masked = order_key(-__builtin_inff());  // (its last nine bits are ones)
   uint32_t key[C];
   float v[C];
 #pragma unroll
@@ -98,26 +113,39 @@ __device__ __forceinline__ void choose(Routing& s, Choice& c0, const void* __res
     key[c] = order_key(v[c] + 0.0f);  // -0 and +0 are equal
   }
   odd = row_umax(odd);
-  float mx = 0.0f, z = -__builtin_inff();
+  const uint32_t most = row_umax(largest<C>(key));
+  const float mx = most <= masked ? 0.0f : __uint_as_float(most & 0x80000000u ? most & 0x7FFFFFFFu : ~most);
+#pragma unroll
+  for (int c = 0; c < C; ++c) key[c] = (key[c] & ~kNumber) | (kNumber - (uint32_t)(first + c));
   int chosen = -1;
+  uint32_t best = 0;
   for (int j = 0; j < top; ++j) {
-    uint32_t own = key[0];
+    best = row_umax(largest<C>(key));
 #pragma unroll
-    for (int c = 1; c < C; ++c) own = umax(own, key[c]);
-    const uint32_t best = row_umax(own);
-    uint32_t at = 0xFFFFu;
+    for (int c = 0; c < C; ++c) key[c] = key[c] == best ? 0u : key[c];
+    if (l16 == j && best > masked) chosen = (int)(kNumber - (best & kNumber));
+  }
+  bool unclear = false;
+  if (ldt == W4_DT_F32) {
+    const uint32_t next = row_umax(largest<C>(key));
+    unclear = next > masked && (next & ~kNumber) == (best & ~kNumber);
+  }
+  if (__ballot(unclear) != 0) {
 #pragma unroll
-    for (int c = C - 1; c >= 0; --c) at = key[c] == best ? (uint32_t)(first + c) : at;
-    at = row_umin(at);
+    for (int c = 0; c < C; ++c) key[c] = order_key(v[c] + 0.0f);
+    for (int j = 0; j < top; ++j) {
+      best = row_umax(largest<C>(key));
+      uint32_t at = 0xFFFFu;
 #pragma unroll
-    for (int c = 0; c < C; ++c) key[c] = at == (uint32_t)(first + c) ? 0u : key[c];
-    const float value = __uint_as_float(best & 0x80000000u ? best & 0x7FFFFFFFu : ~best);
-    if (j == 0 && best > masked) mx = value;
-    if (l16 == j && best > masked) {
-      chosen = (int)at;
-      z = value;
+      for (int c = C - 1; c >= 0; --c) at = key[c] == best ? (uint32_t)(first + c) : at;
+      at = row_umin(at);
+#pragma unroll
+      for (int c = 0; c < C; ++c) key[c] = at == (uint32_t)(first + c) ? 0u : key[c];
+      if (l16 == j) chosen = best > masked ? (int)at : -1;
     }
   }
+  if (t >= T) chosen = -1;
+  const float z = chosen >= 0 ? logit(logits, ldt, t * ldl + chosen) : -__builtin_inff();
   const float weight = expf(z - mx);  // 0 where there is none
   float sum = weight;
   if (!renorm) {
