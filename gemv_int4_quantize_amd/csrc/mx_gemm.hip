@@ -250,85 +250,116 @@ __device__ __forceinline__ void ring_tile(char* smem, const uint8_t* __restrict_
   }
 }
 
-// Tiles of one kind (tm x tn), all of them once for each slice of kt_per_slice stages.  Workgroups go
-// to the eight XCDs (each with an L2 of its own) in turn; each XCD gets a contiguous part of the
-// work, in the order: slices, groups of eight tile rows, tile columns, rows of the group.
-template <int WM, int WN, int FM, int FN, int NB>
+// Work of a launch: the first `full` column tiles in (WM FB 32)-row tiles, the columns left in
+// (WM FM 32)-row tiles; all of that once for each slice of the contraction.
+struct Grid {
+  int full, tn;   // column tiles of the first kind, and in all
+  int high, low;  // row tiles of the two kinds
+  int per;        // stages of a slice
+};
+
+// Workgroups go to the eight XCDs (each with an L2 of its own) in turn; of each kind of tile an XCD gets
+// a contiguous part, in the order: groups of eight tile rows, tile columns, rows of the group, so that
+// its 32 tiles at a time are about 8 x 4 (against plain order, at 8192^3 301 us, 320 without; M = 512,
+// (8192, 2048) 12.4, 14.1).
+template <int WM, int WN, int FB, int FM, int FN, int NB>
 __global__ __launch_bounds__(WM * WN * 64) void mx_ring_kernel(const uint8_t* __restrict__ A, const uint8_t* __restrict__ ae,
                                                                const uint8_t* __restrict__ W, const uint8_t* __restrict__ we,
-                                                               const Epi ep, int M, int N, int pitch, int tm, int tn,
-                                                               int kt_per_slice, float* __restrict__ part) {
+                                                               const Epi ep, int M, int N, int pitch, const Grid g,
+                                                               float* __restrict__ part) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  const int per_xcd = gridDim.x >> 3, left = gridDim.x & 7, xcd = blockIdx.x & 7;
-  const int work = xcd * per_xcd + min(xcd, left) + (blockIdx.x >> 3);
-  const int slice = work / (tm * tn), tile = work - slice * tm * tn;
-  const int grp = tile / (8 * tn), in_grp = tile - grp * 8 * tn, rows_grp = min(8, tm - grp * 8);
-  const int ti = grp * 8 + in_grp % rows_grp, tj = in_grp / rows_grp;
-  ring_tile<WM, WN, FM, FN, NB>(smem, A, ae, W, we, ep, M, N, pitch, ti * WM * FM * 32, tj * WN * FN * 32, slice,
-                                kt_per_slice, part);
+  const int n_high = FB > 0 ? g.full * g.high : 0, n_all = n_high + (g.tn - g.full) * g.low;
+  const int slice = blockIdx.x / (unsigned)n_all;
+  int at = blockIdx.x - (unsigned)slice * n_all;
+  const bool high = at < n_high;
+  if (!high) at -= n_high;
+  const int kind = high ? n_high : n_all - n_high, rows = high ? g.high : g.low, cols = high ? g.full : g.tn - g.full;
+  const int per_xcd = kind >> 3, left = kind & 7, xcd = at & 7;
+  const int tile = xcd * per_xcd + min(xcd, left) + (at >> 3);
+  const int grp = tile / (8 * cols), in_grp = tile - grp * 8 * cols, rows_grp = min(8, rows - grp * 8);
+  const int tr = grp * 8 + in_grp % rows_grp, tc = in_grp / rows_grp + (high ? 0 : g.full);
+  if constexpr (FB > 0)
+    if (high) {
+      ring_tile<WM, WN, FB, FN, NB>(smem, A, ae, W, we, ep, M, N, pitch, tr * WM * FB * 32, tc * WN * FN * 32, slice, g.per, part);
+      return;
+    }
+  ring_tile<WM, WN, FM, FN, NB>(smem, A, ae, W, we, ep, M, N, pitch, tr * WM * FM * 32, tc * WN * FN * 32, slice, g.per, part);
 }
 
 struct MxPlan {
-  int tile = 0, splits = 1;
+  int tile = 0, full = 0, splits = 1;
 };
 
-template <int WM, int WN, int FM, int FN, int NB>
+template <int WM, int WN, int FB, int FM, int FN, int NB>
 hipError_t run_ring(const MxArgs& a, const MxPlan& p, float* part, hipStream_t st) {
-  constexpr int BM = WM * FM * 32, BN = WN * FN * 32, T = WM * WN * 64;
-  constexpr int lds = NB * stage_bytes(T, BM + BN);
+  constexpr int BM = WM * FM * 32, BN = WN * FN * 32, T = WM * WN * 64, BH = FB > 0 ? WM * FB * 32 : 1;
+  const int lds = NB * stage_bytes(T, (p.full > 0 ? BH : BM) + BN);
   const int M = (int)a.M, N = (int)a.N, pitch = (int)(a.P / 2);
-  const int tm = (M + BM - 1) / BM, tn = (N + BN - 1) / BN;
   const int kt = (pitch + BK - 1) / BK;
-  const int per = (kt + p.splits - 1) / p.splits;
-  const int splits = (kt + per - 1) / per;  // every slice gets at least one stage
-  auto k = mx_ring_kernel<WM, WN, FM, FN, NB>;
+  Grid g = {};
+  g.tn = (N + BN - 1) / BN;
+  g.full = p.full;
+  g.high = FB > 0 ? (M + BH - 1) / BH : 0;
+  g.low = (M + BM - 1) / BM;
+  g.per = (kt + p.splits - 1) / p.splits;
+  const int splits = (kt + g.per - 1) / g.per;  // every slice gets at least one stage
+  auto k = mx_ring_kernel<WM, WN, FB, FM, FN, NB>;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  k<<<(unsigned)((int64_t)tm * tn * splits), T, lds, st>>>(a.A, a.a_scales, a.W, a.w_scales, a.ep, M, N, pitch, tm, tn, per,
-                                                           splits > 1 ? part : nullptr);
+  const int64_t wgs = ((int64_t)g.full * g.high + (int64_t)(g.tn - g.full) * g.low) * splits;
+  k<<<(unsigned)wgs, T, lds, st>>>(a.A, a.a_scales, a.W, a.w_scales, a.ep, M, N, pitch, g, splits > 1 ? part : nullptr);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   return launch_splitk_reduce(part, splits, a.M, 0, a.N, a.ep, st);
 }
 
-// Tiles, and what one stage of them takes, in us on MI355X: lat, the least time of a stage; mfma, a
-// workgroup's share of the CU's matrix cores; and t0, a launch's start, first loads and stores.
+// Tiles of bm (0: none) and lower rows and bn columns, and what one stage of them takes, in us on MI355X
+// (fitted to 20 sizes from (M, N, K) = (32, 2048, 2048) to (4096, 11008, 4096), in a captured graph, where
+// the plan is within 1% of the best of all tiles and splits):
+// high, of a bm-row tile; lat, the least time of a stage of a lower one; mfma, a workgroup's share of
+// the CU's matrix cores; and t0, a launch's start, first loads and stores.
 struct Tile {
   const char* name;
-  int bm, bn, slots;  // slots: workgroups that a CU's LDS holds
-  double t0, lat, mfma;
+  int bm, low, bn, slots;  // slots: workgroups that a CU's LDS holds
+  double t0, high, lat, mfma;
 };
 constexpr Tile kTiles[] = {
-    {"mx4_256x256", 256, 256, 1, 8.0, 1.30, 1.50},
-    {"mx4_256x128", 256, 128, 1, 6.5, 0.74, 0.90},
-    {"mx4_128x128", 128, 128, 1, 5.5, 0.45, 0.50},
-    {"mx4_128x64", 128, 64, 2, 4.7, 0.37, 0.30},
-    {"mx4_64x64", 64, 64, 2, 4.3, 0.19, 0.20},
+    {"mx4_256x256", 256, 192, 256, 1, 4.9, 2.20, 1.57, 1.72},
+    {"mx4_256x256", 256, 128, 256, 1, 4.9, 2.20, 1.23, 1.47},
+    {"mx4_256x128", 0, 256, 128, 1, 6.75, 0.00, 0.87, 1.31},
+    {"mx4_128x128", 0, 128, 128, 1, 6.25, 0.00, 0.62, 0.81},
+    {"mx4_128x64", 0, 128, 64, 2, 5.3, 0.00, 0.37, 0.45},
+    {"mx4_64x64", 0, 64, 64, 2, 4.7, 0.00, 0.24, 0.29},
 };
 
-// The plan with the least estimated time: rounds of workgroups, each the contraction's stages at the
-// longer of the two figures; a split adds a launch and the write and read of its fp32 planes.
+// The plan with the least estimated time: rounds of workgroups, each the contraction's stages; a split
+// adds a launch and the write and read of its fp32 planes.  256 x 256 tiles take all of the columns,
+// those that make whole rounds, or none, and the lower tiles the others in a shorter last round.
 MxPlan pick(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps, bool allow_split) {
   const int64_t cus = caps.cus > 0 ? caps.cus : 256, kt = (mx_pitch(K) / 2 + BK - 1) / BK;
   MxPlan best;
   double best_t = 1e30;
   for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
     const Tile& c = kTiles[i];
-    const int64_t rows = (M + c.bm - 1) / c.bm, tn = (N + c.bn - 1) / c.bn;
+    const int64_t low = (M + c.low - 1) / c.low, high = c.bm > 0 ? (M + c.bm - 1) / c.bm : 0, tn = (N + c.bn - 1) / c.bn;
     for (int sp = 1; sp <= (allow_split ? 8 : 1); sp *= 2) {
       if (sp > 1 && kt / sp < 4) break;
       const int64_t steps = (kt + sp - 1) / sp;
-      const int64_t wgs = rows * tn * sp;
-      const int64_t rounds = (wgs + cus * c.slots - 1) / (cus * c.slots);
-      // workgroups of the fullest CU
-      const int64_t resident = std::min(wgs, cus * c.slots);
-      const double per_cu = resident <= cus ? (double)resident / cus : (double)((resident + cus - 1) / cus);
-      const double t = c.t0 + rounds * steps * std::max(c.lat, c.mfma * per_cu) + (sp > 1 ? 4.5 + sp * M * N * 8.0 / 8.0 * 1e-6 : 0.0);
-      if (t < best_t) {
-        best_t = t;
-        best = MxPlan{i, sp};
+      for (const int64_t full : {(int64_t)0, high > 0 ? high * tn / cus * cus / high : 0, high > 0 ? tn : 0}) {
+        const int64_t a = full * high * sp, b = (tn - full) * low * sp;
+        const int64_t rounds = (b + cus * c.slots - 1) / (cus * c.slots);
+        // workgroups of the fullest CU; a round that leaves CUs idle runs at a higher clock
+        const int64_t resident = std::min(b, cus * c.slots);
+        const double per_cu = resident <= cus ? (double)resident / cus : (double)((resident + cus - 1) / cus);
+        const double t = c.t0 + (double)((a + cus - 1) / cus * steps) * c.high +
+                         (double)(rounds * steps) * std::max(c.lat, c.mfma * per_cu) +
+                         (sp > 1 ? 2.1 + sp * M * N * 8.0 / 8.0 * 1e-6 : 0.0);
+        if (t < best_t) {
+          best_t = t;
+          best = MxPlan{i, (int)full, sp};
+        }
       }
     }
   }
@@ -340,29 +371,32 @@ size_t plan_bytes(int64_t M, int64_t N, const MxPlan& p) { return p.splits > 1 ?
 }  // namespace
 
 size_t mx_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps) {
-  return mx_decode_supported(M) ? 0 : plan_bytes(M, N, pick(M, N, K, caps, true));
+  return mx_decode_supported(M, K) ? 0 : plan_bytes(M, N, pick(M, N, K, caps, true));
 }
 
 const char* mx_mm_name(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps) {
   static thread_local char buf[48];
-  if (mx_decode_supported(M)) return "mx4_decode";
+  if (mx_decode_supported(M, K)) return "mx4_decode";
   const MxPlan p = pick(M, N, K, caps, true);
-  if (p.splits == 1) return kTiles[p.tile].name;
-  snprintf(buf, sizeof(buf), "%s_splitk%d", kTiles[p.tile].name, p.splits);
+  const Tile& c = kTiles[p.tile];
+  int at = snprintf(buf, sizeof(buf), "%s", c.name);
+  if (c.bm > 0 && p.full < (N + c.bn - 1) / c.bn) at += snprintf(buf + at, sizeof(buf) - at, "+%dx256", c.low);
+  if (p.splits > 1) snprintf(buf + at, sizeof(buf) - at, "_splitk%d", p.splits);
   return buf;
 }
 
 hipError_t launch_mx_mm(const MxArgs& a, const DeviceCaps& caps, void* ws, size_t ws_bytes, hipStream_t st) {
-  if (mx_decode_supported(a.M)) return launch_mx_decode(a, caps, st);
+  if (mx_decode_supported(a.M, a.K)) return launch_mx_decode(a, caps, st);
   MxPlan p = pick(a.M, a.N, a.K, caps, true);
   if (plan_bytes(a.M, a.N, p) > ws_bytes) p = pick(a.M, a.N, a.K, caps, false);
   float* part = static_cast<float*>(ws);
   switch (p.tile) {
-    case 0: return run_ring<2, 4, 4, 2, 2>(a, p, part, st);
-    case 1: return run_ring<4, 2, 2, 2, 3>(a, p, part, st);
-    case 2: return run_ring<2, 2, 2, 2, 4>(a, p, part, st);
-    case 3: return run_ring<2, 2, 2, 1, 3>(a, p, part, st);
-    default: return run_ring<2, 2, 1, 1, 4>(a, p, part, st);
+    case 0: return run_ring<2, 4, 4, 3, 2, 2>(a, p, part, st);
+    case 1: return run_ring<2, 4, 4, 2, 2, 2>(a, p, part, st);
+    case 2: return run_ring<4, 2, 0, 2, 2, 3>(a, p, part, st);
+    case 3: return run_ring<2, 2, 0, 2, 2, 4>(a, p, part, st);
+    case 4: return run_ring<2, 2, 0, 2, 1, 3>(a, p, part, st);
+    default: return run_ring<2, 2, 0, 1, 1, 4>(a, p, part, st);
   }
 }
 
