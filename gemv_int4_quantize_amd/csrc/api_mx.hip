@@ -146,7 +146,7 @@ int mx4_workspace_bytes(int64_t M, int64_t N, int64_t K, int x_dtype, size_t* by
   if (!bytes) return fail(W4_ERR_INVALID, "bytes is NULL");
   if (x_dtype >= 0 && !is_dtype(x_dtype)) return fail(W4_ERR_INVALID, "x_dtype = %d is unknown", x_dtype);
   if (M == 0) *bytes = 0;
-  else if (x_dtype >= 0 && w4::mx_fused(M, K)) *bytes = 0;
+  else if (x_dtype >= 0 && w4::mx_decode_supported(M, K)) *bytes = 0;
   else if (x_dtype < 0) *bytes = w4::mx_mm_workspace_bytes(M, N, K, device_caps());
   else *bytes = linear_ws(M, N, K).total;
   return ok();
@@ -192,7 +192,7 @@ int mx4_linear(const void* X, int x_dtype, int64_t ldx, int64_t M, const uint8_t
   if (s == W4_OK) s = check_ws(ws);
   if (s != W4_OK) return s;
   if (M == 1) ldx = K;
-  if (w4::mx_fused(M, K)) {
+  if (w4::mx_decode_supported(M, K)) {
     w4::MxArgs a = {};
     a.X = X;
     a.x_dt = x_dtype;
@@ -222,7 +222,7 @@ int mx4_linear(const void* X, int x_dtype, int64_t ldx, int64_t M, const uint8_t
 
 const char* mx4_kernel(int64_t M, int64_t N, int64_t K, int x_dtype) {
   if (check_sizes(M, N, K) != W4_OK || M == 0 || (x_dtype >= 0 && !is_dtype(x_dtype))) return nullptr;
-  if (x_dtype >= 0 && w4::mx_fused(M, K)) return "mx4_decode_fused";
+  if (x_dtype >= 0 && w4::mx_decode_supported(M, K)) return "mx4_decode_fused";
   return w4::mx_mm_name(M, N, K, device_caps());
 }
 

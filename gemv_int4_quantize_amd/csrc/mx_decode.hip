@@ -1,4 +1,4 @@
-// Product of microscaled 4-bit rows for one to four tokens (decode), for gfx950.  The weight is read
+// Product of microscaled 4-bit rows for one to sixteen tokens (decode), for gfx950.  The weight is read
 // once, and its bytes set the time; float tokens are quantized by the same launch.
 //
 // A workgroup stays for several groups of 16 RT channels, its tokens' codes in LDS; its waves share out
@@ -21,8 +21,12 @@ namespace w4 {
 namespace {
 
 constexpr int kNonTemporal = 2;       // cache-policy operand of a load
-constexpr int kMaxM = 4;              // tokens
-constexpr int kTokenLds = 64 * 1024;  // bytes of codes and exponents that a workgroup may hold
+constexpr int kMaxM = 16;             // tokens
+// Columns of all tokens.  Every workgroup quantizes them, and past these the tiles behind a launch that
+// quantizes once are as fast: (N, K) = (12288, 4096), 8 tokens 10.1 us here, 11.9 on the tiles, 12
+// tokens 13.1 and 12.1; (4096, 11008), 4 tokens 8.4, 13.0, 8 tokens 14.8, 13.7; (16384, 16384), 2 tokens
+// 32.4, 36.3, 4 tokens 39.6, 36.4.
+constexpr int64_t kMaxColumns = 45056;
 
 // The tokens in LDS: exponents [M][P / 32], then codes [M][P / 2 + 16] (the pad keeps the tokens' rows in
 // distinct banks).
@@ -33,10 +37,10 @@ constexpr int64_t token_lds(int64_t M, int64_t P) { return codes_at(M, P) + M * 
 // on the source address, so that reads of 16 rows hit distinct banks; then 8 exponents a row, of 32 rows.
 constexpr int slot_bytes(int RT) { return RT * 2048 + 256; }
 
-// XDT: -1: tokens' codes from memory; else the dtype of float tokens.  Loads return in order, so the
-// tokens are asked for before the weights: C chunks of eight of each token per thread (what is left of
-// longer tokens is read behind them).
-template <int NW, int RT, int SLOTS, int XDT, int C>
+// MT: tokens that there is room for.  XDT: -1: their codes from memory; else the dtype of float tokens.
+// Loads return in order, so the tokens are asked for before the weights: C chunks of eight per thread
+// (what is left of more or longer tokens is read behind them).
+template <int NW, int RT, int SLOTS, int MT, int XDT, int C>
 __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(const uint8_t* __restrict__ W, const uint8_t* __restrict__ we,
                                                             const uint8_t* __restrict__ A, const uint8_t* __restrict__ ae,
                                                             const void* __restrict__ X, int64_t ldx, int M, int N, int K,
@@ -44,7 +48,7 @@ __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(const uint8_t* __res
   constexpr int T = NW * 64, nD = 2 * RT + 1;  // loads of a unit
   constexpr int SLOT = slot_bytes(RT);
   extern __shared__ __attribute__((aligned(16))) char smem[];  // rings [NW][SLOTS][SLOT], then the tokens
-  __shared__ float sums[2][NW][RT * 16][kMaxM + 1];            // of groups in turn
+  __shared__ float sums[2][NW][RT * 16][MT + 1];               // of groups in turn
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int units = (P + 255) >> 8, groups = (N + RT * 16 - 1) / (RT * 16);
@@ -105,29 +109,52 @@ __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(const uint8_t* __res
       if (c * 8 + 8 <= K) return load_raw8<XDT>(p);
       return c * 8 < K ? load_raw8_part<XDT>(p, K - c * 8, 0u) : Raw8<XDT>{};
     };
-    auto put = [&](int m, int c, const Raw8<XDT>& r) {
+    auto put = [&](int m, int c, bool in, const Raw8<XDT>& r) {
       uint32_t e;
       const uint32_t code = mx_chunk<XDT>(r, &e);
-      if (c < ch) {
+      if (in) {
         *reinterpret_cast<uint32_t*>(tokens + at_codes + m * (row + 16) + c * 4) = code;
         if ((c & 3) == 0) tokens[m * erow + (c >> 2)] = (char)e;
       }
     };
-    Raw8<XDT> held[kMaxM][C];
+    if constexpr (MT == 4) {  // the same chunks of each token
+      constexpr int CT = C / 4;
+      Raw8<XDT> held[MT][CT];
 #pragma unroll
-    for (int m = 0; m < kMaxM; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        held[m][c] = Raw8<XDT>{};
-        if (m < M && tid + c * T < ch) held[m][c] = chunk(m, tid + c * T);
+        for (int c = 0; c < CT; ++c) {
+          held[m][c] = Raw8<XDT>{};
+          if (m < M && tid + c * T < ch) held[m][c] = chunk(m, tid + c * T);
+        }
+      first_loads();
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if (m >= M) break;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) put(m, tid + c * T, tid + c * T < ch, held[m][c]);
+        for (int c = tid + CT * T; c - tid < ch; c += T) put(m, c, c < ch, c < ch ? chunk(m, c) : Raw8<XDT>{});
       }
-    first_loads();
+    } else {  // the chunks of all tokens in a row
+      const uint32_t all = (uint32_t)(M * ch);
+      Raw8<XDT> held[C];
+      auto fetch = [&](uint32_t i0) {
 #pragma unroll
-    for (int m = 0; m < kMaxM; ++m) {
-      if (m >= M) break;
+        for (int c = 0; c < C; ++c) {
+          const uint32_t i = i0 + tid + c * T;
+          held[c] = i < all ? chunk((int)(i / ch), (int)(i % ch)) : Raw8<XDT>{};
+        }
+      };
+      fetch(0);
+      first_loads();
+      for (uint32_t i0 = 0; i0 < all; i0 += C * T) {
+        if (i0 > 0) fetch(i0);
 #pragma unroll
-      for (int c = 0; c < C; ++c) put(m, tid + c * T, held[m][c]);
-      for (int c = tid + C * T; c - tid < ch; c += T) put(m, c, c < ch ? chunk(m, c) : Raw8<XDT>{});
+        for (int c = 0; c < C; ++c) {
+          const uint32_t i = i0 + tid + c * T;
+          put((int)(i / ch), (int)(i % ch), i < all, held[c]);
+        }
+      }
     }
   } else {
     for (int m = 0; m < M; ++m) {
@@ -189,7 +216,7 @@ __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(const uint8_t* __res
     if (now.u + NW >= units) {
       // the group's sums, by waves in turn.  One barrier a group: the next one's sums have a place of their
       // own, and when they are written every wave has passed this one's.
-      float(*sum)[RT * 16][kMaxM + 1] = sums[turn & 1];
+      float(*sum)[RT * 16][MT + 1] = sums[turn & 1];
       if (r16 < M) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -197,9 +224,9 @@ __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(const uint8_t* __res
           for (int i = 0; i < 4; ++i) sum[wave][r * 16 + q4 * 4 + i][r16] = acc[r][i];
       }
       barrier();
-      const int i = ((wave + turn) & (NW - 1)) * 64 + lane, m = i / (RT * 16), c = i % (RT * 16);
-      const int n = now.group * (RT * 16) + c;
-      if (m < M && n < N) {
+      for (int i = ((wave + turn) & (NW - 1)) * 64 + lane; i < M * (RT * 16); i += T) {
+        const int m = i / (RT * 16), c = i % (RT * 16), n = now.group * (RT * 16) + c;
+        if (n >= N) continue;
         float s = 0.0f;
 #pragma unroll
         for (int v = 0; v < NW; ++v) s += sum[v][c][m];
@@ -214,12 +241,12 @@ __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(const uint8_t* __res
   __builtin_amdgcn_s_waitcnt(0x0070);  // no direct LDS load may land after the workgroup's LDS is handed on
 }
 
-template <int NW, int RT, int SLOTS, int XDT, int C>
+template <int NW, int RT, int SLOTS, int MT, int XDT, int C>
 hipError_t run(const MxArgs& a, const DeviceCaps& caps, hipStream_t st) {
-  static_assert(NW * 64 >= RT * 16 * kMaxM && (NW & (NW - 1)) == 0, "a thread for each of a group's results");
+  static_assert((NW & (NW - 1)) == 0, "waves in turn");
   const int64_t lds = NW * SLOTS * slot_bytes(RT) + token_lds(a.M, a.P);
-  constexpr int64_t fixed = 2 * NW * RT * 16 * (kMaxM + 1) * 4;
-  auto k = mx_decode_kernel<NW, RT, SLOTS, XDT, C>;
+  constexpr int64_t fixed = 2 * NW * RT * 16 * (MT + 1) * 4;
+  auto k = mx_decode_kernel<NW, RT, SLOTS, MT, XDT, C>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
   const int64_t groups = (a.N + RT * 16 - 1) / (RT * 16), per_cu = std::max<int64_t>(1, 160 * 1024 / (lds + fixed));
@@ -229,17 +256,19 @@ hipError_t run(const MxArgs& a, const DeviceCaps& caps, hipStream_t st) {
 }
 
 // Groups of 32 channels and four waves where a CU gets two of them, else smaller groups and more waves.
+template <int MT, int XDT>
+hipError_t run_m(const MxArgs& a, const DeviceCaps& caps, hipStream_t st) {
+  if (a.N < 2 * 32 * (int64_t)caps.cus) return a.P <= 4096 ? run<8, 1, 2, MT, XDT, 4>(a, caps, st) : run<8, 1, 3, MT, XDT, 12>(a, caps, st);
+  return a.P <= 4096 ? run<4, 2, 3, MT, XDT, 8>(a, caps, st) : run<4, 2, 3, MT, XDT, 16>(a, caps, st);
+}
 template <int XDT>
 hipError_t run_x(const MxArgs& a, const DeviceCaps& caps, hipStream_t st) {
-  if (a.N < 2 * 32 * (int64_t)caps.cus) return a.P <= 4096 ? run<8, 1, 2, XDT, 1>(a, caps, st) : run<8, 1, 3, XDT, 3>(a, caps, st);
-  return a.P <= 4096 ? run<4, 2, 3, XDT, 2>(a, caps, st) : run<4, 2, 3, XDT, 4>(a, caps, st);
+  return a.M <= 4 ? run_m<4, XDT>(a, caps, st) : run_m<kMaxM, XDT>(a, caps, st);
 }
 
 }  // namespace
 
-bool mx_fused(int64_t M, int64_t K) { return M <= kMaxM && token_lds(M, mx_pitch(K)) <= kTokenLds; }
-
-bool mx_decode_supported(int64_t M, int64_t K) { return mx_fused(M, K); }
+bool mx_decode_supported(int64_t M, int64_t K) { return M <= kMaxM && M * mx_pitch(K) <= kMaxColumns; }
 
 hipError_t launch_mx_decode(const MxArgs& a, const DeviceCaps& caps, hipStream_t st) {
   if (a.X == nullptr) return run_x<-1>(a, caps, st);
