@@ -247,8 +247,10 @@ hipError_t run(const MxArgs& a, const DeviceCaps& caps, hipStream_t st) {
   const int64_t lds = NW * SLOTS * slot_bytes(RT) + token_lds(a.M, a.P);
   constexpr int64_t fixed = 2 * NW * RT * 16 * (MT + 1) * 4;
   auto k = mx_decode_kernel<NW, RT, SLOTS, MT, XDT, C>;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (e != hipSuccess) return e;
+  if (lds + fixed > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
   const int64_t groups = (a.N + RT * 16 - 1) / (RT * 16), per_cu = std::max<int64_t>(1, 160 * 1024 / (lds + fixed));
   k<<<(unsigned)std::min<int64_t>(groups, per_cu * caps.cus), NW * 64, lds, st>>>(a.W, a.w_scales, a.A, a.a_scales, a.X, a.ldx,
                                                                                 (int)a.M, (int)a.N, (int)a.K, (int)a.P, a.ep);

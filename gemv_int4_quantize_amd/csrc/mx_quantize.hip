@@ -10,7 +10,7 @@ namespace w4 {
 
 namespace {
 
-constexpr int kChunks = 4;  // of eight columns, that a lane has in flight
+constexpr int kChunks = 2;  // of eight columns, that a lane has in flight (4: 64 rows of 4096 3.4 us instead of 2.8)
 
 // Chunk i of [rows][pc] chunks: its row and its place in it.  i counts from a row's start (base).
 struct Place {
