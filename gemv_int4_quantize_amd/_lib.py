@@ -39,7 +39,7 @@ EXPORTS_W8 = (
 # every entry point declared in include/mxfp4.h
 EXPORTS_MX = (
     "mx4_pitch", "mx4_quantize_rows", "mx4_dequantize_rows", "mx4_workspace_bytes", "mx4_mm", "mx4_linear", "mx4_kernel",
-    "mx4_mm_t_workspace_bytes", "mx4_mm_t", "mx4_moe_workspace_bytes", "mx4_moe",
+    "mx4_mm_t_workspace_bytes", "mx4_mm_t", "mx4_sum_workspace_bytes", "mx4_sum_rows", "mx4_moe_workspace_bytes", "mx4_moe",
 )
 
 
@@ -141,6 +141,8 @@ def lib() -> ctypes.CDLL:
     L.mx4_kernel.restype = ctypes.c_char_p
     L.mx4_mm_t_workspace_bytes.argtypes = [i64, i64, i64, i32, i64, psz]
     L.mx4_mm_t.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, i32, pseg, i32, vp, sz, vp]
+    L.mx4_sum_workspace_bytes.argtypes = [i64, i64, psz]
+    L.mx4_sum_rows.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, sz, vp]
     L.mx4_moe_workspace_bytes.argtypes = [i64, i64, i32, i64, i64, i32, psz]
     L.mx4_moe.argtypes = [vp, i32, i64, i64, vp, i32, i64, i64, i32, i32, vp, vp, vp, vp, i64, i64, vp, i64, vp, sz, vp]
     for name in EXPORTS_MX:

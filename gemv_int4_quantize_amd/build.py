@@ -19,7 +19,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libw4a16.so")
 SOURCES = ["api.hip", "quantize.hip", "gemv.hip", "gemm.hip", "gemm_nt.hip", "skinny.hip",
            "api_w8.hip", "w8_quantize.hip", "w8_gemm.hip", "w8_decode.hip", "w8_grad.hip", "scores.hip",
-           "api_mx.hip", "mx_quantize.hip", "mx_gemm.hip", "mx_decode.hip", "mx_grad.hip", "mx_moe.hip"]
+           "api_mx.hip", "mx_quantize.hip", "mx_gemm.hip", "mx_decode.hip", "mx_grad.hip", "mx_sum.hip",
+           "mx_moe.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

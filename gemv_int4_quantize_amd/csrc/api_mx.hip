@@ -282,6 +282,33 @@ int mx4_mm_t(const void* dY, int dtype, int64_t ld, int64_t M, const uint8_t* W,
   return launched(w4::launch_mx_grad(a, device_caps(), wsb > 0 ? w : nullptr, wsb, st), "mx4_mm_t");
 }
 
+int mx4_sum_workspace_bytes(int64_t M, int64_t N, size_t* bytes) {
+  const int s = check_sizes(M, N, 1);
+  if (s != W4_OK) return s;
+  if (!bytes) return fail(W4_ERR_INVALID, "bytes is NULL");
+  *bytes = w4::mx_sum_workspace_bytes(M, N, device_caps());
+  return ok();
+}
+
+int mx4_sum_rows(const void* X, int dtype, int64_t M, int64_t N, int64_t ld, void* out, int out_dtype, void* ws, size_t ws_bytes,
+                 void* stream) {
+  int s = check_sizes(M, N, 1);
+  if (s == W4_OK) s = check_rows(X, dtype, M, N, ld, "X");
+  if (s == W4_OK) s = check_rows(out, out_dtype, 1, N, N, "out");
+  if (s == W4_OK) s = check_ws(ws);
+  if (s != W4_OK) return s;
+  const w4_out_seg seg = {out, N, N};
+  w4::Epi ep;
+  s = make_epi(N, 1, nullptr, out_dtype, &seg, 1, &ep);
+  if (s != W4_OK) return s;
+  const w4::DeviceCaps caps = device_caps();
+  const size_t need = w4::mx_sum_workspace_bytes(M, N, caps);
+  if (need > 0 && (ws == nullptr || ws_bytes < need))
+    return fail(W4_ERR_RESOURCE, "mx4_sum_rows needs a workspace of %zu bytes (got %zu)", need,
+                ws != nullptr ? ws_bytes : (size_t)0);
+  return launched(w4::launch_mx_sum(X, dtype, M, N, ld, ep, caps, ws, static_cast<hipStream_t>(stream)), "mx4_sum_rows");
+}
+
 int mx4_moe_workspace_bytes(int64_t T, int64_t E, int top, int64_t H, int64_t F, int dtype, size_t* bytes) {
   const int s = check_moe(T, E, top, H, F, dtype);
   if (s != W4_OK) return s;

@@ -207,6 +207,11 @@ struct MxGradArgs {
 size_t mx_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int parts, const DeviceCaps& caps);
 hipError_t launch_mx_grad(const MxGradArgs& a, const DeviceCaps& caps, void* ws, size_t ws_bytes, hipStream_t st);
 
+// Column sums of X [M][N] (mx_sum.hip), to the one row of ep.
+size_t mx_sum_workspace_bytes(int64_t M, int64_t N, const DeviceCaps& caps);
+hipError_t launch_mx_sum(const void* X, int dt, int64_t M, int64_t N, int64_t ld, const Epi& ep, const DeviceCaps& caps, void* ws,
+                         hipStream_t st);
+
 // A layer of experts (mx_moe.hip) for T <= kMoeTokens tokens: x [T][mx_parts(dt)][ldx] bf16 parts
 // (rows 16-byte aligned), Hx columns of each (a multiple of 64) to read.
 constexpr int kMoeTokens = 64, kMoeTop = 16, kMoeExperts = 512;

@@ -46,6 +46,13 @@ __device__ __forceinline__ uint32_t quad_umax(uint32_t v) {
   return umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
 }
 
+// Eight columns of a row from column col, 0 past its last.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> mx_chunk_of(const typename Elem<DT>::type* x, int col, int cols) {
+  if (col + 8 <= cols) return load_raw8<DT>(x + col);
+  return col < cols ? load_raw8_part<DT>(x + col, cols - col, 0u) : Raw8<DT>{};
+}
+
 // Codes of eight elements at power p, rounded to nearest even and held at 6 (the conversion takes
 // the power off exactly, subnormal elements and powers included: checked over all 16-bit patterns
 // at 14 powers and fp32 values at and beside every tie).

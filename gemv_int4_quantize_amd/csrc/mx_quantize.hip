@@ -23,12 +23,6 @@ __device__ __forceinline__ Place place(int64_t base_row, uint32_t in_row, uint32
 }
 
 template <int DT>
-__device__ __forceinline__ Raw8<DT> chunk_of(const typename Elem<DT>::type* x, int col, int cols) {
-  if (col + 8 <= cols) return load_raw8<DT>(x + col);
-  return col < cols ? load_raw8_part<DT>(x + col, cols - col, 0u) : Raw8<DT>{};
-}
-
-template <int DT>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict__ X, int64_t rows, int cols, int64_t ld,
                                                           int pc, uint8_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales) {
@@ -42,7 +36,7 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict
   for (int c = 0; c < kChunks; ++c) {
     at[c] = place(row0, in_row, c * 256 + threadIdx.x, (uint32_t)pc);
     r[c] = Raw8<DT>{};
-    if (at[c].row < rows) r[c] = chunk_of<DT>(x + at[c].row * ld, at[c].chunk * 8, cols);
+    if (at[c].row < rows) r[c] = mx_chunk_of<DT>(x + at[c].row * ld, at[c].chunk * 8, cols);
   }
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
@@ -127,7 +121,7 @@ __global__ __launch_bounds__(256) void mx_parts_kernel(const void* __restrict__ 
   const int64_t row0 = first / pc;
   const Place at = place(row0, (uint32_t)(first - row0 * pc), threadIdx.x, (uint32_t)pc);
   if (at.row >= rows) return;
-  const Raw8<DT> r = chunk_of<DT>(x + at.row * ld, at.chunk * 8, cols);
+  const Raw8<DT> r = mx_chunk_of<DT>(x + at.row * ld, at.chunk * 8, cols);
   uint16_t* o = out + (at.row * NP * pc + at.chunk) * 8;
   if constexpr (NP == 1) {
     *reinterpret_cast<u32x4*>(o) = r.q[0];

@@ -15,7 +15,7 @@
  *           bit, for 0, .5, 1, 1.5, 2, 3, 4, 6.  The codes of columns C .. P-1 must be 0.
  *   scales  uint8 [R][P / 32], 4-byte aligned: every 32 columns share 2^(scale - 127); 255: NaN.
  * Tokens and weight channels both use it: X [M][K] is quantized along K, W [N][K] as well.
- * Rows, M and N are below 2^30, columns and K below 2^22.
+ * Rows, M and N are below 2^30, columns and K below 2^22.  Outputs overlap no input.
  */
 #ifndef MXFP4_H
 #define MXFP4_H
@@ -78,6 +78,13 @@ const char* mx4_kernel(int64_t M, int64_t N, int64_t K, int x_dtype);
 int mx4_mm_t_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype, int64_t ld, size_t* bytes);
 int mx4_mm_t(const void* dY, int dtype, int64_t ld, int64_t M, const uint8_t* W, const uint8_t* w_scales, int64_t N,
              int64_t K, int out_dtype, const w4_out_seg* segs, int nsegs, void* ws, size_t ws_bytes, void* stream);
+
+/* out[n] = out_rne(sum_m X[m][n]): X [M][N] F32, F16 or BF16 (row stride ld), out [N] of out_dtype; the bias's
+ * gradient of a linear layer, from dY.  fp32 sums in an order that M and N fix.  M == 0: zeros.  The
+ * workspace that mx4_sum_workspace_bytes reports is required. */
+int mx4_sum_workspace_bytes(int64_t M, int64_t N, size_t* bytes);
+int mx4_sum_rows(const void* X, int dtype, int64_t M, int64_t N, int64_t ld, void* out, int out_dtype, void* ws, size_t ws_bytes,
+                 void* stream);
 
 /* A mixture-of-experts layer for few tokens.  For token t (x = X[t], z = logits[t]) and the `top` experts
  * with the largest logits, by value and then the lower index:

@@ -168,6 +168,29 @@ def test_binding_refusals():
         w4.MXFP4Linear(w, out_dtype=torch.int8)
 
 
+def test_sum_refusals():
+    L, size = w4.lib(), ctypes.c_size_t(0)
+    f32 = _lib.DT_F32
+
+    def call(dtype=f32, M=4, N=8, ld=8, x=_p(), out=_p(), out_dtype=f32, ws=None, ws_bytes=0):
+        return L.mx4_sum_rows(x, dtype, M, N, ld, out, out_dtype, ws, ws_bytes, None)
+
+    for bad in (dict(dtype=7), dict(M=-1), dict(N=0), dict(ld=7), dict(x=None), dict(out=None), dict(out_dtype=9)):
+        assert call(**bad) == _lib.W4_ERR_INVALID, bad
+    assert call(N=1 << 30, ld=1 << 30) == _lib.W4_ERR_UNSUPPORTED
+    for bad in (dict(x=_p(0x10002)), dict(out=_p(0x10001)), dict(ws=_p(0x10008), ws_bytes=64)):
+        assert call(**bad) == _lib.W4_ERR_ALIGN, bad
+    assert L.mx4_sum_workspace_bytes(4096, 8, ctypes.byref(size)) == 0 and size.value > 0
+    assert call(M=4096) == _lib.W4_ERR_RESOURCE and call(M=4096, ws=_p(), ws_bytes=size.value - 1) == _lib.W4_ERR_RESOURCE
+    assert L.mx4_sum_workspace_bytes(4, 8, None) == _lib.W4_ERR_INVALID
+    with pytest.raises(ValueError, match="HIP device"):
+        w4.mxfp4.sum_rows(torch.zeros(2, 3))
+    with pytest.raises(ValueError, match="outputs must"):
+        w4.mxfp4.sum_rows(torch.zeros(2, 3), torch.int8)
+    with pytest.raises(TypeError):
+        w4.mxfp4.sum_rows(torch.zeros(2, 3, dtype=torch.int32))
+
+
 def test_kernel_names():
     k = w4.lib().mx4_kernel
     assert k(2, 4096, 4096, -1) == b"mx4_decode" and k(2, 4096, 4096, _lib.DT_BF16) == b"mx4_decode_fused"
@@ -191,6 +214,7 @@ def test_second_derivatives_raise(monkeypatch):
         return (g.float() @ weight).to(out_dtype)
 
     monkeypatch.setattr(mxfp4, "mm_mxfp4_t", back)
+    monkeypatch.setattr(mxfp4, "sum_rows", lambda g, out_dtype: g.float().sum(0).to(out_dtype))
     w = w4.MXFP4Rows(torch.zeros(8, 64, dtype=torch.uint8), torch.zeros(8, 4, dtype=torch.uint8), 8, 64)
     bias = torch.zeros(8, requires_grad=True)
     for b in (None, bias):
@@ -669,6 +693,59 @@ def test_streams_and_graph_replays(m):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,pad", [(0, 5, 0), (1, 1, 0), (3, 257, 0), (127, 40, 3), (128, 256, 0), (1000, 2049, 5), (20000, 33, 0)])
+@pytest.mark.parametrize("dtype", FLOATS)
+def test_sum_rows(m, n, pad, dtype):
+    x = torch.randn(m, n + pad, device=DEV).to(dtype)[:, :n]
+    want = x.double().sum(0)
+    most = x.double().abs().sum(0)
+    for out in FLOATS:
+        got = w4.mxfp4.sum_rows(x, out)
+        assert got.shape == (n,) and got.dtype == out
+        # m fp32 additions, each off by at most half an ulp of a partial sum, and one rounding
+        tol = most * (m * EPS32) + want.abs() * HALF_ULP[out] * 1.01 + TINY[out]
+        assert ((got.double() - want).abs() <= tol).all(), out
+        assert torch.equal(got, w4.mxfp4.sum_rows(x, out))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n", [(5, 64), (2048, 1024), (4096, 96)])
+def test_captured_step(m, n):
+    """Forward and backward in one graph, the bias's gradient with it, over several replays."""
+    w, _ = _weight(33, n, 256)
+    x = _rows(m, m, 256, torch.bfloat16)[0].contiguous().requires_grad_()
+    bias = torch.randn(n, device=DEV).requires_grad_()
+    gy = torch.randn(m, n, device=DEV)
+
+    def step(x, bias):
+        y = w4.mxfp4_linear(x, w, bias)
+        return y, *torch.autograd.grad(y, (x, bias), gy)
+
+    def eager():  # leaves of its own
+        return step(x.detach().clone().requires_grad_(), bias.detach().clone().requires_grad_())
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            eager()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(x, bias)
+    for i in range(5):
+        with torch.no_grad():
+            x.copy_(_rows(300 + i, m, 256, torch.bfloat16)[0])
+            bias.copy_(torch.randn(n, device=DEV))
+            gy.copy_(torch.randn(m, n, device=DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.detach().clone() for t in out]
+        for a, b in zip(got, eager()):
+            assert torch.equal(a, b), i
 
 
 @pytest.mark.gpu
