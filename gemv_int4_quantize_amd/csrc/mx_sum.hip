@@ -2,8 +2,8 @@
 //   out[n] = out_rne(sum_m X[m][n]), sums in fp32, in an order that M and N alone fix.
 // Bound by reading X once.  A workgroup takes 256 columns and one of S runs of the rows: eight groups of
 // 32 lanes, eight columns a lane, a row a group at a time (512 bytes of 16-bit elements next to one
-// another).  Where the columns alone leave CUs idle the rows are shared, and a second launch adds the S
-// sums: no atomics, and no counter that a captured graph would have to clear.
+// another).  Where the columns alone leave CUs idle the rows are shared, and the S sums are
+// rows that a second launch sums: no atomics, and no counter that a captured graph would have to clear.
 #include <algorithm>
 
 #include "api_common.h"
@@ -53,6 +53,13 @@ int runs(int64_t M, int64_t N, const DeviceCaps& caps) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(2 * caps.cus / blocks, M / 64));
 }
 
+template <int DT>
+hipError_t run(const void* X, int64_t M, int64_t N, int64_t ld, int s, const Epi& ep, float* part, hipStream_t st) {
+  mx_sum_kernel<DT><<<dim3((unsigned)((N + kCols - 1) / kCols), (unsigned)s), 256, 0, st>>>(X, M, (int)N, ld, (M + s - 1) / s, ep,
+                                                                                           part);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 size_t mx_sum_workspace_bytes(int64_t M, int64_t N, const DeviceCaps& caps) {
@@ -63,17 +70,14 @@ size_t mx_sum_workspace_bytes(int64_t M, int64_t N, const DeviceCaps& caps) {
 hipError_t launch_mx_sum(const void* X, int dt, int64_t M, int64_t N, int64_t ld, const Epi& ep, const DeviceCaps& caps, void* ws,
                          hipStream_t st) {
   const int s = runs(M, N, caps);
-  const int64_t per = (M + s - 1) / s;
-  const dim3 grid((unsigned)((N + kCols - 1) / kCols), (unsigned)s);
   float* part = s > 1 ? static_cast<float*>(ws) : nullptr;
+  hipError_t e;
   switch (dt) {
-    case W4_DT_F32: mx_sum_kernel<W4_DT_F32><<<grid, 256, 0, st>>>(X, M, (int)N, ld, per, ep, part); break;
-    case W4_DT_F16: mx_sum_kernel<W4_DT_F16><<<grid, 256, 0, st>>>(X, M, (int)N, ld, per, ep, part); break;
-    default: mx_sum_kernel<W4_DT_BF16><<<grid, 256, 0, st>>>(X, M, (int)N, ld, per, ep, part); break;
+    case W4_DT_F32: e = run<W4_DT_F32>(X, M, N, ld, s, ep, part, st); break;
+    case W4_DT_F16: e = run<W4_DT_F16>(X, M, N, ld, s, ep, part, st); break;
+    default: e = run<W4_DT_BF16>(X, M, N, ld, s, ep, part, st); break;
   }
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || s == 1) return e;
-  return launch_splitk_reduce(part, s, 1, 0, N, ep, st);
+  return e != hipSuccess || s == 1 ? e : run<W4_DT_F32>(part, s, N, N, 1, ep, nullptr, st);
 }
 
 }  // namespace w4
