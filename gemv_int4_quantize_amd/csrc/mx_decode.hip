@@ -2,10 +2,11 @@
 // once, and its bytes set the time; float tokens are quantized by the same launch.
 //
 // A workgroup stays for several groups of 16 RT channels, its tokens' codes in LDS; its waves share out
-// the contraction in 256-column units.  A wave has its own ring of units in LDS, filled by direct loads
-// (into registers, each lane at a row of its own, they cost the vector caches a tag for every 16
-// bytes), and its next units, of
-// this group or the one after it, are on their way while the sums of a group are put together.
+// the contraction in 256-column units.  A wave has its own ring of units in LDS, filled by direct loads,
+// and its next units, of this group or the one after it, are on their way while the sums of a group are put
+// together.  (Loads into registers, each lane at a row of its own, cost the vector caches a tag for every 16
+// bytes: one token at (N, K) = (12288, 4096) 12.9 us, 7.0 here.)  In a captured graph, one token:
+// (2048, 2048) 3.2 us, (4096, 11008) 6.6, (16384, 16384) 30.8 (4.6 TB/s).
 // v_mfma_scale_f32_16x16x128_f8f6f4 with channels as rows and tokens as columns: lane l supplies a
 // block of 32 columns of channel l % 16 and of token l % 16, the same columns of both, and their two
 // exponents, and holds token l % 16 of channels 4 (l / 16) .. + 3.

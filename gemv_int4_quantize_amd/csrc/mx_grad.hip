@@ -4,6 +4,9 @@
 // change with every row, so the 4-bit matrix instructions do not apply; but w has two significant
 // bits, so bf16 holds it exactly, and dY enters as bf16 parts whose sum it is (one of bf16, two of
 // fp16, three of fp32): the parts lengthen the contraction, and nothing is rounded before the sums.
+// What bounds it: the bf16 matrix cores, at the clock that they leave, and the last, partial round of tiles.
+// (M, N, K) = (2048, 4096, 8192), whole rounds: 110 us, 1.25 PFLOP/s (the library's product on a weight that
+// is bf16 already: 101); (2048, 4096, 11008), 1.34 rounds: 167, 1.11 PFLOP/s.
 #include <algorithm>
 
 #include "api_common.h"
@@ -260,9 +263,10 @@ struct GradPlan {
   int tile = 0, full = 0, splits = 1;
 };
 
-// The plan with the least estimated time: rounds of workgroups, each the contraction's stages; a
-// split adds the write and read of its planes (and a launch, most of which the fit found in t0).  256-row tiles take none of the columns,
-// all, or those that make whole rounds, the last, partial round then being one of 128-row tiles.
+// The plan with the least estimated time: rounds of workgroups, each the contraction's stages; a split
+// adds the write and read of its planes (and a launch, most of which the fit found in t0).  256-row tiles
+// take none of the columns, all, or those that make whole rounds, the last, partial round then being one
+// of 128-row tiles.
 GradPlan pick(int64_t M, int64_t N, int64_t K, int parts, const DeviceCaps& caps, bool allow_split) {
   const int64_t cus = caps.cus > 0 ? caps.cus : 256, kt = (N + BK - 1) / BK * parts;
   GradPlan best;

@@ -8,10 +8,14 @@
 // What bounds it: the weights of the experts that some token reaches, each read once.  A wave has its own
 // ring of units in LDS, filled by direct loads (in registers their lanes, each at a row of its own,
 // cost the vector caches a tag for every 16 bytes); they are widened to bf16 (exactly: two significant
-// bits) and multiplied on the matrix cores with up to sixteen tokens as the columns.  The activations enter as bf16 parts
-// whose sum they are (one of bf16, two of fp16, three of fp32), and so does g_j a_j (two parts,
-// 16 bits; three for fp32): the matrix cores have time for it, and what lies between the two
+// bits) and multiplied on the matrix cores with up to sixteen tokens as the columns.  The activations
+// enter as bf16 parts whose sum they are (one of bf16, two of fp16, three of fp32), and so does g_j a_j
+// (two parts, 16 bits; three for fp32): the matrix cores have time for it, and what lies between the two
 // products is not rounded to bf16's eight bits.
+// Launches, bf16: 4 tokens, 2 of 8 experts of 4096 x 11008, 42-49 us (262 MB, 5.3-6.2 TB/s), 29-34 (131 MB),
+// 4.7 for the parts; 32 tokens, 8 of 128 experts of 2048 x 768, 45 (187 MB), 23 and 4.9.  Reads of the
+// same pattern alone reach 5.7-6.4 TB/s; the rest is the choice ahead of the first weight (some 5 us for
+// 32 tokens) and the ends of the launches.  One token, 8 of 128 experts: 10.1, 5.2 and 2.5, all latency.
 #include <algorithm>
 
 #include "api_common.h"
