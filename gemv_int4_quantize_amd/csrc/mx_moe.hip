@@ -15,7 +15,7 @@
 // Launches, bf16: 4 tokens, 2 of 8 experts of 4096 x 11008, 42-49 us (262 MB, 5.3-6.2 TB/s), 29-34 (131 MB),
 // 4.7 for the parts; 32 tokens, 8 of 128 experts of 2048 x 768, 45 (187 MB), 23 and 4.9.  Reads of the
 // same pattern alone reach 5.7-6.4 TB/s; the rest is the choice ahead of the first weight (some 5 us for
-// 32 tokens) and the ends of the launches.  One token, 8 of 128 experts: 10.1, 5.2 and 2.5, all latency.
+// 32 tokens) and the ends of the launches.  One token, 8 of 128 experts: 10.6 and 7.0, all latency.
 #include <algorithm>
 
 #include "api_common.h"
@@ -555,40 +555,40 @@ __device__ __forceinline__ void store(void* out, int64_t i, float v) {
 // NaN among the weights would reach every token.)
 constexpr int kRowPitch = RT * 16 + 4;
 
-template <int DT, int COLS, int SLOTS>
-__global__ __launch_bounds__(NW * 64) void moe_down_kernel(const uint16_t* __restrict__ a, const Reached* __restrict__ reached,
+template <int DT, int COLS, int SLOTS, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void moe_down_kernel(const uint16_t* __restrict__ a, const Reached* __restrict__ reached,
                                                            const uint8_t* __restrict__ W, const uint8_t* __restrict__ we, int T,
                                                            int E, int top, int H, int Fp, int S, void* __restrict__ out,
                                                            int64_t ldo, float* __restrict__ part) {
   constexpr int HP = moe_parts(DT);
   constexpr int nD = 5, nX = COLS == 4 ? HP * 2 : HP * 8;  // loads of a unit's weights and columns
-  // rings [NW][SLOTS][kSlot], columns [NW][column_bytes], sums [NW][T][kRowPitch]
+  // rings [WAVES][SLOTS][kSlot], columns [WAVES][column_bytes], sums [WAVES][T][kRowPitch]
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ Reached s;
-  float* sums = reinterpret_cast<float*>(smem + NW * (SLOTS * kSlot + column_bytes(HP, COLS)));
+  float* sums = reinterpret_cast<float*>(smem + WAVES * (SLOTS * kSlot + column_bytes(HP, COLS)));
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int most = min(E, T * top);
-  for (int i = tid; i < most; i += NW * 64) {  // past the count: not used
+  for (int i = tid; i < most; i += WAVES * 64) {  // past the count: not used
     s.expert[i] = reached->expert[i];
     s.cols[i] = reached->cols[i];
     s.first[i] = reached->first[i];
   }
-  for (int i = tid; i < T * top; i += NW * 64) s.token[i] = reached->token[i];
+  for (int i = tid; i < T * top; i += WAVES * 64) s.token[i] = reached->token[i];
   const int count = __builtin_amdgcn_readfirstlane(reached->count);
   const uint64_t bad = reached->bad;
-  for (int i = tid; i < NW * T * kRowPitch; i += NW * 64) sums[i] = 0.0f;
+  for (int i = tid; i < WAVES * T * kRowPitch; i += WAVES * 64) sums[i] = 0.0f;
   lds_barrier();
   const int group = blockIdx.x / (unsigned)S, slice = blockIdx.x - group * S;
   const int h0 = group * 16 * RT;
   const uint32_t rows = (uint32_t)min(16 * RT, H - h0);
   const int of_expert = (Fp + 255) >> 8, units = count * of_expert;
-  const int per = (units + S * NW - 1) / (S * NW);
-  const int u0 = min((slice * NW + wave) * per, units), u1 = min(u0 + per, units);
+  const int per = (units + S * WAVES - 1) / (S * WAVES);
+  const int u0 = min((slice * WAVES + wave) * per, units), u1 = min(u0 + per, units);
   const rsrc_t rx = mx_rsrc(a, (uint32_t)(T * top) * (uint32_t)(HP * Fp) * 2u);
   float* mine = sums + wave * T * kRowPitch;
   char* own = smem + wave * (SLOTS * kSlot);
-  char* xs = smem + NW * SLOTS * kSlot + wave * column_bytes(HP, COLS);
+  char* xs = smem + WAVES * SLOTS * kSlot + wave * column_bytes(HP, COLS);
   if (u0 < u1) {
     // An expert, its units [from, to) of this wave and the next of them, its tokens from b0.
     struct Place {
@@ -681,12 +681,12 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(const uint16_t* __res
     wait_loads<0>();  // no direct LDS load may land after the workgroup's LDS is handed on
   }
   lds_barrier();
-  for (int i = tid; i < T * RT * 16; i += NW * 64) {
+  for (int i = tid; i < T * RT * 16; i += WAVES * 64) {
     const int t = i / (RT * 16), h = i - t * (RT * 16);
     if (h >= (int)rows) continue;
     float v = 0.0f;
 #pragma unroll
-    for (int k = 0; k < NW; ++k) v += sums[(k * T + t) * kRowPitch + h];
+    for (int k = 0; k < WAVES; ++k) v += sums[(k * T + t) * kRowPitch + h];
     if (part != nullptr) part[((size_t)slice * T + t) * H + h0 + h] = v;
     else store<DT>(out, t * ldo + h0 + h, (bad >> t & 1) != 0 ? __builtin_nanf("") : v);
   }
@@ -705,10 +705,31 @@ __global__ __launch_bounds__(256) void moe_join_kernel(const float* __restrict__
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Tokens of an expert that its weights are widened for at a time: four where experts have few (an
+// expert with more reads its weights again), else sixteen.
+bool few_each(const MoeArgs& a) { return a.T <= 4 || a.T * a.top <= 3 * a.E; }
+
+constexpr int down_lds(int dt, int cols, int slots, int waves, int64_t T) {
+  return waves * (slots * kSlot + column_bytes(moe_parts(dt), cols) + (int)T * kRowPitch * 4) + (int)sizeof(Reached);
+}
+
+// Units of the second launch for the same rows, if all experts that may be reached are.
+int64_t down_units(const MoeArgs& a) { return std::min<int64_t>(a.E, a.T * a.top) * ((mx_pitch(a.F) + 255) / 256); }
+
+// Whether one workgroup of eight waves does all of the units of its rows, so that no launch has to join
+// parts: where a wave gets few of them.  One token, 2 of 8 experts of 4096 x 2816, 22 units: 22.0 us with
+// the join, 19.2 without; 6 of 64 of 2048 x 1408, 36 units: 24.6, 22.9; 4 tokens, 8 of 128 of 2048 x 768,
+// 96 units: 30.3, 33.6.
+bool down_alone(const MoeArgs& a, const DeviceCaps& caps) {
+  return few_each(a) && (a.H + RT * 16 - 1) / (RT * 16) <= caps.cus && down_units(a) <= 8 * 6 &&
+         down_lds(a.dt, 4, 2, 8, a.T) <= 160 * 1024;
+}
+
 // Workgroups of the second launch for the same rows: as many as a round of them, two a CU, holds.
 int down_slices(const MoeArgs& a, const DeviceCaps& caps) {
+  if (down_alone(a, caps)) return 1;
   const int64_t groups = (a.H + RT * 16 - 1) / (RT * 16);
-  const int64_t units = std::min<int64_t>(a.E, a.T * a.top) * ((mx_pitch(a.F) + 255) / 256);
+  const int64_t units = down_units(a);
   const int64_t s = std::min<int64_t>(2 * caps.cus / groups, (units + NW - 1) / NW);
   return (int)std::max<int64_t>(1, std::min<int64_t>(s, 16));
 }
@@ -731,10 +752,6 @@ hipError_t allow_lds(K k, int bytes) {
   return hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// Tokens of an expert that its weights are widened for at a time: four where experts have few (an
-// expert with more reads its weights again), else sixteen.
-bool few_each(const MoeArgs& a) { return a.T <= 4 || a.T * a.top <= 3 * a.E; }
-
 template <int DT, int COLS>
 hipError_t up(const MoeArgs& a, const DeviceCaps& caps, char* ws, const Space& sp, hipStream_t st) {
   const int64_t Fp = mx_pitch(a.F);
@@ -751,30 +768,28 @@ hipError_t up(const MoeArgs& a, const DeviceCaps& caps, char* ws, const Space& s
   return hipGetLastError();
 }
 
-constexpr int down_lds(int dt, int cols, int slots, int64_t T) {
-  return NW * (slots * kSlot + column_bytes(moe_parts(dt), cols) + (int)T * kRowPitch * 4);
-}
-
-template <int DT, int COLS, int SLOTS>
+template <int DT, int COLS, int SLOTS, int WAVES>
 hipError_t down(const MoeArgs& a, char* ws, const Space& sp, int S, hipStream_t st) {
-  const int lds = down_lds(DT, COLS, SLOTS, a.T);
-  const hipError_t e = allow_lds(moe_down_kernel<DT, COLS, SLOTS>, lds);
+  const int lds = down_lds(DT, COLS, SLOTS, WAVES, a.T) - (int)sizeof(Reached);
+  const hipError_t e = allow_lds(moe_down_kernel<DT, COLS, SLOTS, WAVES>, lds);
   if (e != hipSuccess) return e;
   const int groups = (int)((a.H + RT * 16 - 1) / (RT * 16));
-  moe_down_kernel<DT, COLS, SLOTS><<<(unsigned)(groups * S), NW * 64, lds, st>>>(
+  moe_down_kernel<DT, COLS, SLOTS, WAVES><<<(unsigned)(groups * S), WAVES * 64, lds, st>>>(
       reinterpret_cast<const uint16_t*>(ws + sp.rows), reinterpret_cast<const Reached*>(ws), a.W2, a.w2_scales, (int)a.T,
       (int)a.E, a.top, (int)a.H, (int)mx_pitch(a.F), S, a.out, a.ldo, S > 1 ? reinterpret_cast<float*>(ws + sp.part) : nullptr);
   return hipGetLastError();
 }
 
 // Rings of three units where two workgroups of them share a CU, else of two (the sums of many tokens
-// take the place).
+// take the place; of eight waves with a CU to themselves, three are slower: 18.4 us instead of 17.6 for
+// one token and 8 of 128 experts).
 template <int DT, int COLS>
 hipError_t both(const MoeArgs& a, const DeviceCaps& caps, char* ws, const Space& sp, int S, hipStream_t st) {
   const hipError_t e = up<DT, COLS>(a, caps, ws, sp, st);
   if (e != hipSuccess) return e;
-  return down_lds(DT, COLS, 3, a.T) + (int)sizeof(Reached) <= 80 * 1024 ? down<DT, COLS, 3>(a, ws, sp, S, st)
-                                                                         : down<DT, COLS, 2>(a, ws, sp, S, st);
+  if constexpr (COLS == 4)
+    if (down_alone(a, caps)) return down<DT, COLS, 2, 8>(a, ws, sp, S, st);
+  return down_lds(DT, COLS, 3, NW, a.T) <= 80 * 1024 ? down<DT, COLS, 3, NW>(a, ws, sp, S, st) : down<DT, COLS, 2, NW>(a, ws, sp, S, st);
 }
 
 template <int DT>

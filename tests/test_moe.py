@@ -177,7 +177,8 @@ def _check(got, x, z, w1, w2, top, renorm, what=""):
 SIZES = [  # T, E, top, H, F
     (1, 1, 1, 1, 1), (1, 8, 2, 64, 96), (1, 128, 8, 256, 128), (2, 4, 4, 130, 33), (3, 20, 3, 1003, 700), (5, 8, 2, 512, 300),
     (15, 16, 2, 128, 257), (16, 60, 4, 200, 130), (17, 8, 3, 192, 129), (31, 64, 6, 320, 64), (33, 3, 2, 96, 96),
-    (48, 32, 1, 384, 200), (64, 128, 8, 256, 64), (64, 2, 2, 72, 40), (7, 512, 16, 64, 32), (64, 512, 16, 64, 32), (4, 8, 2, 2048, 1408)]
+    (48, 32, 1, 384, 200), (64, 128, 8, 256, 64), (64, 2, 2, 72, 40), (7, 512, 16, 64, 32), (64, 512, 16, 64, 32), (4, 8, 2, 2048, 1408),
+    (1, 8, 2, 96, 7000), (4, 16, 4, 160, 1100)]
 
 
 @pytest.mark.gpu
