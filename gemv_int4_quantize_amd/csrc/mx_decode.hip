@@ -1,5 +1,5 @@
-// Product of microscaled 4-bit rows for one to sixteen tokens (decode), for gfx950.  The weight is read
-// once, and its bytes set the time; float tokens are quantized by the same launch.
+// Products of microscaled 4-bit rows for few tokens, for gfx950: one to eight that are quantized by the same
+// launch (decode), or up to 32 whose codes are ready.  The weight is read once, and its bytes set the time.
 //
 // A workgroup stays for several groups of 16 RT channels, its tokens' codes in LDS; its waves share out
 // the contraction in 256-column units.  A wave has its own ring of units in LDS, filled by direct loads,
@@ -22,12 +22,13 @@ namespace w4 {
 namespace {
 
 constexpr int kNonTemporal = 2;       // cache-policy operand of a load
-constexpr int kMaxM = 16;             // tokens
-// Columns of all tokens.  Every workgroup quantizes them, and past these the tiles behind a launch that
-// quantizes once are as fast: (N, K) = (12288, 4096), 8 tokens 10.1 us here, 11.9 on the tiles, 12
-// tokens 13.1 and 12.1; (4096, 11008), 4 tokens 8.4, 13.0, 8 tokens 14.8, 13.7; (16384, 16384), 2 tokens
-// 32.4, 36.3, 4 tokens 39.6, 36.4.
-constexpr int64_t kMaxColumns = 45056;
+constexpr int kMaxM = 8;              // tokens
+// Columns of all tokens, up to four of them and up to eight.  Every workgroup quantizes them, and past these
+// a launch that quantizes once and one for ready codes are as fast.  (N, K) = (12288, 4096): 8 tokens 9.7 us
+// here, 9.8 so, 10 tokens 11.6, 10.2; (4096, 11008): 4 tokens 8.3, 8.7, 6 tokens 13.1, 8.9; (8192, 2048):
+// 8 tokens 5.5, 6.3, 10 tokens 6.9, 6.5; (16384, 16384): 2 tokens 33, 3 tokens 37.5, 32.9.
+constexpr int64_t max_columns(int64_t M) { return M <= 4 ? 45056 : 32768; }
+constexpr int kFewM = 32;  // tokens whose codes are ready
 
 // The tokens in LDS: exponents [M][P / 32], then codes [M][P / 2 + 16] (the pad keeps the tokens' rows in
 // distinct banks).
@@ -269,12 +270,182 @@ hipError_t run_x(const MxArgs& a, const DeviceCaps& caps, hipStream_t st) {
   return a.M <= 4 ? run_m<4, XDT>(a, caps, st) : run_m<kMaxM, XDT>(a, caps, st);
 }
 
+// Up to 16 CT tokens whose codes are ready: as above, but a unit in the ring also holds the tokens' rows,
+// read again for each group of 16 RT channels (they stay in the L2s).  No split planes, no second launch:
+// 32 tokens at (N, K) = (4096, 11008) 9.5 us, on tiles and a sum of splits 11.8; (4096, 4096) 5.4, 8.2; 24
+// tokens at (16384, 16384) 35.0, 38.0.
+template <int NW, int RT, int CT, int SLOTS>
+__global__ __launch_bounds__(NW * 64) void mx_few_kernel(const uint8_t* __restrict__ W, const uint8_t* __restrict__ we,
+                                                         const uint8_t* __restrict__ A, const uint8_t* __restrict__ ae, int M,
+                                                         int N, int P, const Epi ep) {
+  constexpr int T = NW * 64, nD = 2 * (RT + CT) + 2;  // loads of a unit
+  constexpr int EXPS = (RT + CT) * 2048, SLOT = EXPS + 512;
+  static_assert(RT <= 2 && CT <= 2, "exponents of 32 rows by a load");
+  extern __shared__ __attribute__((aligned(16))) char smem[];  // rings [NW][SLOTS][SLOT]
+  __shared__ float sums[2][NW][RT * 16][CT * 16 + 1];          // of groups in turn
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int units = (P + 255) >> 8, groups = (N + RT * 16 - 1) / (RT * 16);
+  const int row = P >> 1, erow = P >> 5;  // bytes of a row's codes and exponents
+  const int r16 = lane & 15, q4 = lane >> 4;
+  char* own = smem + wave * (SLOTS * SLOT);
+  int off[2];  // where a lane's loads of 8 rows begin
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = 8 * j + (lane >> 3);
+    off[j] = r * row + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+  }
+  const int eoff = (lane >> 1) * erow + (lane & 1) * 4;
+  // A group of channels and the unit (one step also where the wave has none).
+  struct Place {
+    int group, u;
+  };
+  auto advance = [&](Place& p) {
+    p.u += NW;
+    if (p.u < units) return;
+    p.u = wave;
+    p.group += gridDim.x;
+  };
+  // channels and tokens past the last one, and all of a place past the end: 0, without a request
+  auto load = [&](const Place& p, int slot) {
+    char* at = own + slot * SLOT;
+    const bool in = p.group < groups && p.u < units;
+    const size_t n0 = (size_t)p.group * (RT * 16);
+    const int rows = in ? min(RT * 16, N - (int)n0) : 0, tokens = in ? M : 0;
+#pragma unroll
+    for (int r = 0; r < RT + CT; ++r) {
+      const uint8_t* base = r < RT ? W + (n0 + r * 16) * row : A + (size_t)((r - RT) * 16) * row;
+      const int left = r < RT ? rows - r * 16 : tokens - (r - RT) * 16;
+      const rsrc_t rs = mx_rsrc(base, __builtin_amdgcn_readfirstlane(max(0, min(left, 16)) * (uint32_t)row));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        char* to = at + r * 2048 + j * 1024;
+        if (r < RT) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)to, 16, (int)off[j], (int)(p.u * 128), 0, kNonTemporal);
+        else __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)to, 16, (int)off[j], (int)(p.u * 128), 0, 0);
+      }
+    }
+    const rsrc_t re = mx_rsrc(we + n0 * erow, __builtin_amdgcn_readfirstlane(rows * (uint32_t)erow));
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(re, (lds_void*)(at + EXPS), 4, (int)eoff, (int)(p.u * 8), 0, 0);
+    const rsrc_t ra = mx_rsrc(ae, __builtin_amdgcn_readfirstlane(tokens * (uint32_t)erow));
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(at + EXPS + 256), 4, (int)eoff, (int)(p.u * 8), 0, 0);
+  };
+  Place now = {(int)blockIdx.x, wave}, ahead = now;
+#pragma unroll
+  for (int k = 0; k < SLOTS - 1; ++k) {
+    load(ahead, k);
+    advance(ahead);
+  }
+  f32x4 acc[RT][CT];
+  auto begin = [&]() {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  begin();
+  int slot = 0, turn = 0;
+  while (now.group < groups) {
+    load(ahead, slot == 0 ? SLOTS - 1 : slot - 1);
+    advance(ahead);
+    {
+      constexpr int n = (SLOTS - 1) * nD;
+      static_assert(n < 64, "the wait's counter");
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt((n & 15) | 0xF70 | ((n >> 4) << 14));
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (now.u < units) {
+      const char* at = own + slot * SLOT;
+      u32x2 ew[RT], ex[CT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) ew[r] = *reinterpret_cast<const u32x2*>(at + EXPS + (r * 16 + r16) * 8);
+#pragma unroll
+      for (int c = 0; c < CT; ++c) ex[c] = *reinterpret_cast<const u32x2*>(at + EXPS + 256 + (c * 16 + r16) * 8);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && now.u * 256 + 128 >= P) break;  // the row ends in the middle of its last unit
+        const int chunk = r16 * 128 + (((4 * h + q4) ^ (r16 >> 1)) << 4);
+        u32x4 x[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) x[c] = *reinterpret_cast<const u32x4*>(at + (RT + c) * 2048 + chunk);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const u32x4 w = *reinterpret_cast<const u32x4*>(at + r * 2048 + chunk);
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+            acc[r][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(w), mx_operand(x[c]), acc[r][c], kFp4, kFp4, 0,
+                                                                         (int)(ew[r][h] >> (8 * q4)), 0, (int)(ex[c][h] >> (8 * q4)));
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    slot = slot == SLOTS - 1 ? 0 : slot + 1;
+    if (now.u + NW >= units) {
+      // the group's sums, by waves in turn, with one barrier a group (as above)
+      float(*sum)[RT * 16][CT * 16 + 1] = sums[turn & 1];
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[wave][r * 16 + q4 * 4 + i][c * 16 + r16] = acc[r][c][i];
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      for (int i = ((wave + turn) & (NW - 1)) * 64 + lane; i < M * (RT * 16); i += T) {
+        const int m = i / (RT * 16), c = i % (RT * 16), n = now.group * (RT * 16) + c;
+        if (n >= N) continue;
+        float s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NW; ++v) s += sum[v][c][m];
+        epi_put(ep, epi_col(ep, n), m, s);
+      }
+      ++turn;
+      begin();
+    }
+    advance(now);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0070);  // no direct LDS load may land after the workgroup's LDS is handed on
+}
+
+template <int NW, int RT, int CT, int SLOTS>
+hipError_t run_few(const MxArgs& a, const DeviceCaps& caps, hipStream_t st) {
+  static_assert((NW & (NW - 1)) == 0, "waves in turn");
+  constexpr int lds = NW * SLOTS * ((RT + CT) * 2048 + 512), fixed = 2 * NW * RT * 16 * (CT * 16 + 1) * 4;
+  static_assert(lds + fixed <= 160 * 1024, "a CU's LDS");
+  auto k = mx_few_kernel<NW, RT, CT, SLOTS>;
+  if (lds + fixed > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t groups = (a.N + RT * 16 - 1) / (RT * 16), per_cu = 160 * 1024 / (lds + fixed);
+  k<<<(unsigned)std::min<int64_t>(groups, per_cu * caps.cus), NW * 64, lds, st>>>(a.W, a.w_scales, a.A, a.a_scales, (int)a.M, (int)a.N,
+                                                                                (int)a.P, a.ep);
+  return hipGetLastError();
+}
+
 }  // namespace
 
-bool mx_decode_supported(int64_t M, int64_t K) { return M <= kMaxM && M * mx_pitch(K) <= kMaxColumns; }
+bool mx_decode_supported(int64_t M, int64_t K) { return M <= kMaxM && M * mx_pitch(K) <= max_columns(M); }
+
+// One or two ready tokens are faster where they lie in LDS: (4096, 11008) 6.1 us for one, 6.8 here; from
+// three on here: four 7.5, 6.8.
+bool mx_few_supported(int64_t M, int64_t K) { return M <= kFewM && !(M <= 2 && mx_decode_supported(M, K)); }
+
+// Groups of 32 channels where they make nearly whole rounds of the CUs, else of 16, two workgroups a CU
+// (twice the tokens' reads): 16 tokens at (8192, 8192) 10.6 us, 11.6 of 16; at (11008, 4096), 1.3 rounds, 9.0,
+// 8.3.  Tiles for as many: 13.1 and 9.1.
+hipError_t launch_mx_few(const MxArgs& a, const DeviceCaps& caps, hipStream_t st) {
+  const int64_t groups = (a.N + 31) / 32, rounds = (groups + caps.cus - 1) / caps.cus;
+  if (groups * 5 >= rounds * caps.cus * 4) return a.M <= 16 ? run_few<4, 2, 1, 3>(a, caps, st) : run_few<4, 2, 2, 3>(a, caps, st);
+  return a.M <= 16 ? run_few<4, 1, 1, 3>(a, caps, st) : run_few<4, 1, 2, 2>(a, caps, st);
+}
 
 hipError_t launch_mx_decode(const MxArgs& a, const DeviceCaps& caps, hipStream_t st) {
-  if (a.X == nullptr) return run_x<-1>(a, caps, st);
+  if (a.X == nullptr) return run_m<4, -1>(a, caps, st);
   switch (a.x_dt) {
     case W4_DT_F32: return run_x<W4_DT_F32>(a, caps, st);
     case W4_DT_F16: return run_x<W4_DT_F16>(a, caps, st);

@@ -194,6 +194,7 @@ def test_sum_refusals():
 def test_kernel_names():
     k = w4.lib().mx4_kernel
     assert k(2, 4096, 4096, -1) == b"mx4_decode" and k(2, 4096, 4096, _lib.DT_BF16) == b"mx4_decode_fused"
+    assert k(32, 4096, 4096, -1) == k(32, 4096, 4096, _lib.DT_BF16) == b"mx4_few"
     assert k(64, 4096, 4096, -1) == k(64, 4096, 4096, _lib.DT_F32) is not None
     assert w4.mxfp4_kernel_for(8192, 8192, 8192) == "mx4_256x256"
     for bad in ((2, 4096, 4096, 9), (0, 64, 64, -1), (4, 0, 64, -1), (4, 64, 1 << 22, -1)):
@@ -368,7 +369,8 @@ def test_all_codes_and_scales():
 SHAPES = [(1, 1, 1), (1, 64, 64), (1, 2048, 2048), (2, 33, 70), (3, 1000, 4096), (4, 512, 11008), (5, 100, 129),
           (16, 48, 4096), (17, 515, 2048), (32, 256, 1030), (33, 130, 640), (64, 96, 8192), (65, 300, 1000),
           (127, 257, 511), (128, 128, 128), (200, 640, 192), (257, 259, 300), (300, 1003, 1555), (515, 2050, 257),
-          (8, 5000, 300), (12, 9000, 384), (4, 9000, 257), (700, 2304, 640)]
+          (8, 5000, 300), (12, 9000, 384), (4, 9000, 257), (700, 2304, 640),
+          (16, 8000, 300), (29, 8190, 1100), (24, 16384, 640), (32, 9000, 256), (1, 40, 60000), (6, 8, 5000), (31, 17, 60)]
 
 
 @pytest.mark.gpu
