@@ -218,7 +218,7 @@ hipError_t launch_mx_sum(const void* X, int dt, int64_t M, int64_t N, int64_t ld
 // A layer of experts (mx_moe.hip) for T <= kMoeTokens tokens: x [T][mx_parts(dt)][ldx] bf16 parts
 // (rows 16-byte aligned), Hx columns of each (a multiple of 64) to read.
 constexpr int kMoeTokens = 64, kMoeTop = 16, kMoeExperts = 512;
-constexpr int moe_parts(int dt) { return dt == W4_DT_F32 ? 3 : 2; }  // of what lies between the products
+constexpr int kMoeParts = 3;  // of what lies between the products: all bits of an fp32
 struct MoeArgs {
   const uint16_t* x;
   int64_t ldx, Hx;

@@ -10,8 +10,9 @@
 // cost the vector caches a tag for every 16 bytes); they are widened to bf16 (exactly: two significant
 // bits) and multiplied on the matrix cores with up to sixteen tokens as the columns.  The activations
 // enter as bf16 parts whose sum they are (one of bf16, two of fp16, three of fp32), and so does g_j a_j
-// (two parts, 16 bits; three for fp32): the matrix cores have time for it, and what lies between the two
-// products is not rounded to bf16's eight bits.
+// (three of an fp32): the matrix cores have time for it, and nothing is rounded between the products.  (Two
+// parts, 16 bits, lose differences of nearly equal activations; in a captured graph 19.6 us instead of 20.6
+// for one token and 8 of 128 experts of 2048 x 768, 76.8 instead of 80.5 for 4 tokens and 2 of 8 of 4096 x 11008.)
 // Launches, bf16: 4 tokens, 2 of 8 experts of 4096 x 11008, 42-49 us (262 MB, 5.3-6.2 TB/s), 29-34 (131 MB),
 // 4.7 for the parts; 32 tokens, 8 of 128 experts of 2048 x 768, 45 (187 MB), 23 and 4.9.  Reads of the
 // same pattern alone reach 5.7-6.4 TB/s; the rest is the choice ahead of the first weight (some 5 us for
@@ -381,7 +382,7 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(const uint16_t* __restr
                                                          const uint8_t* __restrict__ W, const uint8_t* __restrict__ we, int T,
                                                          int E, int top, int renorm, int P, int F, int Fp,
                                                          uint16_t* __restrict__ a, Reached* __restrict__ reached) {
-  constexpr int NP = mx_parts(DT), HP = moe_parts(DT);
+  constexpr int NP = mx_parts(DT), HP = kMoeParts;
   constexpr int nD = 5, nX = COLS == 4 ? NP * 2 : NP * 8;  // loads of a unit's weights and columns
   extern __shared__ __attribute__((aligned(16))) char ring[];  // [NW][kSlots][kSlot], then columns [NW][column_bytes]
   __shared__ Routing s;
@@ -465,7 +466,7 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(const uint16_t* __restr
     for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   };
   // Sums of the waves, activation, weight, and the parts (as of mx_parts_kernel: the rest cut to eight
-  // bits, the last one rounded), by waves in turn.  One barrier an item: the next item's sums have a
+  // bits), by waves in turn.  One barrier an item: the next item's sums have a
   // place of their own, and when they are written every wave has passed this one's.
   int turn = 0;
   auto finish = [&](const Place& p) {
@@ -493,7 +494,6 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(const uint16_t* __restr
 #pragma unroll
       for (int k = 0; k < HP; ++k) {
         uint32_t bits = __float_as_uint(v) >> 16;
-        if (k == HP - 1 && !odd) bits = pack_bf16x2(v, 0.0f) & 0xFFFFu;
         if (odd) bits = k > 0 ? 0u : (__float_as_uint(v) & 0x7FFFFFu) != 0 ? 0x7FC0u : bits;
         o[(size_t)k * Fp] = (uint16_t)bits;
         v -= __uint_as_float(bits << 16);
@@ -560,15 +560,23 @@ __global__ __launch_bounds__(WAVES * 64) void moe_down_kernel(const uint16_t* __
                                                            const uint8_t* __restrict__ W, const uint8_t* __restrict__ we, int T,
                                                            int E, int top, int H, int Fp, int S, void* __restrict__ out,
                                                            int64_t ldo, float* __restrict__ part) {
-  constexpr int HP = moe_parts(DT);
+  constexpr int HP = kMoeParts;
   constexpr int nD = 5, nX = COLS == 4 ? HP * 2 : HP * 8;  // loads of a unit's weights and columns
-  // rings [WAVES][SLOTS][kSlot], columns [WAVES][column_bytes], sums [WAVES][T][kRowPitch]
+  // rings [WAVES][SLOTS][kSlot], columns [WAVES][column_bytes], sums [WAVES][T][kRowPitch], and of Reached
+  // as much as there may be: all of it would take the place of the second workgroup on a CU
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ Reached s;
   float* sums = reinterpret_cast<float*>(smem + WAVES * (SLOTS * kSlot + column_bytes(HP, COLS)));
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int most = min(E, T * top);
+  struct {
+    uint16_t *expert, *first;
+    uint8_t *cols, *token;
+  } s;
+  s.expert = reinterpret_cast<uint16_t*>(sums + WAVES * T * kRowPitch);
+  s.first = s.expert + most;
+  s.cols = reinterpret_cast<uint8_t*>(s.first + most);
+  s.token = s.cols + most;
   for (int i = tid; i < most; i += WAVES * 64) {  // past the count: not used
     s.expert[i] = reached->expert[i];
     s.cols[i] = reached->cols[i];
@@ -709,8 +717,9 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 // expert with more reads its weights again), else sixteen.
 bool few_each(const MoeArgs& a) { return a.T <= 4 || a.T * a.top <= 3 * a.E; }
 
-constexpr int down_lds(int dt, int cols, int slots, int waves, int64_t T) {
-  return waves * (slots * kSlot + column_bytes(moe_parts(dt), cols) + (int)T * kRowPitch * 4) + (int)sizeof(Reached);
+int down_lds(const MoeArgs& a, int cols, int slots, int waves) {
+  return waves * (slots * kSlot + column_bytes(kMoeParts, cols) + (int)a.T * kRowPitch * 4) +
+         (int)(5 * std::min<int64_t>(a.E, a.T * a.top) + a.T * a.top);
 }
 
 // Units of the second launch for the same rows, if all experts that may be reached are.
@@ -722,7 +731,7 @@ int64_t down_units(const MoeArgs& a) { return std::min<int64_t>(a.E, a.T * a.top
 // 96 units: 30.3, 33.6.
 bool down_alone(const MoeArgs& a, const DeviceCaps& caps) {
   return few_each(a) && (a.H + RT * 16 - 1) / (RT * 16) <= caps.cus && down_units(a) <= 8 * 6 &&
-         down_lds(a.dt, 4, 2, 8, a.T) <= 160 * 1024;
+         down_lds(a, 4, 2, 8) <= 160 * 1024;
 }
 
 // Workgroups of the second launch for the same rows: as many as a round of them, two a CU, holds.
@@ -741,7 +750,7 @@ struct Space {
 Space space_of(const MoeArgs& a, const DeviceCaps& caps) {
   Space s;
   s.rows = up256(sizeof(Reached));
-  s.part = s.rows + up256((size_t)a.T * a.top * moe_parts(a.dt) * mx_pitch(a.F) * 2);
+  s.part = s.rows + up256((size_t)a.T * a.top * kMoeParts * mx_pitch(a.F) * 2);
   const int slices = down_slices(a, caps);
   s.total = s.part + (slices > 1 ? up256((size_t)slices * a.T * a.H * 4) : 0);
   return s;
@@ -770,7 +779,7 @@ hipError_t up(const MoeArgs& a, const DeviceCaps& caps, char* ws, const Space& s
 
 template <int DT, int COLS, int SLOTS, int WAVES>
 hipError_t down(const MoeArgs& a, char* ws, const Space& sp, int S, hipStream_t st) {
-  const int lds = down_lds(DT, COLS, SLOTS, WAVES, a.T) - (int)sizeof(Reached);
+  const int lds = down_lds(a, COLS, SLOTS, WAVES);
   const hipError_t e = allow_lds(moe_down_kernel<DT, COLS, SLOTS, WAVES>, lds);
   if (e != hipSuccess) return e;
   const int groups = (int)((a.H + RT * 16 - 1) / (RT * 16));
@@ -789,7 +798,7 @@ hipError_t both(const MoeArgs& a, const DeviceCaps& caps, char* ws, const Space&
   if (e != hipSuccess) return e;
   if constexpr (COLS == 4)
     if (down_alone(a, caps)) return down<DT, COLS, 2, 8>(a, ws, sp, S, st);
-  return down_lds(DT, COLS, 3, NW, a.T) <= 80 * 1024 ? down<DT, COLS, 3, NW>(a, ws, sp, S, st) : down<DT, COLS, 2, NW>(a, ws, sp, S, st);
+  return down_lds(a, COLS, 3, NW) <= 80 * 1024 ? down<DT, COLS, 3, NW>(a, ws, sp, S, st) : down<DT, COLS, 2, NW>(a, ws, sp, S, st);
 }
 
 template <int DT>

@@ -93,8 +93,8 @@ int mx4_sum_rows(const void* X, int dtype, int64_t M, int64_t N, int64_t ld, voi
  * G_e is rows 2 F e .. 2 F e + F - 1 of the mx4 rows W1 [E * 2F][H], its up projection U_e the next F,
  * and D_e is rows e H .. e H + H - 1 of W2 [E * H][F].  X [T][H] has dtype F32, F16 or BF16 and row
  * stride ldx, out the same dtype and row stride ldo; logits [T][E] any of the three, row stride ldl.
- * The weights and x enter as they are, sums are fp32; g_j a_j keeps 16 significant bits (F32: all 24)
- * between the two products; one rounding of the result.
+ * The weights and x enter as they are, sums, a_j and g_j are fp32, and so is g_j a_j between the two
+ * products; one rounding of the result.
  * A logit of -infinity is an expert that is masked: it is never run, also where fewer than `top` are
  * left.  A token whose logits are all -infinity gets 0.  A token with a NaN or +infinity among its
  * logits gets NaN.

@@ -1,5 +1,5 @@
 """The experts' layer where experts have many tokens (sixteen columns a product), on contractions of several
-units."""
+units, and what it keeps of the activations between its two products."""
 
 import pytest
 import torch
@@ -93,3 +93,31 @@ def test_agreeing_tokens_on_few_columns(T):
         x, z = _inputs(T, T, E, H, dtype, torch.float32)
         z = z[:1].expand(T, E).contiguous()
         _check(w4.moe_mxfp4(x, z, w1, w2, top), x, z, w1, w2, top, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("T,E,H,F", [(1, 1, 64, 32), (1, 1, 1100, 2100), (4, 2, 2100, 300), (16, 64, 200, 40), (16, 2, 1300, 300),
+                                     (8, 64, 96, 2000), (38, 64, 96, 40), (39, 64, 96, 40),
+                                     (64, 3, 96, 64)])
+def test_nothing_is_lost_between_the_products(T, E, H, F, dtype):
+    """Differences of nearly equal activations come out whole: silu(64) is 64 in fp32, so that
+    g a = 64 (1 + 2^-8 + 2^-j) and 64 (1 + 2^-8) for the columns that the down projection subtracts, both
+    exact in fp32; 64 2^-j is left for every j down to fp32's last bit."""
+    gate_up, down = torch.zeros(E, 2 * F, H, device=DEV), torch.zeros(E, H, F, device=DEV)
+    one, more, small, last = H // 2, H - 3, H - 2, H - 1
+    gate_up[:, :F, 0] = 1.0
+    gate_up[:, F:, one] = gate_up[:, F:, more] = 1.0
+    gate_up[:, F, small] = 1.0  # the first activation has the small number too
+    down[:, :, 0], down[:, :, F - 1] = 1.0, -1.0
+    down[:, last] = -down[:, last]
+    w1, w2 = w4.quantize_mxfp4(gate_up.flatten(0, 1)), w4.quantize_mxfp4(down.flatten(0, 1))
+    j = torch.arange(T, device=DEV) % 7 + 17 if T > 1 else torch.tensor([19], device=DEV)
+    x = torch.zeros(T, H, device=DEV)
+    x[:, 0], x[:, one], x[:, more], x[:, small] = 64.0, 1.0, 2.0**-8, torch.exp2(-j.float())
+    z = torch.full((T, E), -INF, device=DEV)
+    z[torch.arange(T, device=DEV), torch.arange(T, device=DEV) % E] = 0.5
+    y = w4.moe_mxfp4(x.to(dtype), z, w1, w2, 1).double()
+    want = torch.exp2(6.0 - j.double())[:, None].repeat(1, H)
+    want[:, last] *= -1
+    assert torch.equal(y, want)
