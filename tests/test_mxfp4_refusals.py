@@ -37,3 +37,13 @@ def test_no_derivative_is_lost(name):
         call(t)
     with torch.no_grad(), pytest.raises(ValueError, match="HIP device"):
         call(t.clone().requires_grad_())
+
+
+@pytest.mark.parametrize("gate_up,down", [((4, 40, 64), (2, 64, 40)), ((2, 160, 64), (4, 64, 40)), ((4, 80, 64), (4, 40, 64)),
+                                          ((1, 320, 64), (4, 64, 40)), ((4, 80, 64), (1, 256, 40)), ((8, 40, 64), (4, 64, 40))])
+def test_experts_of_other_shapes(monkeypatch, gate_up, down):
+    """Weights whose rows add up, but not expert by expert."""
+    monkeypatch.setattr(w4.mxfp4, "quantize_mxfp4", lambda t: _rows(*t.shape))
+    assert w4.MXFP4MoE.from_weight(torch.zeros(4, 80, 64), torch.zeros(4, 64, 40), 2).experts == 4
+    with pytest.raises(ValueError, match="are wanted"):
+        w4.MXFP4MoE.from_weight(torch.zeros(gate_up), torch.zeros(down), 1)
