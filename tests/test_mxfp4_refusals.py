@@ -47,3 +47,17 @@ def test_experts_of_other_shapes(monkeypatch, gate_up, down):
     assert w4.MXFP4MoE.from_weight(torch.zeros(4, 80, 64), torch.zeros(4, 64, 40), 2).experts == 4
     with pytest.raises(ValueError, match="are wanted"):
         w4.MXFP4MoE.from_weight(torch.zeros(gate_up), torch.zeros(down), 1)
+
+
+def test_logits_of_other_tokens(monkeypatch):
+    """As many tokens, in another order of the leading sizes, are not the same tokens."""
+    seen = []
+    monkeypatch.setattr(w4.mxfp4, "moe_mxfp4", lambda x, z, *_: seen.append((x.shape, z.shape)) or x)
+    layer = w4.MXFP4MoE(_rows(4 * 2 * 40, 64), _rows(4 * 64, 40), 2)
+    for x, z in (((2, 3, 64), (3, 2, 4)), ((2, 3, 64), (1, 6, 4)), ((6, 1, 64), (2, 3, 4))):
+        with pytest.raises(ValueError, match="same tokens"):
+            layer(torch.zeros(x), torch.zeros(z))
+    for x, z in (((2, 3, 64), (2, 3, 4)), ((2, 3, 64), (6, 4)), ((6, 64), (2, 3, 4)), ((64,), (4,)), ((64,), (1, 4)), ((6, 64), (6, 4))):
+        assert layer(torch.zeros(x), torch.zeros(z)).shape == x
+        t = 1 if len(x) == 1 else 6
+        assert seen[-1] == ((t, 64), (t, 4))
