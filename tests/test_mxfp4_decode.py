@@ -1,0 +1,62 @@
+"""Few float tokens of the MXFP4 product where a workgroup goes through several groups of channels, its waves
+through several units of each."""
+
+import pytest
+import torch
+
+import gemv_int4_quantize_amd as w4
+from test_mxfp4 import DEV, FLOATS
+
+# groups of 32 channels past two for every CU (N >= 16384): up to four tokens and up to eight, up to 4096
+# columns and more, each with at least three groups a workgroup and an odd rest; and groups of 16
+WALKS = [(1, 50021, 4090), (4, 50021, 4000), (1, 50021, 8010), (4, 50021, 8100), (3, 40001, 14900), (6, 50021, 1100), (8, 50021, 4000),
+         (5, 50021, 6000), (8, 16411, 2100), (4, 16000, 9000), (2, 16383, 4100), (7, 16001, 4500), (8, 16383, 1030), (1, 12291, 16300)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", WALKS)
+@pytest.mark.parametrize("dtype", FLOATS)
+def test_walk_over_groups(m, n, k, dtype):
+    """Whole numbers, so that every sum is exact: tokens whose blocks reach 4 keep the power, weights of random
+    codes at two powers.  Terms are multiples of 1/4 up to 48."""
+    assert w4.mxfp4_kernel_for(m, n, k) == "mx4_decode_fused"
+    assert 4 * 48 * k < 1 << 24
+    g = torch.Generator(device=DEV).manual_seed(m * 31 + n)
+    p = (k + 127) // 128 * 128
+    codes = torch.randint(0, 256, (n, p // 2), dtype=torch.uint8, device=DEV, generator=g)
+    codes[:, (k + 1) // 2:] = 0
+    if k % 2:
+        codes[:, k // 2] &= 15
+    w = w4.MXFP4Rows(codes, torch.randint(127, 129, (n, p // 32), dtype=torch.uint8, device=DEV, generator=g), n, k)
+    x = torch.randint(-4, 5, (m, k), device=DEV, generator=g) * 0.5
+    x[:, ::32] = 4.0
+    x = x.to(dtype)
+    bias = torch.randint(-9, 10, (n,), device=DEV, generator=g).float()
+    want = torch.empty(m, n, dtype=torch.float64, device=DEV)
+    for c in range(0, n, 8192):
+        part = w4.MXFP4Rows(w.codes[c:c + 8192], w.scales[c:c + 8192], min(8192, n - c), k)
+        want[:, c:c + 8192] = x.double() @ w4.dequantize_mxfp4(part, torch.float32).double().t()
+    want += bias.double()
+    assert torch.equal(w4.mm_mxfp4(x, w, bias=bias).double(), want)
+    outs = [torch.full((m + 1, c), 5.0, device=DEV) for c in (33, n - 33)]
+    w4.mm_mxfp4_split(x, w, [o[:m] for o in outs], bias=bias)
+    assert torch.equal(torch.cat([o[:m] for o in outs], 1).double(), want) and all((o[m] == 5).all() for o in outs)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k", [100, 300, 640, 1555, 3900])
+@pytest.mark.parametrize("m", [2, 3, 5, 8])
+def test_tokens_of_an_odd_number_of_pieces(m, k):
+    """Rows of an odd multiple of 128 columns, once padded: each token's exponents meet its own codes."""
+    n = 70
+    g = torch.Generator(device=DEV).manual_seed(k + m)
+    w = w4.quantize_mxfp4(torch.randint(-6, 7, (n, k), device=DEV, generator=g).float())
+    x = torch.randint(-2, 3, (m, k), device=DEV, generator=g).float()
+    x[:, ::32] = 4.0
+    blocks = (k + 31) // 32
+    power = torch.randint(-3, 4, (m, blocks), device=DEV, generator=g).float()
+    x = x * torch.exp2(power).repeat_interleave(32, 1)[:, :k]
+    q = w4.quantize_mxfp4(x)
+    assert torch.equal(w4.dequantize_mxfp4(q, torch.float32), x)
+    want = x.double() @ w4.dequantize_mxfp4(w, torch.float32).double().t()
+    assert torch.equal(w4.mm_mxfp4(x, w).double(), want) and torch.equal(w4.mm_mxfp4(q, w).double(), want)
