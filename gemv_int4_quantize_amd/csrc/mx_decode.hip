@@ -30,9 +30,10 @@ constexpr int kMaxM = 8;              // tokens
 constexpr int64_t max_columns(int64_t M) { return M <= 4 ? 45056 : 32768; }
 constexpr int kFewM = 32;  // tokens whose codes are ready
 
-// The tokens in LDS: exponents [M][P / 32], then codes [M][P / 2 + 16] (the pad keeps the tokens' rows in
-// distinct banks).
-constexpr int codes_at(int64_t M, int64_t P) { return (int)((M * (P >> 5) + 15) & ~(int64_t)15); }
+// The tokens in LDS: exponents [M][P / 32 rounded up to 8] (a unit's eight are read as one), then codes
+// [M][P / 2 + 16] (the pad keeps the tokens' rows in distinct banks).
+constexpr int exponents_pitch(int64_t P) { return (int)(((P >> 5) + 7) & ~(int64_t)7); }
+constexpr int codes_at(int64_t M, int64_t P) { return (int)((M * exponents_pitch(P) + 15) & ~(int64_t)15); }
 constexpr int64_t token_lds(int64_t M, int64_t P) { return codes_at(M, P) + M * ((P >> 1) + 16); }
 
 // A unit in LDS: 128 bytes a row, the 16-byte chunks (a block of 32 columns each) at chunk ^ (row / 2 % 8),
@@ -58,7 +59,7 @@ __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(const uint8_t* __res
   const int r16 = lane & 15, q4 = lane >> 4;
   char* own = smem + wave * (SLOTS * SLOT);
   char* tokens = smem + NW * SLOTS * SLOT;
-  const int at_codes = codes_at(M, P);
+  const int at_codes = codes_at(M, P), epitch = exponents_pitch(P);
 
   int off[2];  // where a lane's loads of 8 rows begin
 #pragma unroll
@@ -116,7 +117,7 @@ __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(const uint8_t* __res
       const uint32_t code = mx_chunk<XDT>(r, &e);
       if (in) {
         *reinterpret_cast<uint32_t*>(tokens + at_codes + m * (row + 16) + c * 4) = code;
-        if ((c & 3) == 0) tokens[m * erow + (c >> 2)] = (char)e;
+        if ((c & 3) == 0) tokens[m * epitch + (c >> 2)] = (char)e;
       }
     };
     if constexpr (MT == 4) {  // the same chunks of each token
@@ -164,7 +165,7 @@ __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(const uint8_t* __res
         *reinterpret_cast<u32x4*>(tokens + at_codes + m * (row + 16) + c * 16) =
             *reinterpret_cast<const u32x4*>(A + (size_t)m * row + c * 16);
       for (int c = tid; c < erow / 4; c += T)
-        *reinterpret_cast<uint32_t*>(tokens + m * erow + c * 4) = *reinterpret_cast<const uint32_t*>(ae + (size_t)m * erow + c * 4);
+        *reinterpret_cast<uint32_t*>(tokens + m * epitch + c * 4) = *reinterpret_cast<const uint32_t*>(ae + (size_t)m * erow + c * 4);
     }
     first_loads();
   }
@@ -182,7 +183,7 @@ __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(const uint8_t* __res
   for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int m0 = min(r16, M - 1);
   const char* xc = tokens + at_codes + m0 * (row + 16) + q4 * 16;
-  const char* xe = tokens + m0 * erow;
+  const char* xe = tokens + m0 * epitch;
   int slot = 0, turn = 0;
   while (now.group < groups) {
     load(ahead, slot == 0 ? SLOTS - 1 : slot - 1);
