@@ -193,7 +193,7 @@ hipError_t launch_mx_mm(const MxArgs& a, const DeviceCaps& caps, void* ws, size_
 bool mx_decode_supported(int64_t M, int64_t K);
 hipError_t launch_mx_decode(const MxArgs& a, const DeviceCaps& caps, hipStream_t st);
 // Few tokens of ready codes.
-bool mx_few_supported(int64_t M, int64_t K);
+bool mx_few_supported(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps);
 hipError_t launch_mx_few(const MxArgs& a, const DeviceCaps& caps, hipStream_t st);
 
 // Input gradient (mx_grad.hip): dY [M][parts][ld] bf16 parts (ld a multiple of 8, L <= ld columns of

@@ -434,7 +434,15 @@ bool mx_decode_supported(int64_t M, int64_t K) { return M <= kMaxM && M * mx_pit
 
 // One or two ready tokens are faster where they lie in LDS: (4096, 11008) 6.1 us for one, 6.8 here; from
 // three on here: four 7.5, 6.8.
-bool mx_few_supported(int64_t M, int64_t K) { return M <= kFewM && !(M <= 2 && mx_decode_supported(M, K)); }
+// The waves of a workgroup go through a whole row, so where groups of 16 channels leave half of the CUs idle
+// a long one is faster on tiles that split it: (512, 65536) 16 tokens 24.5 us here, 20.9 so, 32 tokens 35.6,
+// 23.0; (2048, 32768) 14.8, 16.5 and 20.4, 18.4; (2048, 16384) 8.7, 11.4 and 11.7, 12.5; (128, 4096) 3.9, 6.7
+// and 5.0, 7.2.  With more groups it is the other way about, or within a tenth: (3000, 65536) 29.0, 33.2 and 40.4,
+// 37.7; (8192, 65536) 61, 70 and 64, 72.
+bool mx_few_supported(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps) {
+  if (M > kFewM || (M <= 2 && mx_decode_supported(M, K))) return false;
+  return (N + 15) / 16 * 2 > caps.cus || mx_pitch(K) <= (M <= 16 ? 36864 : 18432);
+}
 
 // Groups of 32 channels where they make nearly whole rounds of the CUs, else of 16, two workgroups a CU
 // (twice the tokens' reads): 16 tokens at (8192, 8192) 10.6 us, 11.6 of 16; at (11008, 4096), 1.3 rounds, 9.0,

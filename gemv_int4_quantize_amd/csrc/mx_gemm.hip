@@ -322,7 +322,8 @@ hipError_t run_ring(const MxArgs& a, const MxPlan& p, float* part, hipStream_t s
 
 // Tiles of bm (0: none) and lower rows and bn columns, and what one stage of them takes, in us on MI355X
 // (fitted to 20 sizes from (M, N, K) = (32, 2048, 2048) to (4096, 11008, 4096), in a captured graph, where
-// the plan is within 1% of the best of all tiles and splits):
+// the plan is within 1% of the best of all tiles and splits; of 32 tokens and fewer only long rows of few
+// channels come here now):
 // high, of a bm-row tile; lat, the least time of a stage of a lower one; mfma, a workgroup's share of
 // the CU's matrix cores; and t0, a launch's start, first loads and stores.
 struct Tile {
@@ -376,12 +377,12 @@ size_t plan_bytes(int64_t M, int64_t N, const MxPlan& p) { return p.splits > 1 ?
 }  // namespace
 
 size_t mx_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps) {
-  return mx_decode_supported(M, K) || mx_few_supported(M, K) ? 0 : plan_bytes(M, N, pick(M, N, K, caps, true));
+  return mx_few_supported(M, N, K, caps) || mx_decode_supported(M, K) ? 0 : plan_bytes(M, N, pick(M, N, K, caps, true));
 }
 
 const char* mx_mm_name(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps) {
   static thread_local char buf[48];
-  if (mx_few_supported(M, K)) return "mx4_few";
+  if (mx_few_supported(M, N, K, caps)) return "mx4_few";
   if (mx_decode_supported(M, K)) return "mx4_decode";
   const MxPlan p = pick(M, N, K, caps, true);
   const Tile& c = kTiles[p.tile];
@@ -392,7 +393,7 @@ const char* mx_mm_name(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps) 
 }
 
 hipError_t launch_mx_mm(const MxArgs& a, const DeviceCaps& caps, void* ws, size_t ws_bytes, hipStream_t st) {
-  if (mx_few_supported(a.M, a.K)) return launch_mx_few(a, caps, st);
+  if (mx_few_supported(a.M, a.N, a.K, caps)) return launch_mx_few(a, caps, st);
   if (mx_decode_supported(a.M, a.K)) return launch_mx_decode(a, caps, st);
   MxPlan p = pick(a.M, a.N, a.K, caps, true);
   if (plan_bytes(a.M, a.N, p) > ws_bytes) p = pick(a.M, a.N, a.K, caps, false);

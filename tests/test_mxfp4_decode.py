@@ -60,3 +60,49 @@ def test_tokens_of_an_odd_number_of_pieces(m, k):
     assert torch.equal(w4.dequantize_mxfp4(q, torch.float32), x)
     want = x.double() @ w4.dequantize_mxfp4(w, torch.float32).double().t()
     assert torch.equal(w4.mm_mxfp4(x, w).double(), want) and torch.equal(w4.mm_mxfp4(q, w).double(), want)
+
+
+def test_long_rows_of_few_channels_are_split():
+    """The few-token kernel does not split a row: where it would leave half of the CUs idle over a long one,
+    tiles that split it run, and the workspace they ask for is reported."""
+    import ctypes
+
+    L = w4.lib()
+
+    def kernel(m, n, k):
+        return L.mx4_kernel(m, n, k, -1).decode()
+
+    for m, n, k in ((16, 512, 65536), (32, 512, 65536), (32, 2048, 32768), (17, 100, 20480), (4, 2048, 40960), (2, 512, 65536)):
+        assert "splitk" in kernel(m, n, k), (m, n, k)
+        for xdt in (-1, 2):
+            size = ctypes.c_size_t(0)
+            assert L.mx4_workspace_bytes(m, n, k, xdt, ctypes.byref(size)) == 0
+            assert size.value >= 2 * m * n * 4 + (0 if xdt < 0 else m * k * 17 // 32)
+    for m, n, k in ((16, 512, 32768), (32, 512, 16384), (32, 2049, 65536), (16, 4096, 262144), (3, 128, 4096), (32, 128, 4096)):
+        assert kernel(m, n, k) == "mx4_few", (m, n, k)
+    assert kernel(1, 512, 40960) == "mx4_decode"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(16, 512, 65500), (32, 500, 20500), (3, 40, 40961), (2, 100, 30001), (31, 2048, 18433), (17, 33, 18432),
+                                   (1, 70, 60001), (8, 512, 36864), (9, 17, 36865)])
+def test_long_rows(m, n, k):
+    """Whole numbers of both kinds of tokens on both sides of the rule: |sum| <= 36 k, in quarters."""
+    assert 4 * 36 * k < 1 << 24
+    g = torch.Generator(device=DEV).manual_seed(m + n)
+
+    def rows(r):
+        c = torch.randint(0, 256, (r, (k + 127) // 128 * 64), dtype=torch.uint8, device=DEV, generator=g)
+        c[:, (k + 1) // 2:] = 0
+        if k % 2:
+            c[:, k // 2] &= 15
+        return w4.MXFP4Rows(c, torch.full((r, (k + 127) // 128 * 4), 127, dtype=torch.uint8, device=DEV), r, k)
+
+    w = rows(n)
+    x = w4.dequantize_mxfp4(rows(m), torch.float32)
+    x[:, ::32] = 6.0  # blocks whose largest magnitude is 6 keep the power
+    a = w4.quantize_mxfp4(x)
+    assert torch.equal(w4.dequantize_mxfp4(a, torch.float32), x)
+    want = x.double() @ w4.dequantize_mxfp4(w, torch.float32).double().t()
+    for t in (a, x, x.bfloat16(), x.half()):
+        assert torch.equal(w4.mm_mxfp4(t, w).double(), want)
