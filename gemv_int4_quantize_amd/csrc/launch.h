@@ -189,10 +189,11 @@ struct MxArgs {
 size_t mx_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps);
 const char* mx_mm_name(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps);
 hipError_t launch_mx_mm(const MxArgs& a, const DeviceCaps& caps, void* ws, size_t ws_bytes, hipStream_t st);
-// Few tokens (mx_decode.hip); float ones are quantized inside that launch.  Ready codes: at most four.
+// Few tokens (mx_decode.hip): float ones, quantized inside that launch, or one or two of ready codes.
 bool mx_decode_supported(int64_t M, int64_t K);
+bool mx_decode_ready_supported(int64_t M, int64_t K);
 hipError_t launch_mx_decode(const MxArgs& a, const DeviceCaps& caps, hipStream_t st);
-// Few tokens of ready codes.
+// More of ready codes.
 bool mx_few_supported(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps);
 hipError_t launch_mx_few(const MxArgs& a, const DeviceCaps& caps, hipStream_t st);
 

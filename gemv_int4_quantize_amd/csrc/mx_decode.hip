@@ -28,7 +28,8 @@ constexpr int kMaxM = 8;              // tokens
 // here, 9.8 so, 10 tokens 11.6, 10.2; (4096, 11008): 4 tokens 8.3, 8.7, 6 tokens 13.1, 8.9; (8192, 2048):
 // 8 tokens 5.5, 6.3, 10 tokens 6.9, 6.5; (16384, 16384): 2 tokens 33, 3 tokens 37.5, 32.9.
 constexpr int64_t max_columns(int64_t M) { return M <= 4 ? 45056 : 32768; }
-constexpr int kFewM = 32;  // tokens whose codes are ready
+constexpr int kFewM = 32;   // tokens whose codes are ready
+constexpr int kReadyM = 2;  // of them, in the decode kernel
 
 // The tokens in LDS: exponents [M][P / 32 rounded up to 8] (a unit's eight are read as one), then codes
 // [M][P / 2 + 16] (the pad keeps the tokens' rows in distinct banks).
@@ -431,6 +432,7 @@ hipError_t run_few(const MxArgs& a, const DeviceCaps& caps, hipStream_t st) {
 }  // namespace
 
 bool mx_decode_supported(int64_t M, int64_t K) { return M <= kMaxM && M * mx_pitch(K) <= max_columns(M); }
+bool mx_decode_ready_supported(int64_t M, int64_t K) { return M <= kReadyM && mx_decode_supported(M, K); }
 
 // One or two ready tokens are faster where they lie in LDS: (4096, 11008) 6.1 us for one, 6.8 here; from
 // three on here: four 7.5, 6.8.
@@ -440,7 +442,7 @@ bool mx_decode_supported(int64_t M, int64_t K) { return M <= kMaxM && M * mx_pit
 // and 5.0, 7.2.  With more groups it is the other way about, or within a tenth: (3000, 65536) 29.0, 33.2 and 40.4,
 // 37.7; (8192, 65536) 61, 70 and 64, 72.
 bool mx_few_supported(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps) {
-  if (M > kFewM || (M <= 2 && mx_decode_supported(M, K))) return false;
+  if (M > kFewM || mx_decode_ready_supported(M, K)) return false;
   return (N + 15) / 16 * 2 > caps.cus || mx_pitch(K) <= (M <= 16 ? 36864 : 18432);
 }
 
@@ -454,7 +456,7 @@ hipError_t launch_mx_few(const MxArgs& a, const DeviceCaps& caps, hipStream_t st
 }
 
 hipError_t launch_mx_decode(const MxArgs& a, const DeviceCaps& caps, hipStream_t st) {
-  if (a.X == nullptr) return run_m<4, -1>(a, caps, st);
+  if (a.X == nullptr) return run_m<kReadyM, -1>(a, caps, st);
   switch (a.x_dt) {
     case W4_DT_F32: return run_x<W4_DT_F32>(a, caps, st);
     case W4_DT_F16: return run_x<W4_DT_F16>(a, caps, st);

@@ -377,13 +377,13 @@ size_t plan_bytes(int64_t M, int64_t N, const MxPlan& p) { return p.splits > 1 ?
 }  // namespace
 
 size_t mx_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps) {
-  return mx_few_supported(M, N, K, caps) || mx_decode_supported(M, K) ? 0 : plan_bytes(M, N, pick(M, N, K, caps, true));
+  return mx_few_supported(M, N, K, caps) || mx_decode_ready_supported(M, K) ? 0 : plan_bytes(M, N, pick(M, N, K, caps, true));
 }
 
 const char* mx_mm_name(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps) {
   static thread_local char buf[48];
   if (mx_few_supported(M, N, K, caps)) return "mx4_few";
-  if (mx_decode_supported(M, K)) return "mx4_decode";
+  if (mx_decode_ready_supported(M, K)) return "mx4_decode";
   const MxPlan p = pick(M, N, K, caps, true);
   const Tile& c = kTiles[p.tile];
   int at = snprintf(buf, sizeof(buf), "%s", c.name);
@@ -394,7 +394,7 @@ const char* mx_mm_name(int64_t M, int64_t N, int64_t K, const DeviceCaps& caps) 
 
 hipError_t launch_mx_mm(const MxArgs& a, const DeviceCaps& caps, void* ws, size_t ws_bytes, hipStream_t st) {
   if (mx_few_supported(a.M, a.N, a.K, caps)) return launch_mx_few(a, caps, st);
-  if (mx_decode_supported(a.M, a.K)) return launch_mx_decode(a, caps, st);
+  if (mx_decode_ready_supported(a.M, a.K)) return launch_mx_decode(a, caps, st);
   MxPlan p = pick(a.M, a.N, a.K, caps, true);
   if (plan_bytes(a.M, a.N, p) > ws_bytes) p = pick(a.M, a.N, a.K, caps, false);
   float* part = static_cast<float*>(ws);
