@@ -14,6 +14,8 @@
  *           2j + 1 in the high ones.  A code is e2m1: sign, two exponent bits, one mantissa
  *           bit, for 0, .5, 1, 1.5, 2, 3, 4, 6.  The codes of columns C .. P-1 must be 0.
  *   scales  uint8 [R][P / 32], 4-byte aligned: every 32 columns share 2^(scale - 127); 255: NaN.
+ *           Blocks of nothing but columns C .. P-1 may have any scale but 255, which would make the
+ *           products of their row NaN (the quantizer writes 0).
  * Tokens and weight channels both use it: X [M][K] is quantized along K, W [N][K] as well.
  * Rows, M and N are below 2^30, columns and K below 2^22.  Outputs overlap no input.
  */

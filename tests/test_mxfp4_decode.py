@@ -106,3 +106,31 @@ def test_long_rows(m, n, k):
     want = x.double() @ w4.dequantize_mxfp4(w, torch.float32).double().t()
     for t in (a, x, x.bfloat16(), x.half()):
         assert torch.equal(w4.mm_mxfp4(t, w).double(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k", [1, 33, 130, 300, 1100])
+def test_scales_past_the_last_column(k):
+    """Blocks of nothing but padding may hold any scale but NaN's; the quantizer's are 0."""
+    g = torch.Generator(device=DEV).manual_seed(k)
+    n, blocks = 40, (k + 31) // 32
+    w = w4.quantize_mxfp4(torch.randn(n, k, device=DEV, generator=g))
+    x = torch.randn(70, k, device=DEV, generator=g).bfloat16()
+    a = w4.quantize_mxfp4(x)
+    assert not w.scales[:, blocks:].any() and not a.scales[:, blocks:].any()
+    dirty = [w4.MXFP4Rows(r.codes, r.scales.clone(), r.rows, k) for r in (w, a)]
+    for r in dirty:
+        r.scales[:, blocks:] = torch.randint(1, 255, r.scales[:, blocks:].shape, dtype=torch.uint8, device=DEV, generator=g)
+        assert torch.equal(w4.dequantize_mxfp4(r), w4.dequantize_mxfp4(w if r.rows == n else a))
+    for m in (1, 3, 8, 20, 70):
+        want = w4.mm_mxfp4(x[:m], w)
+        some = w4.MXFP4Rows(dirty[1].codes[:m], dirty[1].scales[:m], m, k)
+        assert torch.equal(w4.mm_mxfp4(x[:m], dirty[0]), want) and torch.equal(w4.mm_mxfp4(some, dirty[0]), w4.mm_mxfp4(some, w))
+    dy = torch.randn(9, n, device=DEV, generator=g)
+    assert torch.equal(w4.mm_mxfp4_t(dy, dirty[0]), w4.mm_mxfp4_t(dy, w))
+    w1 = w4.quantize_mxfp4(torch.randn(2 * 2 * 24, k, device=DEV, generator=g))  # two experts, k -> 24 -> k
+    w2 = w4.quantize_mxfp4(torch.randn(2 * k, 24, device=DEV, generator=g))
+    z = torch.randn(6, 2, device=DEV, generator=g)
+    want = w4.moe_mxfp4(x[:6], z, w1, w2, 1)
+    w1.scales[:, blocks:], w2.scales[:, 1:] = 254, 254
+    assert torch.equal(w4.moe_mxfp4(x[:6], z, w1, w2, 1), want)
