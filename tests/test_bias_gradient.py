@@ -1,4 +1,4 @@
-"""The bias's gradient of the int4 and int8 layers: captured with its step, and its own derivative."""
+"""The bias's gradient of the linear layers: captured with its step, and its own derivative."""
 
 import pytest
 import torch
@@ -6,7 +6,8 @@ import torch
 import gemv_int4_quantize_amd as w4
 
 DEV = "cuda:0"
-LAYERS = {"int4": (w4.w4a16_linear, lambda w: w4.quantize_pack(w, "rowwise")), "int8": (w4.w8a8_linear, lambda w: w4.quantize_int8(w))}
+LAYERS = {"int4": (w4.w4a16_linear, lambda w: w4.quantize_pack(w, "rowwise")), "int8": (w4.w8a8_linear, lambda w: w4.quantize_int8(w)),
+          "mxfp4": (w4.mxfp4_linear, lambda w: w4.quantize_mxfp4(w))}
 
 
 def _randn(seed, *shape):
@@ -16,7 +17,7 @@ def _randn(seed, *shape):
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", LAYERS)
 @pytest.mark.parametrize("bdt", [torch.float32, torch.float16, torch.bfloat16, torch.float64])
-@pytest.mark.parametrize("m,n,out_dtype", [(5, 64, None), (2048, 1024, None), (4096, 96, torch.bfloat16), (8192, 256, None)])
+@pytest.mark.parametrize("m,n,out_dtype", [(5, 64, None), (15, 2048, None), (16, 48, None), (2048, 1024, None), (4096, 96, torch.bfloat16), (8192, 256, None)])
 def test_captured_step(kind, m, n, out_dtype, bdt):
     """Forward and backward in one graph, the bias's gradient with it, over several replays."""
     linear, make = LAYERS[kind]
@@ -87,13 +88,14 @@ def test_types_and_strides(kind):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("kind", LAYERS)
+@pytest.mark.parametrize("kind", ["int4", "int8"])  # (mxfp4's is differentiable once)
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-def test_derivative_of_the_sum(kind, dtype):
+@pytest.mark.parametrize("m", [7, 40])
+def test_derivative_of_the_sum(kind, dtype, m):
     """The bias's gradient is linear in the output's: differentiated, it hands its gradient to every row."""
     linear, make = LAYERS[kind]
     w = make(_randn(6, 24, 256))
-    x, h = _randn(7, 7, 256), _randn(8, 24).to(dtype)
+    x, h = _randn(7, m, 256), _randn(8, 24).to(dtype)
 
     def step():
         bias = torch.zeros(24, dtype=dtype, device=DEV, requires_grad=True)
@@ -101,7 +103,7 @@ def test_derivative_of_the_sum(kind, dtype):
         (db,) = torch.autograd.grad(linear(x, w, bias, dtype), bias, gy, create_graph=True)
         return db, *torch.autograd.grad(db, gy, h)
 
-    ones = torch.ones(7, 24, dtype=dtype, device=DEV)
+    ones = torch.ones(m, 24, dtype=dtype, device=DEV)
     eager = step()
     eager = [t.detach().clone() for t in eager]
     graph = torch.cuda.CUDAGraph()
@@ -110,4 +112,19 @@ def test_derivative_of_the_sum(kind, dtype):
     graph.replay()
     torch.cuda.synchronize()
     for db, back in (eager, captured):
-        assert (db == 7).all() and back.dtype == dtype and torch.equal(back, h.expand(7, 24))
+        assert (db == m).all() and back.dtype == dtype and torch.equal(back, h.expand(m, 24))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", LAYERS)
+@pytest.mark.parametrize("n", [24, 2048])
+def test_few_rows_agree(kind, n):
+    """Sums of few rows have the bits of torch's in every layer, also where terms cancel."""
+    linear, make = LAYERS[kind]
+    w = make(_randn(9, n, 256))
+    for m in (1, 2, 14, 15):
+        gy = _randn(m, m, n)
+        gy[-1] = -gy[:-1].double().sum(0).float()
+        bias = torch.zeros(n, device=DEV, requires_grad=True)
+        linear(_randn(1, m, 256), w, bias).backward(gy)
+        assert torch.equal(bias.grad, gy.sum(0))
