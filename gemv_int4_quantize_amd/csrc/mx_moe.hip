@@ -713,8 +713,11 @@ __global__ __launch_bounds__(256) void moe_join_kernel(const float* __restrict__
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Tokens of an expert that its weights are widened for at a time: four where experts have few (an
-// expert with more reads its weights again), else sixteen.
+// Tokens of an expert that its weights are widened for at a time: four where experts have few, else sixteen.
+// The choice itself is not known here.  An expert with more than four tokens reads its weights again for
+// the next four, but T top <= 3 E bounds that by 3 E / 4 such reads in all, so a batch whose tokens all agree
+// costs less than one that reaches every expert: 32 tokens, 8 of 128 experts of 2048 x 768, 55 us and 77; 64,
+// 6 of 128, 89 and 106.
 bool few_each(const MoeArgs& a) { return a.T <= 4 || a.T * a.top <= 3 * a.E; }
 
 int down_lds(const MoeArgs& a, int cols, int slots, int waves) {
@@ -791,13 +794,17 @@ hipError_t down(const MoeArgs& a, char* ws, const Space& sp, int S, hipStream_t 
 
 // Rings of three units where two workgroups of them share a CU, else of two (the sums of many tokens
 // take the place; of eight waves with a CU to themselves, three are slower: 18.4 us instead of 17.6 for
-// one token and 8 of 128 experts).
+// one token and 8 of 128 experts).  From 37 tokens on the columns that four-column products keep in LDS
+// would leave place for one: sixteen columns, from registers, are faster there even where experts have few
+// tokens (48 tokens, 8 of 128 experts of 2048 x 768, 105 us in all instead of 119; 37, 84 either way).
 template <int DT, int COLS>
 hipError_t both(const MoeArgs& a, const DeviceCaps& caps, char* ws, const Space& sp, int S, hipStream_t st) {
   const hipError_t e = up<DT, COLS>(a, caps, ws, sp, st);
   if (e != hipSuccess) return e;
-  if constexpr (COLS == 4)
+  if constexpr (COLS == 4) {
     if (down_alone(a, caps)) return down<DT, COLS, 2, 8>(a, ws, sp, S, st);
+    if (down_lds(a, COLS, 2, NW) > 80 * 1024) return down<DT, 16, 2, NW>(a, ws, sp, S, st);
+  }
   return down_lds(a, COLS, 3, NW) <= 80 * 1024 ? down<DT, COLS, 3, NW>(a, ws, sp, S, st) : down<DT, COLS, 2, NW>(a, ws, sp, S, st);
 }
 
