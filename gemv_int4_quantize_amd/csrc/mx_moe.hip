@@ -11,8 +11,8 @@
 // bits) and multiplied on the matrix cores with up to sixteen tokens as the columns.  The activations
 // enter as bf16 parts whose sum they are (one of bf16, two of fp16, three of fp32), and so does g_j a_j
 // (three of an fp32): the matrix cores have time for it, and nothing is rounded between the products.  (Two
-// parts, 16 bits, lose differences of nearly equal activations; in a captured graph 19.6 us instead of 20.6
-// for one token and 8 of 128 experts of 2048 x 768, 76.8 instead of 80.5 for 4 tokens and 2 of 8 of 4096 x 11008.)
+// parts, 16 bits, lose differences of nearly equal activations; in a captured graph 173 us instead of 196 for
+// 32 tokens, 2 of 8 experts of 4096 x 11008, sixteen columns a product; of four, 77.0 and 78.6 for 4 tokens.)
 // Launches, bf16: 4 tokens, 2 of 8 experts of 4096 x 11008, 42-49 us (262 MB, 5.3-6.2 TB/s), 29-34 (131 MB),
 // 4.7 for the parts; 32 tokens, 8 of 128 experts of 2048 x 768, 45 (187 MB), 23 and 4.9.  Reads of the
 // same pattern alone reach 5.7-6.4 TB/s; the rest is the choice ahead of the first weight (some 5 us for
@@ -274,7 +274,8 @@ __device__ __forceinline__ void dma_exponents(char* at, const uint8_t* we, uint3
 // COLS = 16: as they are multiplied.  COLS = 4 (eight loads would fetch mostly nothing, and the caches'
 // return path is what the weights need as well: 108 us with them, 96 without, 4 tokens on 2 of 8 experts
 // of 4096 x 11008): rows of four tokens by two loads a part, through LDS (put, [NP][4][512 bytes], the
-// 16-byte chunks of token t at chunk ^ t, so that reads hit distinct banks).
+// 16-byte chunks of part k of token t at chunk ^ (t + 4 k), so that reads hit distinct banks), and the parts
+// are columns of their own, 4 k + t of sixteen: one product takes all of them, and join adds their sums.
 template <int NP, int COLS>
 struct Columns {
   u32x4 x[NP][COLS == 4 ? 2 : 8];
@@ -308,16 +309,31 @@ struct Columns {
 #pragma unroll
       for (int k = 0; k < NP; ++k)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) *reinterpret_cast<u32x4*>(xs + k * 2048 + j * 1024 + lane * 16) = x[k][j];
+        for (int j = 0; j < 2; ++j) *reinterpret_cast<u32x4*>(xs + k * 2048 + j * 1024 + (lane ^ 4 * k) * 16) = x[k][j];
     }
   }
+  // the operands of a product: parts [kOperands] of a column, or the part that a column is
+  static constexpr int kOperands = COLS == 4 ? 1 : NP;
   __device__ __forceinline__ u32x4 operand(const char* xs, int k, int h, int i, int lane) const {
     if constexpr (COLS == 4) {
-      const int t = lane & 3;  // columns past the fourth: not used
-      return *reinterpret_cast<const u32x4*>(xs + k * 2048 + t * 512 + ((((4 * h + (lane >> 4)) * 4 + i) ^ t) << 4));
+      const int t = lane & 3, p = min((lane & 15) >> 2, NP - 1);  // columns past the parts: not used
+      return *reinterpret_cast<const u32x4*>(xs + p * 2048 + t * 512 + ((((4 * h + (lane >> 4)) * 4 + i) ^ (t + 4 * p)) << 4));
     } else {
       return x[k][h * 4 + i];
     }
+  }
+  // a column's sum in the lane of that column
+  __device__ __forceinline__ static f32x4 join(const f32x4& v) {
+    f32x4 s = v;
+    if constexpr (COLS == 4 && NP > 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[i] += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[i]), 0x104, 0xF, 0xF, false));  // lane + 4
+        if constexpr (NP > 2)
+          s[i] += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[i]), 0x108, 0xF, 0xF, false));  // lane + 8
+      }
+    }
+    return s;
   }
 };
 
@@ -350,7 +366,7 @@ __device__ __forceinline__ void multiply(const char* base, const Columns<NP, COL
 #pragma unroll
       for (int r = 0; r < RT; ++r) a[r] = mx_bf16x8(w[h][r][i], p[r]);
 #pragma unroll
-      for (int k = 0; k < NP; ++k) {
+      for (int k = 0; k < Columns<NP, COLS>::kOperands; ++k) {
         const u32x4 x = c.operand(xs, k, h, i, lane);
 #pragma unroll
         for (int r = 0; r < RT; ++r) acc[r] = mfma16(a[r], x, acc[r]);
@@ -471,6 +487,8 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(const uint16_t* __restr
   int turn = 0;
   auto finish = [&](const Place& p) {
     float(*sum)[RT * 16][COLS + 1] = sums[turn & 1];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = Columns<NP, COLS>::join(acc[r]);
     if ((lane & 15) < COLS) {
 #pragma unroll
       for (int r = 0; r < RT; ++r)
@@ -667,6 +685,8 @@ __global__ __launch_bounds__(WAVES * 64) void moe_down_kernel(const uint16_t* __
       slot = slot == SLOTS - 1 ? 0 : slot + 1;
       if (now.u + 1 >= now.to) {
         const int col = now.b0 + (lane & 15);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[r] = Columns<HP, COLS>::join(acc[r]);
         if ((lane & 15) < COLS && col < now.cols) {
           float* to = mine + s.token[now.first + col] * kRowPitch + (lane >> 4) * 4;
 #pragma unroll
