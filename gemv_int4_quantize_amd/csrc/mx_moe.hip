@@ -13,10 +13,10 @@
 // (three of an fp32): the matrix cores have time for it, and nothing is rounded between the products.  (Two
 // parts, 16 bits, lose differences of nearly equal activations; in a captured graph 173 us instead of 196 for
 // 32 tokens, 2 of 8 experts of 4096 x 11008, sixteen columns a product; of four, 77.0 and 78.6 for 4 tokens.)
-// Launches, bf16: 4 tokens, 2 of 8 experts of 4096 x 11008, 42-49 us (262 MB, 5.3-6.2 TB/s), 29-34 (131 MB),
-// 4.7 for the parts; 32 tokens, 8 of 128 experts of 2048 x 768, 45 (187 MB), 23 and 4.9.  Reads of the
+// Launches, bf16: 4 tokens, 2 of 8 experts of 4096 x 11008, 43-50 us (262 MB, 5.3-6.2 TB/s), 31-35 (131 MB),
+// 4.8 for the parts; 32 tokens, 8 of 128 experts of 2048 x 768, 46 (187 MB), 25 and 4.6.  Reads of the
 // same pattern alone reach 5.7-6.4 TB/s; the rest is the choice ahead of the first weight (some 5 us for
-// 32 tokens) and the ends of the launches.  One token, 8 of 128 experts: 10.6 and 7.0, all latency.
+// 32 tokens) and the ends of the launches.  One token, 8 of 128 experts: 10.7 and 7.5, all latency.
 #include <algorithm>
 
 #include "api_common.h"
@@ -274,7 +274,7 @@ __device__ __forceinline__ void dma_exponents(char* at, const uint8_t* we, uint3
 // COLS = 16: as they are multiplied.  COLS = 4 (eight loads would fetch mostly nothing, and the caches'
 // return path is what the weights need as well: 108 us with them, 96 without, 4 tokens on 2 of 8 experts
 // of 4096 x 11008): rows of four tokens by two loads a part, through LDS (put, [NP][4][512 bytes], the
-// 16-byte chunks of part k of token t at chunk ^ (t + 4 k), so that reads hit distinct banks), and the parts
+// 16-byte chunks of part k of token t at chunk ^ (t + 4 k), so that most reads hit distinct banks), and the parts
 // are columns of their own, 4 k + t of sixteen: one product takes all of them, and join adds their sums.
 template <int NP, int COLS>
 struct Columns {
@@ -749,9 +749,9 @@ int down_lds(const MoeArgs& a, int cols, int slots, int waves) {
 int64_t down_units(const MoeArgs& a) { return std::min<int64_t>(a.E, a.T * a.top) * ((mx_pitch(a.F) + 255) / 256); }
 
 // Whether one workgroup of eight waves does all of the units of its rows, so that no launch has to join
-// parts: where a wave gets few of them.  One token, 2 of 8 experts of 4096 x 2816, 22 units: 22.0 us with
-// the join, 19.2 without; 6 of 64 of 2048 x 1408, 36 units: 24.6, 22.9; 4 tokens, 8 of 128 of 2048 x 768,
-// 96 units: 30.3, 33.6.
+// parts: where a wave gets few of them.  One token in a captured graph, with the join and without: 22 units
+// 22.1 us and 19.3, 36 units 22.9 and 22.0, 48 units 24.5 and 25.0, 64 units 24.7 and 28.4; 4 tokens, 96 units
+// 30.2 and 33.5.
 bool down_alone(const MoeArgs& a, const DeviceCaps& caps) {
   return few_each(a) && (a.H + RT * 16 - 1) / (RT * 16) <= caps.cus && down_units(a) <= 8 * 6 &&
          down_lds(a, 4, 2, 8) <= 160 * 1024;
@@ -813,7 +813,7 @@ hipError_t down(const MoeArgs& a, char* ws, const Space& sp, int S, hipStream_t 
 }
 
 // Rings of three units where two workgroups of them share a CU, else of two (the sums of many tokens
-// take the place; of eight waves with a CU to themselves, three are slower: 18.4 us instead of 17.6 for
+// take the place; of eight waves with a CU to themselves, three are slower: 20.2 us instead of 19.9 for
 // one token and 8 of 128 experts).  From 37 tokens on the columns that four-column products keep in LDS
 // would leave place for one: sixteen columns, from registers, are faster there even where experts have few
 // tokens (48 tokens, 8 of 128 experts of 2048 x 768, 105 us in all instead of 119; 37, 84 either way).
