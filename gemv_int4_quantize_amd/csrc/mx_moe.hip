@@ -812,27 +812,34 @@ hipError_t down(const MoeArgs& a, char* ws, const Space& sp, int S, hipStream_t 
   return hipGetLastError();
 }
 
+// Whether the second launch takes four tokens at a time: to four tokens an expert on average (three parts of
+// sixteen columns are more to fetch than those of the first launch: 13 tokens, 2 of 8 experts of 4096 x 11008,
+// 134 us in all instead of 160 with sixteen; 16 tokens 164 and 166, 24 tokens 191 and 180), and as long as
+// the columns that it keeps in LDS leave place for two workgroups a CU, up to 36 tokens (48 tokens, 8 of 128
+// experts of 2048 x 768, 119 us, 105 with sixteen columns, from registers).
+bool few_down(const MoeArgs& a) { return (few_each(a) || a.T * a.top <= 4 * a.E) && down_lds(a, 4, 2, NW) <= 80 * 1024; }
+
 // Rings of three units where two workgroups of them share a CU, else of two (the sums of many tokens
 // take the place; of eight waves with a CU to themselves, three are slower: 20.2 us instead of 19.9 for
-// one token and 8 of 128 experts).  From 37 tokens on the columns that four-column products keep in LDS
-// would leave place for one: sixteen columns, from registers, are faster there even where experts have few
-// tokens (48 tokens, 8 of 128 experts of 2048 x 768, 105 us in all instead of 119; 37, 84 either way).
+// one token and 8 of 128 experts).
 template <int DT, int COLS>
-hipError_t both(const MoeArgs& a, const DeviceCaps& caps, char* ws, const Space& sp, int S, hipStream_t st) {
-  const hipError_t e = up<DT, COLS>(a, caps, ws, sp, st);
-  if (e != hipSuccess) return e;
-  if constexpr (COLS == 4) {
-    if (down_alone(a, caps)) return down<DT, COLS, 2, 8>(a, ws, sp, S, st);
-    if (down_lds(a, COLS, 2, NW) > 80 * 1024) return down<DT, 16, 2, NW>(a, ws, sp, S, st);
-  }
+hipError_t down_ring(const MoeArgs& a, char* ws, const Space& sp, int S, hipStream_t st) {
   return down_lds(a, COLS, 3, NW) <= 80 * 1024 ? down<DT, COLS, 3, NW>(a, ws, sp, S, st) : down<DT, COLS, 2, NW>(a, ws, sp, S, st);
+}
+
+template <int DT>
+hipError_t both(const MoeArgs& a, const DeviceCaps& caps, char* ws, const Space& sp, int S, hipStream_t st) {
+  const hipError_t e = few_each(a) ? up<DT, 4>(a, caps, ws, sp, st) : up<DT, 16>(a, caps, ws, sp, st);
+  if (e != hipSuccess) return e;
+  if (down_alone(a, caps)) return down<DT, 4, 2, 8>(a, ws, sp, S, st);
+  return few_down(a) ? down_ring<DT, 4>(a, ws, sp, S, st) : down_ring<DT, 16>(a, ws, sp, S, st);
 }
 
 template <int DT>
 hipError_t run(const MoeArgs& a, const DeviceCaps& caps, char* ws, hipStream_t st) {
   const Space sp = space_of(a, caps);
   const int S = down_slices(a, caps);
-  const hipError_t e = few_each(a) ? both<DT, 4>(a, caps, ws, sp, S, st) : both<DT, 16>(a, caps, ws, sp, S, st);
+  const hipError_t e = both<DT>(a, caps, ws, sp, S, st);
   if (e != hipSuccess || S == 1) return e;
   moe_join_kernel<DT><<<dim3((unsigned)((a.H + 255) / 256), (unsigned)a.T), 256, 0, st>>>(
       reinterpret_cast<const float*>(ws + sp.part), reinterpret_cast<const Reached*>(ws), (int)a.T, (int)a.H, S, a.out, a.ldo);

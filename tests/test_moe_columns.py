@@ -61,9 +61,9 @@ def _check(got, *args):
 
 # T, E, top, H, F with T > 4 and T top > 3 E: waves with several units and a last one that is half a unit; more
 # items than workgroups; waves of the second launch with several units of several experts, at both ring
-# depths; a batch whose tokens all agree, and experts without any
+# depths; to four tokens an expert; a batch whose tokens all agree, and experts without any
 WIDE = [(20, 4, 2, 2500, 700), (33, 8, 4, 1300, 1100), (20, 8, 3, 4100, 1100), (64, 8, 3, 4100, 1100), (64, 4, 1, 1150, 2300),
-        (7, 2, 1, 900, 1410), (37, 5, 5, 260, 520)]
+        (7, 2, 1, 900, 1410), (37, 5, 5, 260, 520), (13, 8, 2, 2100, 1300), (30, 16, 2, 700, 520)]
 
 
 @pytest.mark.gpu
